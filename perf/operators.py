@@ -370,18 +370,18 @@ def _philox_words(group, tensor, step, seed):
     return x0, x1, x2, x3
 
 
-def _bytes8(lo, hi):
-    """The eight bytes of two words, in order."""
-    sh = torch.tensor([0, 8, 16, 24], device=lo.device)
-    return torch.cat([(lo[:, None] >> sh) & 255, (hi[:, None] >> sh) & 255], 1).reshape(-1).int()
+def _halves8(words):
+    """The eight 16-bit halves of four words, low half first."""
+    w = torch.stack(words, 1)
+    return torch.stack([w & 0xFFFF, w >> 16], 2).reshape(-1).int()
 
 
-def _stochastic8(x, byte, keep_nonzero):
-    """x rounded to E4M3 times its block's scale: up where fraction + byte/256 reaches one."""
+def _stochastic8(x, rnd, keep_nonzero):
+    """x rounded to E4M3 times its block's scale: up where fraction + rnd/65536 reaches one."""
     e = _scale8(x).repeat_interleave(32)
     y = x.abs() * _pow2(-e)
-    fine = ((y.view(torch.int32) + (byte << 12)) & ~0xFFFFF).view(torch.float32)
-    low = torch.floor(y * 512.0 + byte.float() / 256.0) / 512.0
+    fine = ((y.view(torch.int32) + (rnd << 4)) & ~0xFFFFF).view(torch.float32)
+    low = torch.floor(y * 512.0 + rnd.float() / 65536.0) / 512.0
     q = torch.where(y < 2.0 ** -6, low, fine)
     if keep_nonzero:
         q = torch.where(x > 0, q.clamp_min(2.0 ** -9), q)
@@ -404,9 +404,9 @@ def _plain_adamw(st):
     p = st["p"] * (1.0 - LR * st["decay_at"]) - (LR / (1.0 - B1 ** STEP)) * (m / denom)
     out = {"p": p, "w": p.bfloat16(), "m": m, "v": v, "norm": norm}
     if eight:
-        w = _philox_words(st["group8"], st["tensor8"], STEP, st["seed"])
-        out["m"] = _stochastic8(m, _bytes8(w[0], w[1]), False)
-        out["v"] = _stochastic8(v.sqrt(), _bytes8(w[2], w[3]), True)
+        rnd = _halves8(_philox_words(st["group8"], st["tensor8"], STEP, st["seed"]))
+        out["m"] = _stochastic8(m, rnd, False)
+        out["v"] = _stochastic8(v.sqrt(), rnd, True)
     return out
 
 
@@ -516,8 +516,8 @@ def _e4m3_64(codes, scales):
     return v * torch.exp2(scales.double() - 127).repeat_interleave(32)
 
 
-def _random_bytes(st):
-    """The generator's sixteen bytes for every group of eight elements, from its published rounds."""
+def _random_halves(st):
+    """The generator's 16 bits for every element (128 for eight), from its published rounds."""
     u = np.uint64
     low, c = u(0xFFFFFFFF), [st["group8"].cpu().numpy().astype(u), None, None, st["tensor8"].cpu().numpy().astype(u)]
     c[1], c[2] = np.zeros_like(c[0]), np.full_like(c[0], STEP)
@@ -527,18 +527,18 @@ def _random_bytes(st):
         c = [(b >> u(32)) ^ c[1] ^ u(key[0]), b & low, (a >> u(32)) ^ c[3] ^ u(key[1]), a & low]
         key = [(key[0] + 0x9E3779B9) & 0xFFFFFFFF, (key[1] + 0xBB67AE85) & 0xFFFFFFFF]
     words = np.stack(c, 1).astype("<u4")
-    return torch.from_numpy(words.view(np.uint8).reshape(-1, 16)).to(DEV)
+    return torch.from_numpy(words.view("<u2").reshape(-1).astype(np.int32)).to(DEV)
 
 
-def _rounded_64(x, byte):
-    """x in units of its block's scale on the E4M3 grid, rounded up where the fraction and byte/256
+def _rounded_64(x, rnd):
+    """x in units of its block's scale on the E4M3 grid, rounded up where the fraction and rnd/65536
     reach one, and the scales."""
     top = x.abs().reshape(-1, 32).amax(1)
     e = torch.ceil(torch.log2(torch.where(top > 0, top, torch.ones_like(top)) / 448)).clamp_min(-117)
     unit = torch.exp2(torch.where(top > 0, e, torch.full_like(e, -127)))
     y = x.abs() / unit.repeat_interleave(32)
     gap = torch.exp2(torch.floor(torch.log2(y.clamp_min(2.0 ** -6))) - 3)
-    return torch.floor(y / gap + byte.double() / 256) * gap, unit
+    return torch.floor(y / gap + rnd.double() / 65536) * gap, unit
 
 
 def _exact_adamw(st, case):
@@ -554,11 +554,11 @@ def _exact_adamw(st, case):
     step = (m / (1 - B1 ** STEP)) / ((v / (1 - B2 ** STEP)).sqrt() + EPS)
     p = p0 - LR * (step + st["decay_at"].double() * p0)
     if eight:
-        byte = _random_bytes(st)
+        rnd = _random_halves(st)
         r = v.sqrt()
-        q, q_unit = _rounded_64(r, byte[:, 8:].reshape(-1))
+        q, q_unit = _rounded_64(r, rnd)
         v = torch.where(r > 0, q.clamp_min(1 / 512), torch.zeros_like(q)), q_unit
-        q, q_unit = _rounded_64(m, byte[:, :8].reshape(-1))
+        q, q_unit = _rounded_64(m, rnd)
         m = torch.sign(m) * q, q_unit
     return {"p": p, "w": p, "m": m, "v": v, "norm": norm}
 
