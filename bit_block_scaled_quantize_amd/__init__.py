@@ -6,7 +6,8 @@ returns; all arithmetic runs in the HIP kernels. If the library is not built the
 still succeeds but every call raises, so nothing can silently fall back to another path.
 
 Names follow the C entry points: quantize, quantize_noalloc, rht_quantize, rht_rows_quantize,
-gemm, gemm_ex, grouped_gemm, grouped_gemm_k, amax, amax_pair, mx_quantize, mx_quantize_columns, mx_gemm, dequantize.
+gemm, gemm_ex, grouped_gemm, grouped_gemm_k, amax, amax_pair, mx_quantize, mx_quantize_columns, mx_gemm, dequantize,
+adamw.
 """
 from __future__ import annotations
 
@@ -27,13 +28,14 @@ _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 _BLOCK = {"1x16": 0, "16x16": 1}
 _ROUND = {"rn": 0, "sr": 1}
 OP_QUANTIZE, OP_RHT_QUANTIZE, OP_GEMM, OP_GROUPED_GEMM, OP_AMAX_PAIR, OP_GEMM_EX = 0, 1, 2, 3, 4, 5
+OP_ADAMW = 6
 OUT_FP32, OUT_FP32_ACCUMULATE, OUT_BF16 = 0, 1, 2
 
 EXPORTED = ("nvfp4_quantize", "nvfp4_quantize_noalloc", "nvfp4_rht_quantize", "nvfp4_gemm", "nvfp4_gemm_ex", "nvfp4_grouped_gemm",
             "mxfp4_quantize", "mxfp4_quantize_columns", "mxfp4_gemm", "nvfp4_rht_rows_quantize",
             "nvfp4_grouped_gemm_k",
             "nvfp4_amax", "nvfp4_amax_pair", "nvfp4_workspace_size", "nvfp4_last_error",
-            "nvfp4_dequantize")
+            "nvfp4_dequantize", "nvfp4_adamw", "nvfp4_adamw_table", "nvfp4_adamw_table_size")
 
 
 class NVFP4Error(RuntimeError):
@@ -49,6 +51,19 @@ class _CTensor(ctypes.Structure):
 class _CMXTensor(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
                 ("cols", ctypes.c_int64)]
+
+
+class _CAdamWTensor(ctypes.Structure):
+    _fields_ = ([("n", ctypes.c_int64)]
+                + [(k, ctypes.c_void_p) for k in ("grad", "p", "p_out", "w_out", "m", "v", "m_out", "v_out",
+                                                  "m_scale", "v_scale", "m_scale_out", "v_scale_out")]
+                + [("weight_decay", ctypes.c_float), ("grad_dt", ctypes.c_int)])
+
+
+class _CAdamWHyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("max_norm", ctypes.c_double),
+                ("seed", ctypes.c_uint64)]
 
 
 _lib = None
@@ -86,8 +101,12 @@ def _load():
     lib.nvfp4_workspace_size.restype = sz
     lib.nvfp4_last_error.restype = ctypes.c_char_p
     lib.nvfp4_dequantize.argtypes = [pt, vp, i64, vp, vp]
+    lib.nvfp4_adamw_table_size.argtypes = [ctypes.POINTER(_CAdamWTensor), i64]
+    lib.nvfp4_adamw_table_size.restype = sz
+    lib.nvfp4_adamw_table.argtypes = [ctypes.POINTER(_CAdamWTensor), i64, ctypes.c_int, vp, sz, ctypes.POINTER(i64)]
+    lib.nvfp4_adamw.argtypes = [vp, i64, i64, ctypes.c_int, ctypes.POINTER(_CAdamWHyper), vp, vp, vp, sz, vp]
     for name in EXPORTED:
-        if name not in ("nvfp4_workspace_size", "nvfp4_last_error"):
+        if name not in ("nvfp4_workspace_size", "nvfp4_last_error", "nvfp4_adamw_table_size"):
             getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -119,11 +138,12 @@ def _on_stream(fn):
     kernels are enqueued on. torch's caching allocator hands a freed block out again only to
     work on the stream it belongs to, so a workspace freed when the function returns cannot be
     given to other work while these kernels may still be using it."""
-    sig = inspect.signature(fn)
+    names = list(inspect.signature(fn).parameters)
+    at = names.index("stream")
 
     @functools.wraps(fn)
     def wrapper(*args, **kwargs):
-        stream = sig.bind(*args, **kwargs).arguments.get("stream")
+        stream = args[at] if len(args) > at else kwargs.get("stream")
         if stream is None:
             return fn(*args, **kwargs)
         with torch.cuda.stream(stream):
@@ -536,3 +556,103 @@ def dequantize(q: NVFP4Tensor, segments: torch.Tensor | None = None, stream=None
     qc = q.c()
     _check(lib.nvfp4_dequantize(ctypes.byref(qc), _ptr(segments), nseg, _ptr(y), _stream(stream)))
     return y
+
+
+@dataclass
+class AdamWTensor:
+    """One tensor of an AdamW step (nvfp4_adamw_tensor): contiguous GPU tensors of the same number
+    of elements. m and v are FP32, or uint8 E4M3 codes (v then holds sqrt(v)) with uint8 E8M0
+    scales, one per 32 elements. An output left out is its input (the step is in place); w_out
+    receives the BF16 weight."""
+    p: torch.Tensor
+    grad: torch.Tensor
+    m: torch.Tensor
+    v: torch.Tensor
+    m_scale: torch.Tensor | None = None
+    v_scale: torch.Tensor | None = None
+    w_out: torch.Tensor | None = None
+    p_out: torch.Tensor | None = None
+    m_out: torch.Tensor | None = None
+    v_out: torch.Tensor | None = None
+    m_scale_out: torch.Tensor | None = None
+    v_scale_out: torch.Tensor | None = None
+    weight_decay: float = 0.0
+
+
+class AdamWPlan:
+    """The device table of the tensors that adamw steps together (nvfp4_adamw_table). It holds
+    their addresses and keeps them alive: gradients have to stay where they are from step to
+    step (NVFP4Linear.main_grad does; zero a .grad instead of setting it to None)."""
+
+    def __init__(self, tensors):
+        tensors = list(tensors)
+        if not tensors:
+            raise NVFP4Error("an AdamW plan needs at least one tensor")
+        lib = _load()
+        self.tensors = tensors
+        self.eight_bit = tensors[0].m.dtype == torch.uint8
+        self.device = tensors[0].p.device
+        array = (_CAdamWTensor * len(tensors))(*(self._entry(i, t) for i, t in enumerate(tensors)))
+        size = lib.nvfp4_adamw_table_size(array, len(tensors))
+        host = torch.empty((max(size, 1),), dtype=torch.uint8)
+        chunks = ctypes.c_int64()
+        _check(lib.nvfp4_adamw_table(array, len(tensors), int(self.eight_bit), _ptr(host), size, ctypes.byref(chunks)))
+        self.chunks = chunks.value
+        self.table = host.to(self.device)
+
+    def _entry(self, i: int, t: AdamWTensor) -> _CAdamWTensor:
+        n = t.p.numel()
+        state = torch.uint8 if self.eight_bit else torch.float32
+
+        def need(name, x, dtype, count=n):
+            if (not isinstance(x, torch.Tensor) or x.dtype != dtype or x.numel() != count or not x.is_contiguous()
+                    or x.device.type != "cuda" or x.device != self.device):
+                raise NVFP4Error(f"tensor {i}: {name} must be a contiguous {dtype} tensor of {count} elements on "
+                                 f"the GPU of the first tensor")
+            return x.data_ptr()
+
+        if not isinstance(t.grad, torch.Tensor) or t.grad.dtype not in _DTYPE:
+            raise NVFP4Error(f"tensor {i}: grad must be a bfloat16 or float32 tensor")
+        c = _CAdamWTensor(n=n, weight_decay=float(t.weight_decay), grad_dt=_DTYPE[t.grad.dtype])
+        c.grad = need("grad", t.grad, t.grad.dtype)
+        c.p = need("p", t.p, torch.float32)
+        c.p_out = c.p if t.p_out is None else need("p_out", t.p_out, torch.float32)
+        if t.w_out is not None:
+            c.w_out = need("w_out", t.w_out, torch.bfloat16)
+        for k in ("m", "v"):
+            src, dst = getattr(t, k), getattr(t, k + "_out")
+            setattr(c, k, need(k, src, state))
+            setattr(c, k + "_out", getattr(c, k) if dst is None else need(k + "_out", dst, state))
+            if self.eight_bit:
+                src, dst, blocks = getattr(t, k + "_scale"), getattr(t, k + "_scale_out"), (n + 31) // 32
+                setattr(c, k + "_scale", need(k + "_scale", src, torch.uint8, blocks))
+                setattr(c, k + "_scale_out",
+                        getattr(c, k + "_scale") if dst is None else need(k + "_scale_out", dst, torch.uint8, blocks))
+        return c
+
+
+@_on_stream
+def adamw(plan: AdamWPlan, lr: float, betas=(0.9, 0.95), eps: float = 1e-8, step: int = 1,
+          max_norm: float | None = None, seed: int = 0, norm_out: torch.Tensor | None = None,
+          amax_out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """nvfp4_adamw: one AdamW step (number `step`, from 1) of the plan's tensors. With max_norm the
+    gradients are clipped by their norm over all tensors, which norm_out (float32 [1], allocated if
+    left out) receives and the call returns; a norm that is not finite leaves every tensor as it
+    was. amax_out (float32 [tensors]) receives each tensor's max|weight|, the `amax` of its next
+    quantize. seed: of the 8-bit states' stochastic rounding."""
+    lib = _load()
+    if max_norm is not None and norm_out is None:
+        norm_out = torch.empty((1,), dtype=torch.float32, device=plan.device)
+    _check_vec(norm_out, 1, "norm_out")
+    _check_vec(amax_out, len(plan.tensors), "amax_out")
+    ws_n = 0
+    if max_norm is not None:
+        if workspace is None:
+            workspace, ws_n = _workspace(OP_ADAMW, 0, 0, 1, plan.device)
+        else:
+            ws_n = workspace.numel()
+    hyper = _CAdamWHyper(lr, betas[0], betas[1], eps, step, 0.0 if max_norm is None else max_norm, seed & (2 ** 64 - 1))
+    _check(lib.nvfp4_adamw(_ptr(plan.table), len(plan.tensors), plan.chunks, int(plan.eight_bit), ctypes.byref(hyper),
+                           _ptr(norm_out), _ptr(amax_out), _ptr(workspace) if max_norm is not None else None, ws_n,
+                           _stream(stream)))
+    return norm_out

@@ -1,7 +1,9 @@
 // C ABI of libnvfp4 (declared in include/nvfp4.h): host-side validation, workspace
 // sizing and dispatch to the gfx950 kernels. Nothing here allocates device memory.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstring>
 #include <mutex>
 #include <string>
 
@@ -120,6 +122,7 @@ size_t nvfp4_workspace_size(int op, int64_t rows, int64_t cols, int64_t nseg) {
       return round_up(segs > partials ? segs : partials, kWsAlign);
     }
     case NVFP4_OP_AMAX_PAIR: return round_up(2 * partials, kWsAlign);
+    case NVFP4_OP_ADAMW: return round_up((size_t)nvfp4::kAdamWMaxParts * sizeof(double), kWsAlign);
     case NVFP4_OP_GEMM_EX: return round_up(nvfp4::gemm_ex_workspace_bytes(rows, cols), kWsAlign);
     default: return 0;
   }
@@ -490,6 +493,114 @@ int nvfp4_dequantize(const nvfp4_tensor* q, const int64_t* segments, int64_t nse
   if (nseg < 1 || (!segments && nseg != 1)) return fail(NVFP4_ERR_INVALID, "bad segment table (nseg=%lld)", (long long)nseg);
   return hip_status(nvfp4::launch_dequantize(q->codes, q->scales, q->global_scale, segments, nseg,
                                              q->rows, q->cols, y, (hipStream_t)hip_stream), "dequantize");
+}
+
+size_t nvfp4_adamw_table_size(const nvfp4_adamw_tensor* tensors, int64_t count) {
+  if (!tensors || count < 1 || count > (int64_t(1) << 31) - 1) return 0;
+  uint64_t chunks = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (tensors[i].n < 0) return 0;
+    chunks += (uint64_t)tensors[i].n / nvfp4::kAdamWChunk + (tensors[i].n % nvfp4::kAdamWChunk != 0);
+    if (chunks > (uint64_t)0x7FFFFFFF) return 0;
+  }
+  return (size_t)count * sizeof(nvfp4::AdamWEntry) + (size_t)chunks * sizeof(int32_t);
+}
+
+int nvfp4_adamw_table(const nvfp4_adamw_tensor* tensors, int64_t count, nvfp4_state state, void* table,
+                      size_t table_bytes, int64_t* chunks) {
+  if (!tensors || !table || !chunks) return fail(NVFP4_ERR_INVALID, "tensors, table or chunks is NULL");
+  if (count < 1) return fail(NVFP4_ERR_INVALID, "bad tensor count %lld", (long long)count);
+  if (state != NVFP4_STATE_FP32 && state != NVFP4_STATE_8BIT) return fail(NVFP4_ERR_INVALID, "bad state %d", (int)state);
+  const bool eight = state == NVFP4_STATE_8BIT;
+  for (int64_t i = 0; i < count; ++i) {
+    const nvfp4_adamw_tensor& t = tensors[i];
+    if (t.n < 0) return fail(NVFP4_ERR_INVALID, "tensor %lld: n = %lld", (long long)i, (long long)t.n);
+    if (t.grad_dt != NVFP4_IN_BF16 && t.grad_dt != NVFP4_IN_FP32)
+      return fail(NVFP4_ERR_INVALID, "tensor %lld: bad grad_dt %d", (long long)i, (int)t.grad_dt);
+    if (t.n == 0) continue;
+    if (!t.grad || !t.p || !t.p_out || !t.m || !t.v || !t.m_out || !t.v_out)
+      return fail(NVFP4_ERR_INVALID, "tensor %lld has a NULL grad/p/m/v pointer", (long long)i);
+    if (eight && (!t.m_scale || !t.v_scale || !t.m_scale_out || !t.v_scale_out))
+      return fail(NVFP4_ERR_INVALID, "tensor %lld has a NULL scale pointer", (long long)i);
+    const size_t state_align = eight ? 1 : 4;
+    if (!aligned(t.grad, t.grad_dt == NVFP4_IN_FP32 ? 4 : 2) || !aligned(t.p, 4) || !aligned(t.p_out, 4) ||
+        !aligned(t.w_out, 2) || !aligned(t.m, state_align) || !aligned(t.v, state_align) ||
+        !aligned(t.m_out, state_align) || !aligned(t.v_out, state_align))
+      return fail(NVFP4_ERR_INVALID, "tensor %lld has a pointer not aligned to its element", (long long)i);
+  }
+  const size_t need = nvfp4_adamw_table_size(tensors, count);
+  if (need == 0) return fail(NVFP4_ERR_UNSUPPORTED, "more than 2^31 - 1 chunks of %lld elements", (long long)nvfp4::kAdamWChunk);
+  if (table_bytes < need) return fail(NVFP4_ERR_INVALID, "table of %zu bytes required, got %zu", need, table_bytes);
+  uint8_t* entry = static_cast<uint8_t*>(table);
+  uint8_t* list = entry + (size_t)count * sizeof(nvfp4::AdamWEntry);
+  int64_t c = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const nvfp4_adamw_tensor& t = tensors[i];
+    nvfp4::AdamWEntry e{};
+    e.n = t.n;
+    e.first_chunk = c;
+    e.grad = t.grad;
+    e.p = t.p;
+    e.p_out = t.p_out;
+    e.w_out = t.w_out;
+    e.m = t.m;
+    e.v = t.v;
+    e.m_out = t.m_out;
+    e.v_out = t.v_out;
+    e.m_scale = t.m_scale;
+    e.v_scale = t.v_scale;
+    e.m_scale_out = t.m_scale_out;
+    e.v_scale_out = t.v_scale_out;
+    e.weight_decay = t.weight_decay;
+    // whole-vector access: 8 elements of every array start on 16 bytes (8 for the codes)
+    const size_t sa = eight ? 8 : 16;
+    const bool vec = aligned(t.grad, 16) && aligned(t.p, 16) && aligned(t.p_out, 16) && aligned(t.w_out, 16) &&
+                     aligned(t.m, sa) && aligned(t.v, sa) && aligned(t.m_out, sa) && aligned(t.v_out, sa);
+    e.flags = (vec ? nvfp4::kAdamWAligned : 0) | (t.grad_dt == NVFP4_IN_BF16 ? nvfp4::kAdamWGradBf16 : 0);
+    memcpy(entry + (size_t)i * sizeof(e), &e, sizeof(e));
+    const int32_t id = (int32_t)i;
+    for (int64_t k = 0; k < (t.n + nvfp4::kAdamWChunk - 1) / nvfp4::kAdamWChunk; ++k, ++c)
+      memcpy(list + (size_t)c * sizeof(id), &id, sizeof(id));
+  }
+  *chunks = c;
+  return NVFP4_OK;
+}
+
+int nvfp4_adamw(const void* table, int64_t count, int64_t chunks, nvfp4_state state,
+                const nvfp4_adamw_hyper* hyper, float* norm_out, float* amax_out, void* workspace,
+                size_t ws_bytes, void* hip_stream) {
+  if (!table || !hyper) return fail(NVFP4_ERR_INVALID, "table or hyper is NULL");
+  if (!aligned(table, 16)) return fail(NVFP4_ERR_INVALID, "table must be 16-byte aligned");
+  if (count < 1 || count > 0x7FFFFFFF || chunks < 0 || chunks > 0x7FFFFFFF)
+    return fail(NVFP4_ERR_INVALID, "bad count %lld or chunks %lld", (long long)count, (long long)chunks);
+  if (state != NVFP4_STATE_FP32 && state != NVFP4_STATE_8BIT) return fail(NVFP4_ERR_INVALID, "bad state %d", (int)state);
+  const nvfp4_adamw_hyper& h = *hyper;
+  if (!std::isfinite(h.lr) || !(h.beta1 >= 0 && h.beta1 < 1) || !(h.beta2 >= 0 && h.beta2 < 1) ||
+      !((float)h.eps > 0 && std::isfinite(h.eps)) || h.step < 1 || !(h.max_norm >= 0))
+    return fail(NVFP4_ERR_INVALID, "lr %g, beta1 %g, beta2 %g, eps %g, step %lld or max_norm %g out of range", h.lr,
+                h.beta1, h.beta2, h.eps, (long long)h.step, h.max_norm);
+  const bool clip = h.max_norm > 0;
+  if (norm_out && !clip) return fail(NVFP4_ERR_INVALID, "norm_out needs max_norm > 0");
+  if (clip) {
+    const size_t need = nvfp4_workspace_size(NVFP4_OP_ADAMW, 0, 0, 0);
+    if (!workspace || ws_bytes < need || !aligned(workspace, kWsAlign))
+      return fail(NVFP4_ERR_WORKSPACE, "workspace of %zu bytes (256-byte aligned) required, got %zu", need, ws_bytes);
+  }
+  nvfp4::AdamWHyper d;
+  d.lr = (float)h.lr;
+  d.beta1 = (float)h.beta1;
+  d.one_beta1 = (float)(1.0 - h.beta1);
+  d.beta2 = (float)h.beta2;
+  d.one_beta2 = (float)(1.0 - h.beta2);
+  d.eps = (float)h.eps;
+  d.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(h.beta2, (double)h.step)));
+  d.step_size = (float)(h.lr / (1.0 - std::pow(h.beta1, (double)h.step)));
+  d.max_norm = (float)h.max_norm;
+  d.step = (uint32_t)h.step;
+  d.seed = h.seed;
+  return hip_status(nvfp4::launch_adamw(table, count, chunks, state == NVFP4_STATE_8BIT, d, clip,
+                                        static_cast<double*>(workspace), norm_out, amax_out, (hipStream_t)hip_stream),
+                    "adamw");
 }
 
 }  // extern "C"

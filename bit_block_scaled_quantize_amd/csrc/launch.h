@@ -72,6 +72,35 @@ hipError_t launch_fill(float* p, int64_t n, float v, hipStream_t stream);
 
 constexpr int kMaxAmaxPartials = 1024;
 
+// AdamW over many tensors. The device table is `count` entries followed by one int32 per chunk
+// (the entry that the chunk belongs to); a chunk is kAdamWChunk consecutive elements of one tensor.
+constexpr int64_t kAdamWChunk = 8192;
+constexpr int kAdamWMaxParts = 1024;                     // partial sums of the gradient norm
+enum AdamWFlags : int32_t { kAdamWAligned = 1, kAdamWGradBf16 = 2 };
+struct AdamWEntry {
+  int64_t n, first_chunk;
+  const void* grad;
+  const float* p;
+  float* p_out;
+  uint16_t* w_out;                                       // or null
+  const void *m, *v;                                     // FP32, or E4M3 codes
+  void *m_out, *v_out;
+  const uint8_t *m_scale, *v_scale;                      // 8-bit states: E8M0 per 32 elements
+  uint8_t *m_scale_out, *v_scale_out;
+  float weight_decay;
+  int32_t flags;
+};
+static_assert(sizeof(AdamWEntry) % 8 == 0, "the chunk list follows the entries");
+struct AdamWHyper {
+  float lr, beta1, one_beta1, beta2, one_beta2, eps, inv_sqrt_bc2, step_size, max_norm;
+  uint32_t step;
+  uint64_t seed;
+};
+int adamw_norm_parts(int64_t chunks);
+// clip: ws holds adamw_norm_parts(chunks) doubles. norm_out, amax_out: device float[1], float[count], or null.
+hipError_t launch_adamw(const void* table, int64_t count, int64_t chunks, bool eight, const AdamWHyper& hp,
+                        bool clip, double* ws, float* norm_out, float* amax_out, hipStream_t stream);
+
 struct GemmOperand {
   const uint8_t* codes;
   const uint8_t* scales;

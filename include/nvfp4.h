@@ -61,7 +61,7 @@ typedef enum { NVFP4_BLOCK_1X16 = 0, NVFP4_BLOCK_16X16 = 1 } nvfp4_block;
 typedef enum { NVFP4_ROUND_RN = 0, NVFP4_ROUND_SR = 1 } nvfp4_round;
 typedef enum {
   NVFP4_OP_QUANTIZE = 0, NVFP4_OP_RHT_QUANTIZE = 1, NVFP4_OP_GEMM = 2,
-  NVFP4_OP_GROUPED_GEMM = 3, NVFP4_OP_AMAX_PAIR = 4, NVFP4_OP_GEMM_EX = 5
+  NVFP4_OP_GROUPED_GEMM = 3, NVFP4_OP_AMAX_PAIR = 4, NVFP4_OP_GEMM_EX = 5, NVFP4_OP_ADAMW = 6
 } nvfp4_op;
 /* Output of nvfp4_gemm_ex: FP32, FP32 added to what D holds, or BF16. */
 typedef enum { NVFP4_OUT_FP32 = 0, NVFP4_OUT_FP32_ACCUMULATE = 1, NVFP4_OUT_BF16 = 2 } nvfp4_out;
@@ -366,6 +366,87 @@ int nvfp4_amax(const void* x, nvfp4_dtype dt, int64_t rows, int64_t cols, int64_
 int nvfp4_amax_pair(const void* x, nvfp4_dtype dt, int64_t tokens, int64_t cols, int64_t ld,
                     uint16_t sign_mask, float* amax_out, void* workspace, size_t ws_bytes,
                     void* hip_stream);
+
+/* How the two running means of AdamW are held: FP32, or 8 bits (below). */
+typedef enum { NVFP4_STATE_FP32 = 0, NVFP4_STATE_8BIT = 1 } nvfp4_state;
+
+/* One tensor of an AdamW step: n elements, contiguous. Every output may be its input (the usual
+ * in-place step) or a buffer that overlaps no input and no other output. */
+typedef struct nvfp4_adamw_tensor {
+  int64_t n;                   /* elements, >= 0                                            */
+  const void* grad;            /* device BF16 or FP32 (grad_dt) [n]                         */
+  const float* p;              /* device FP32 [n]: the parameter (a BF16 weight's master copy) */
+  float* p_out;                /* device FP32 [n]                                           */
+  uint16_t* w_out;             /* NULL, or device BF16 [n]: p_out rounded to nearest even   */
+  const void* m;               /* FP32 [n], or E4M3 codes uint8 [n]                         */
+  const void* v;               /* FP32 [n], or E4M3 codes uint8 [n] of sqrt(v)              */
+  void* m_out;
+  void* v_out;
+  const uint8_t* m_scale;      /* 8-bit states: E8M0 per 32 elements, uint8 [ceil(n/32)]    */
+  const uint8_t* v_scale;
+  uint8_t* m_scale_out;
+  uint8_t* v_scale_out;
+  float weight_decay;          /* decoupled decay of this tensor (0 for biases and norms)   */
+  nvfp4_dtype grad_dt;
+} nvfp4_adamw_tensor;
+
+typedef struct nvfp4_adamw_hyper {
+  double lr, beta1, beta2, eps;  /* 0 <= beta < 1, eps > 0                                   */
+  int64_t step;                  /* 1 for the first step (bias correction, random bytes)     */
+  double max_norm;               /* > 0: clip the gradient's norm over all tensors; 0: do not */
+  uint64_t seed;                 /* of the 8-bit states' stochastic rounding                 */
+} nvfp4_adamw_hyper;
+
+/*
+ * nvfp4_adamw - one AdamW step over many tensors at once (the optimizer states and the master
+ * weights stay in high precision around the 4-bit GEMMs: artiverse.ca "NVIDIA's 4-bit floating
+ * point pushes AI training limits", paragraph on which parts run in 4-bit). The gradient is the
+ * FP32 main gradient that nvfp4_gemm_ex accumulates, or a BF16 one. Per element, in FP32:
+ *   g  = c * grad,  c = min(1, max_norm / (norm + 1e-6)) with max_norm > 0, else 1
+ *   m' = beta1 m + (1 - beta1) g;   v' = beta2 v + (1 - beta2) g^2
+ *   p' = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m' / (sqrt(v' / (1 - beta2^step)) + eps)
+ * norm = sqrt(sum of grad^2 over all tensors), summed in a fixed order. With max_norm > 0 a norm
+ * that is infinite or NaN makes the step write back what it read (w_out = BF16(p)); without it
+ * non-finite gradients are outside the contract.
+ *
+ * NVFP4_STATE_8BIT holds m and r = sqrt(v) as E4M3 codes with one scale 2^e per 32 consecutive
+ * elements (E8M0 code e + 127; e is the smallest exponent with max|x| <= 448 * 2^e, at least
+ * -117; code 0 and value 0 for an all-zero block). A value y = |x| 2^-e is rounded up to the next
+ * E4M3 value iff its fraction of the gap + h/65536 >= 1; a nonzero r never becomes 0. Element
+ * 8b + j (j < 8) of tensor i takes for h the 16 bits of half j % 2 (low first) of word j / 2 of
+ * Philox4x32-10 with key (lo32 seed, hi32 seed) and counter (lo32 b, hi32 b, lo32 step, i), the
+ * same h for m and r.
+ *
+ *   table      device copy of the bytes that nvfp4_adamw_table wrote for these tensors, 16-byte
+ *              aligned, and the count, chunks and state of that call.
+ *   norm_out   NULL, or device float[1] receiving norm (max_norm > 0 only).
+ *   amax_out   NULL, or device float[count] receiving max|w_out| (max|p_out| where w_out is
+ *              NULL) of each tensor: the amax_in of the weight's next nvfp4_quantize.
+ *   workspace  nvfp4_workspace_size(NVFP4_OP_ADAMW, 0, 0, 0) bytes, 256-byte aligned; may be NULL
+ *              with max_norm = 0.
+ * The result is deterministic. Errors: NVFP4_ERR_INVALID (NULL table, count or chunks out of
+ * range, hyperparameters out of range, bad enum), NVFP4_ERR_WORKSPACE, NVFP4_ERR_HIP.
+ */
+int nvfp4_adamw(const void* table, int64_t count, int64_t chunks, nvfp4_state state,
+                const nvfp4_adamw_hyper* hyper, float* norm_out, float* amax_out,
+                void* workspace, size_t ws_bytes, void* hip_stream);
+
+/* Bytes of the table of `count` tensors (their n alone is read), 0 for a bad argument. */
+size_t nvfp4_adamw_table_size(const nvfp4_adamw_tensor* tensors, int64_t count);
+
+/*
+ * nvfp4_adamw_table - checks the tensors and writes their table (the optimizer side of artiverse.ca
+ * "NVIDIA's 4-bit floating point pushes AI training limits", as above) to HOST memory: the caller
+ * copies it to the device once and keeps it for as long as the tensors stay where they are.
+ * Nothing is enqueued.
+ *   tensors    host array [count], count >= 1.
+ *   table      host memory of at least nvfp4_adamw_table_size bytes.
+ *   chunks     receives the value to pass to nvfp4_adamw.
+ * Errors: NVFP4_ERR_INVALID (NULL or misaligned pointers with n > 0, n < 0, bad dtype or state,
+ * table_bytes too small), NVFP4_ERR_UNSUPPORTED (more than 2^31 - 1 chunks of 8192 elements).
+ */
+int nvfp4_adamw_table(const nvfp4_adamw_tensor* tensors, int64_t count, nvfp4_state state, void* table,
+                      size_t table_bytes, int64_t* chunks);
 
 /* Bytes of device workspace `op` needs for the given shape (0 if none). The library allocates
  * no memory itself (caller-owned buffers, see the conventions above), so the partial maxima of

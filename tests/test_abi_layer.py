@@ -1,0 +1,76 @@
+"""Host-side refusals of the layer operators' C entries (no GPU: every call fails its checks before
+anything is enqueued, or touches host memory alone)."""
+import ctypes
+import os
+
+import pytest
+
+import bit_block_scaled_quantize_amd as nv
+
+INVALID, UNSUPPORTED, WORKSPACE = -1, -2, -3
+FAKE = 0x10000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(nv.LIB_PATH):
+        pytest.skip("libnvfp4.so not built")
+    return nv.library()
+
+
+def _entry(n=100, **kw):
+    f = {k: FAKE for k in ("grad", "p", "p_out", "w_out", "m", "v", "m_out", "v_out", "m_scale", "v_scale",
+                           "m_scale_out", "v_scale_out")}
+    f.update(kw)
+    return nv._CAdamWTensor(n=n, grad_dt=f.pop("grad_dt", 1), weight_decay=0.0, **f)
+
+
+def _table(lib, entries, state=0, bytes_=None, null=False):
+    arr = (nv._CAdamWTensor * len(entries))(*entries)
+    size = lib.nvfp4_adamw_table_size(arr, len(entries))
+    buf = ctypes.create_string_buffer(max(size, 64))
+    chunks = ctypes.c_int64(-1)
+    st = lib.nvfp4_adamw_table(arr, len(entries), state, None if null else buf, size if bytes_ is None else bytes_,
+                               ctypes.byref(chunks))
+    return st, chunks.value, size
+
+
+def test_adamw_table(lib):
+    st, chunks, _ = _table(lib, [_entry(1), _entry(8192), _entry(8193), _entry(0, grad=None, p=None)])
+    assert (st, chunks) == (0, 4)
+    assert _table(lib, [_entry()], null=True)[0] == INVALID
+    assert _table(lib, [_entry()], state=2)[0] == INVALID
+    assert _table(lib, [_entry(n=-1)])[0] == INVALID
+    assert _table(lib, [_entry(grad_dt=5)])[0] == INVALID
+    assert _table(lib, [_entry(p=None)])[0] == INVALID
+    assert _table(lib, [_entry(p=FAKE + 2)])[0] == INVALID
+    assert _table(lib, [_entry(grad=FAKE + 2)])[0] == INVALID
+    assert _table(lib, [_entry(grad=FAKE + 2, grad_dt=0)])[0] == 0
+    assert _table(lib, [_entry(m=FAKE + 1)])[0] == INVALID
+    assert _table(lib, [_entry(m=FAKE + 1)], state=1)[0] == 0
+    assert _table(lib, [_entry(m_scale=None)], state=1)[0] == INVALID
+    assert _table(lib, [_entry(m_scale=None)], state=0)[0] == 0
+    assert _table(lib, [_entry()], bytes_=8)[0] == INVALID
+    assert _table(lib, [_entry(n=1 << 50)])[0] == UNSUPPORTED
+    assert lib.nvfp4_adamw_table_size(None, 1) == 0
+
+
+def test_adamw_validation(lib):
+    def call(table=FAKE, count=1, chunks=1, state=0, ws=FAKE, ws_n=8192, norm=None, **hp):
+        h = dict(lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, step=1, max_norm=1.0, seed=0)
+        h.update(hp)
+        return lib.nvfp4_adamw(table, count, chunks, state, ctypes.byref(nv._CAdamWHyper(**h)), norm, None, ws, ws_n, None)
+
+    assert lib.nvfp4_workspace_size(nv.OP_ADAMW, 0, 0, 0) == 8192
+    assert call(table=None) == INVALID
+    assert call(table=FAKE + 8) == INVALID
+    assert call(count=0) == INVALID
+    assert call(chunks=-1) == INVALID
+    assert call(state=3) == INVALID
+    for hp in (dict(lr=float("inf")), dict(beta1=1.0), dict(beta2=float("nan")), dict(eps=0.0), dict(eps=1e-60),
+               dict(step=0), dict(max_norm=-1.0), dict(max_norm=float("nan"))):
+        assert call(**hp) == INVALID, hp
+    assert call(max_norm=0.0, norm=FAKE) == INVALID
+    assert call(ws=None) == WORKSPACE
+    assert call(ws_n=100) == WORKSPACE
+    assert lib.nvfp4_adamw(FAKE, 1, 1, 0, None, None, None, None, 0, None) == INVALID
