@@ -7,7 +7,7 @@ still succeeds but every call raises, so nothing can silently fall back to anoth
 
 Names follow the C entry points: quantize, quantize_noalloc, rht_quantize, rht_rows_quantize,
 gemm, gemm_ex, grouped_gemm, grouped_gemm_k, amax, amax_pair, mx_quantize, mx_quantize_columns, mx_gemm, dequantize,
-adamw.
+gemm_act, act_grad, adamw.
 """
 from __future__ import annotations
 
@@ -28,14 +28,15 @@ _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 _BLOCK = {"1x16": 0, "16x16": 1}
 _ROUND = {"rn": 0, "sr": 1}
 OP_QUANTIZE, OP_RHT_QUANTIZE, OP_GEMM, OP_GROUPED_GEMM, OP_AMAX_PAIR, OP_GEMM_EX = 0, 1, 2, 3, 4, 5
-OP_ADAMW = 6
+OP_ADAMW, OP_GEMM_ACT, OP_ACT_GRAD = 6, 7, 8
+ACTIVATIONS = {"none": 0, "relu2": 1, "gelu": 2, "silu": 3}
 OUT_FP32, OUT_FP32_ACCUMULATE, OUT_BF16 = 0, 1, 2
 
 EXPORTED = ("nvfp4_quantize", "nvfp4_quantize_noalloc", "nvfp4_rht_quantize", "nvfp4_gemm", "nvfp4_gemm_ex", "nvfp4_grouped_gemm",
             "mxfp4_quantize", "mxfp4_quantize_columns", "mxfp4_gemm", "nvfp4_rht_rows_quantize",
             "nvfp4_grouped_gemm_k",
             "nvfp4_amax", "nvfp4_amax_pair", "nvfp4_workspace_size", "nvfp4_last_error",
-            "nvfp4_dequantize", "nvfp4_adamw", "nvfp4_adamw_table", "nvfp4_adamw_table_size")
+            "nvfp4_dequantize", "nvfp4_gemm_act", "nvfp4_act_grad", "nvfp4_adamw", "nvfp4_adamw_table", "nvfp4_adamw_table_size")
 
 
 class NVFP4Error(RuntimeError):
@@ -92,6 +93,9 @@ def _load():
     lib.nvfp4_rht_rows_quantize.argtypes = [vp, ctypes.c_int, i64, i64, i64, ctypes.c_uint16, ctypes.c_int,
                                             u64, u64, vp, pt, vp, sz, vp]
     lib.nvfp4_gemm_ex.argtypes = [pt, pt, vp, i64, ctypes.c_int, vp, vp, sz, vp]
+    lib.nvfp4_gemm_act.argtypes = [pt, pt, vp, i64, vp, ctypes.c_int, ctypes.c_int, vp, i64, vp, i64, vp, vp, sz, vp]
+    lib.nvfp4_act_grad.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i64, ctypes.c_int, vp, i64, vp, ctypes.c_int,
+                                   vp, sz, vp]
     lib.nvfp4_grouped_gemm.argtypes = [i64, vp, pt, pt, i64, vp, i64, vp, sz, vp]
     lib.nvfp4_grouped_gemm_k.argtypes = [i64, vp, pt, pt, vp, i64, vp]
     lib.nvfp4_amax.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i64, ctypes.c_int,
@@ -223,6 +227,11 @@ def _check_out(out: torch.Tensor, rows: int, cols: int, dtype, what: str = "out"
         raise NVFP4Error(f"{what} must be a 2-D {dtype} GPU tensor with unit column stride")
     if out.shape[0] < rows or out.shape[1] < cols:
         raise NVFP4Error(f"{what} shape {tuple(out.shape)} smaller than ({rows}, {cols})")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Elements from one row to the next; a single row may have any stride in torch."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
 def _check_table(t, what: str):
@@ -463,6 +472,80 @@ def gemm_ex(a: NVFP4Tensor, b: NVFP4Tensor, out: torch.Tensor | None = None,
     _check(lib.nvfp4_gemm_ex(ctypes.byref(ac), ctypes.byref(bc), _ptr(out), out.stride(0), kind,
                              _ptr(amax_out), _ptr(workspace), ws_n, _stream(stream)))
     return out
+
+
+def _activation(name: str) -> int:
+    if name not in ACTIVATIONS:
+        raise NVFP4Error(f"unknown activation {name!r}: one of {', '.join(ACTIVATIONS)}")
+    return ACTIVATIONS[name]
+
+
+@_on_stream
+def gemm_act(a: NVFP4Tensor, b: NVFP4Tensor, bias: torch.Tensor | None = None, activation: str = "none",
+             residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+             preact: torch.Tensor | None = None, amax_out: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """nvfp4_gemm_act: D = activation(A * B^T + bias) + residual in BF16. bias: [N], bfloat16 or
+    float32; residual: [M, N] bfloat16; preact: a bfloat16 [M, N] tensor that receives A * B^T +
+    bias (what act_grad needs); amax_out (float32 [1]) receives max |D| as stored."""
+    lib = _load()
+    kind = _activation(activation)
+    m, n = a.rows, b.rows
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=a.codes.device)
+    _check_q(a, what="A")
+    _check_q(b, what="B")
+    _check_out(out, m, n, torch.bfloat16)
+    if bias is not None and (bias.dtype not in _DTYPE or bias.dim() != 1 or bias.numel() != n
+                             or not bias.is_contiguous() or bias.device.type != "cuda"):
+        raise NVFP4Error(f"bias must be a contiguous bfloat16 or float32 GPU tensor of {n} elements")
+    if residual is not None:
+        _check_out(residual, m, n, torch.bfloat16, "residual")
+    if preact is not None:
+        _check_out(preact, m, n, torch.bfloat16, "preact")
+    _check_vec(amax_out, 1, "amax_out")
+    if workspace is None:
+        ws_n = workspace_size(OP_GEMM_ACT, m, n)
+        workspace = torch.empty((ws_n,), dtype=torch.uint8, device=a.codes.device) if ws_n else None
+    else:
+        ws_n = workspace.numel()
+    ac, bc = a.c(), b.c()
+    _check(lib.nvfp4_gemm_act(ctypes.byref(ac), ctypes.byref(bc), _ptr(out), _row_stride(out), _ptr(bias),
+                              0 if bias is None else _DTYPE[bias.dtype], kind, _ptr(residual),
+                              0 if residual is None else _row_stride(residual), _ptr(preact),
+                              0 if preact is None else _row_stride(preact), _ptr(amax_out), _ptr(workspace), ws_n,
+                              _stream(stream)))
+    return out
+
+
+@_on_stream
+def act_grad(dy: torch.Tensor, preact: torch.Tensor | None = None, activation: str = "none",
+             dz: torch.Tensor | None = None, dbias: torch.Tensor | None = None, accumulate: bool = False,
+             bias_only: bool = False, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """nvfp4_act_grad: dZ = dY * activation'(Z) in BF16 (returned; allocated if dz is left out) and,
+    with dbias (float32 [N]), its column sums written or (accumulate) added there. dy: [M, N]
+    bfloat16 or float32; preact: gemm_act's. bias_only: no dZ, the column sums alone."""
+    lib = _load()
+    kind = _activation(activation)
+    dt, m, n, ldy = _input(dy)
+    if preact is not None:
+        _check_out(preact, m, n, torch.bfloat16, "preact")
+    if dz is not None:
+        _check_out(dz, m, n, torch.bfloat16, "dz")
+    elif not bias_only:
+        dz = torch.empty((m, n), dtype=torch.bfloat16, device=dy.device)
+    _check_vec(dbias, n, "dbias")
+    ws_n = 0
+    if dbias is not None:
+        if workspace is None:
+            ws_n = workspace_size(OP_ACT_GRAD, m, n)
+            workspace = torch.empty((ws_n,), dtype=torch.uint8, device=dy.device) if ws_n else None
+        else:
+            ws_n = workspace.numel()
+    _check(lib.nvfp4_act_grad(_ptr(dy), dt, m, n, _row_stride(dy), _ptr(preact), 0 if preact is None else _row_stride(preact),
+                              kind, _ptr(dz), 0 if dz is None else _row_stride(dz), _ptr(dbias), int(accumulate),
+                              _ptr(workspace), ws_n, _stream(stream)))
+    return dz
 
 
 @_on_stream

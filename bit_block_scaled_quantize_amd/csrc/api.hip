@@ -102,6 +102,11 @@ int check_input(const void* x, nvfp4_dtype dt, int64_t rows, int64_t cols, int64
   return NVFP4_OK;
 }
 
+int check_act(nvfp4_act act) {
+  if (act < NVFP4_ACT_NONE || act > NVFP4_ACT_SILU) return fail(NVFP4_ERR_INVALID, "bad activation %d", (int)act);
+  return NVFP4_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -122,6 +127,8 @@ size_t nvfp4_workspace_size(int op, int64_t rows, int64_t cols, int64_t nseg) {
       return round_up(segs > partials ? segs : partials, kWsAlign);
     }
     case NVFP4_OP_AMAX_PAIR: return round_up(2 * partials, kWsAlign);
+    case NVFP4_OP_GEMM_ACT: return round_up(nvfp4::gemm_ex_workspace_bytes(rows, cols), kWsAlign);
+    case NVFP4_OP_ACT_GRAD: return round_up(nvfp4::act_grad_workspace_bytes(rows, cols), kWsAlign);
     case NVFP4_OP_ADAMW: return round_up((size_t)nvfp4::kAdamWMaxParts * sizeof(double), kWsAlign);
     case NVFP4_OP_GEMM_EX: return round_up(nvfp4::gemm_ex_workspace_bytes(rows, cols), kWsAlign);
     default: return 0;
@@ -447,6 +454,58 @@ int nvfp4_gemm_ex(const nvfp4_tensor* A, const nvfp4_tensor* B, void* D, int64_t
   const nvfp4::GemmOperand b{B->codes, B->scales, B->global_scale};
   return hip_status(nvfp4::launch_gemm_ex(a, b, A->rows, B->rows, A->cols, (int)out_kind, D, ldd, amax_out,
                                           static_cast<float*>(workspace), (hipStream_t)hip_stream), "gemm_ex");
+}
+
+int nvfp4_gemm_act(const nvfp4_tensor* A, const nvfp4_tensor* B, uint16_t* D, int64_t ldd, const void* bias,
+                   nvfp4_dtype bias_dt, nvfp4_act act, const uint16_t* residual, int64_t ldr, uint16_t* preact,
+                   int64_t ldp, float* amax_out, void* workspace, size_t ws_bytes, void* hip_stream) {
+  int st;
+  if ((st = check_operand(A, "A")) || (st = check_operand(B, "B"))) return st;
+  if (A->cols != B->cols) return fail(NVFP4_ERR_INVALID, "K mismatch: A has %lld, B has %lld", (long long)A->cols, (long long)B->cols);
+  const int64_t N = B->rows;
+  if (!D && A->rows > 0 && N > 0) return fail(NVFP4_ERR_INVALID, "D is NULL");   // an empty D is never written
+  if ((st = check_act(act))) return st;
+  if (bias && bias_dt != NVFP4_IN_BF16 && bias_dt != NVFP4_IN_FP32) return fail(NVFP4_ERR_INVALID, "bad bias dtype %d", (int)bias_dt);
+  if (ldd < N || (residual && ldr < N) || (preact && ldp < N))
+    return fail(NVFP4_ERR_INVALID, "a row stride (ldd %lld, ldr %lld, ldp %lld) is below N (%lld)", (long long)ldd,
+                (long long)ldr, (long long)ldp, (long long)N);
+  if (!aligned(D, 2) || !aligned(residual, 2) || !aligned(preact, 2) ||
+      !aligned(bias, bias_dt == NVFP4_IN_FP32 ? 4 : 2) || !aligned(amax_out, 4))
+    return fail(NVFP4_ERR_INVALID, "a buffer is not aligned to its element size");
+  const size_t need = nvfp4_workspace_size(NVFP4_OP_GEMM_ACT, A->rows, N, 1);
+  if (need && (!workspace || ws_bytes < need || !aligned(workspace, kWsAlign)))
+    return fail(NVFP4_ERR_WORKSPACE, "workspace of %zu bytes (256-byte aligned) required, got %zu", need, workspace ? ws_bytes : (size_t)0);
+  const nvfp4::GemmOperand a{A->codes, A->scales, A->global_scale};
+  const nvfp4::GemmOperand b{B->codes, B->scales, B->global_scale};
+  const nvfp4::ActOut out{bias, residual, preact, ldr, ldp, bias_dt == NVFP4_IN_FP32, false};
+  return hip_status(nvfp4::launch_gemm_act(a, b, A->rows, N, A->cols, (int)act, out, D, ldd, amax_out,
+                                           static_cast<float*>(workspace), (hipStream_t)hip_stream), "gemm_act");
+}
+
+int nvfp4_act_grad(const void* dy, nvfp4_dtype dt, int64_t M, int64_t N, int64_t ldy, const uint16_t* z,
+                   int64_t ldz, nvfp4_act act, uint16_t* dz, int64_t lddz, float* dbias, int accumulate,
+                   void* workspace, size_t ws_bytes, void* hip_stream) {
+  int st;
+  if (dt != NVFP4_IN_BF16 && dt != NVFP4_IN_FP32) return fail(NVFP4_ERR_INVALID, "bad dtype %d", (int)dt);
+  if (M < 0 || N < 0) return fail(NVFP4_ERR_INVALID, "bad shape [%lld, %lld]", (long long)M, (long long)N);
+  if ((st = check_act(act))) return st;
+  if (!dz && !dbias) return fail(NVFP4_ERR_INVALID, "neither dz nor dbias given");
+  if (act == NVFP4_ACT_NONE) z = nullptr;                    // not read
+  if (M > 0 && N > 0) {
+    if (!dy) return fail(NVFP4_ERR_INVALID, "dy is NULL");
+    if (act != NVFP4_ACT_NONE && !z) return fail(NVFP4_ERR_INVALID, "z is NULL");
+  }
+  if (ldy < N || (z && ldz < N) || (dz && lddz < N))
+    return fail(NVFP4_ERR_INVALID, "a row stride (ldy %lld, ldz %lld, lddz %lld) is below N (%lld)", (long long)ldy,
+                (long long)ldz, (long long)lddz, (long long)N);
+  if (!aligned(dy, dt == NVFP4_IN_FP32 ? 4 : 2) || !aligned(z, 2) || !aligned(dz, 2) || !aligned(dbias, 4))
+    return fail(NVFP4_ERR_INVALID, "a buffer is not aligned to its element size");
+  const size_t need = dbias ? nvfp4_workspace_size(NVFP4_OP_ACT_GRAD, M, N, 1) : 0;
+  if (need && (!workspace || ws_bytes < need || !aligned(workspace, kWsAlign)))
+    return fail(NVFP4_ERR_WORKSPACE, "workspace of %zu bytes (256-byte aligned) required, got %zu", need, workspace ? ws_bytes : (size_t)0);
+  return hip_status(nvfp4::launch_act_grad(dy, dt == NVFP4_IN_FP32, ldy, z, ldz, (int)act, dz, lddz, dbias,
+                                           accumulate != 0, M, N, static_cast<float*>(workspace),
+                                           (hipStream_t)hip_stream), "act_grad");
 }
 
 int nvfp4_grouped_gemm(int64_t G, const int64_t* m_offsets, const nvfp4_tensor* A,

@@ -32,7 +32,7 @@
 //    operands loaded straight into registers one K step ahead.
 // In both, scale bytes at or past K are forced to 0, which zeroes whatever codes sit in a
 // partial last step.
-#include "device_common.h"
+#include "activation.h"
 #include "launch.h"
 
 namespace nvfp4 {
@@ -269,13 +269,16 @@ struct Operand {
 // `amax` (the tensor amax the next quantization of D needs, so that quantization is one pass).
 // artiverse.ca "NVIDIA's 4-bit floating point pushes AI training limits": only the GEMMs run
 // in 4-bit, the layer's other tensors in higher precision.
-enum OutKind : int { kOutF32 = 0, kOutF32Add = 1, kOutBF16 = 2 };
+// kOutAct + ActKind: nvfp4_gemm_act, the BF16 output act(z + bias) + residual of ActOut.
+enum OutKind : int { kOutF32 = 0, kOutF32Add = 1, kOutBF16 = 2, kOutAct = 8 };
+constexpr bool is_act(int kind) { return kind >= kOutAct; }
 
 struct ExtOut {
   void* d;          // output, row stride ldd elements
   int64_t ldd;
   float* part;      // a K-split tile's partial sums (tile-local, FP32), else null
   float* amax;      // device float or null
+  ActOut act;       // KIND >= kOutAct
 };
 
 // The tile a persistent workgroup computes next (same operands and tile shape): its first
@@ -292,6 +295,56 @@ __device__ __forceinline__ uint32_t bf16_rn_pair(float v, float w) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f32{v, w}, bf16x2));
 }
 __device__ __forceinline__ uint32_t bf16_rn_bits(float v) { return bf16_rn_pair(v, 0.0f) & 0xFFFFu; }
+
+// ---- nvfp4_gemm_act's output -------------------------------------------------------------
+// z = product + bias (FP32); the pre-activation BF16(z) where asked for; d = BF16(act(z) +
+// residual). act takes the unrounded z.
+__device__ __forceinline__ float bias_at(const ActOut& o, int64_t col) {
+  if (o.bias == nullptr) return 0.0f;
+  return o.bias_f32 ? static_cast<const float*>(o.bias)[col] : bf16_lo(static_cast<const uint16_t*>(o.bias)[col]);
+}
+
+// Element (row, col); returns |stored d|.
+template <int ACT>
+__device__ __forceinline__ float put_act(const ActOut& o, uint16_t* d, int64_t ldd, int64_t row, int64_t col, float v) {
+  const float z = v + bias_at(o, col);
+  if (o.preact != nullptr) o.preact[row * o.ldp + col] = (uint16_t)bf16_rn_bits(z);
+  float y = act<ACT>(z);
+  if (o.residual != nullptr) y += bf16_lo(o.residual[row * o.ldr + col]);
+  const uint32_t b = bf16_rn_bits(y);
+  d[row * ldd + col] = (uint16_t)b;
+  return fabsf(__uint_as_float(b << 16));
+}
+
+// Eight consecutive elements of a row, every array moved as one 16-byte vector.
+template <int ACT>
+__device__ __forceinline__ float put_act8(const ActOut& o, uint16_t* d, int64_t ldd, int64_t row, int64_t col,
+                                          const float (&v)[8], const float (&bias)[8]) {
+  float z[8], y[8];
+  v4u32 res = {0, 0, 0, 0};
+  if (o.residual != nullptr) res = ld_u32x4(o.residual + row * o.ldr + col);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    z[q] = v[q] + bias[q];
+    y[q] = act<ACT>(z[q]);
+  }
+  if (o.preact != nullptr)
+    *reinterpret_cast<v4u32*>(o.preact + row * o.ldp + col) =
+        v4u32{bf16_rn_pair(z[0], z[1]), bf16_rn_pair(z[2], z[3]), bf16_rn_pair(z[4], z[5]), bf16_rn_pair(z[6], z[7])};
+  v4u32 w;
+  float mx = 0.0f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (o.residual != nullptr) {
+      y[2 * q] += bf16_lo(res[q]);
+      y[2 * q + 1] += bf16_hi(res[q]);
+    }
+    w[q] = bf16_rn_pair(y[2 * q], y[2 * q + 1]);
+    mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[q])), fabsf(bf16_hi(w[q]))));
+  }
+  *reinterpret_cast<v4u32*>(d + row * ldd + col) = w;
+  return mx;
+}
 
 // Stores v as output element (row, col); returns |stored value|.
 template <int KIND>
@@ -383,7 +436,7 @@ __device__ __forceinline__ void gemm_tile_big(Operand A, Operand B, int64_t m0, 
                                               int64_t n0, int64_t n1, int64_t K, int64_t k_begin,
                                               int64_t k_end, bool accumulate, float alpha,
                                               float* __restrict__ D, int64_t ldd, uint8_t* lds,
-                                              const ExtOut ext = ExtOut{nullptr, 0, nullptr, nullptr},
+                                              const ExtOut ext = ExtOut{nullptr, 0, nullptr, nullptr, {}},
                                               const TileNext nx = TileNext{false, 0, 0, 0, 0},
                                               bool prefetched = false) {
   using big::kFragBytes;
@@ -640,6 +693,60 @@ __device__ __forceinline__ void gemm_tile_big(Operand A, Operand B, int64_t m0, 
   // D fragment layout (32 x 32): lane l holds column l % 32 and, for q = 0..15, row
   // 8*(q/4) + 4*(l/32) + q%4.
   float mx = 0.0f;
+  if constexpr (EXT && is_act(KIND)) {
+    if (!accumulate) {
+      // Each wave passes its tile through LDS 32 rows at a time, so that the residual's loads and
+      // the stores of D and the pre-activation are 16 bytes a lane along the rows (a fragment
+      // alone gives 2-byte accesses, three streams of them). The stage buffers are free once every
+      // wave has done its LDS reads; a wave's area is its own from there on. Row pitch 8 floats
+      // past the tile: 4 rows (the two lane halves' distance) are 32 banks apart.
+      constexpr int kPitch = kWaveN + 8;
+      static_assert(4 * 32 * kPitch * 4 <= big::kLdsBytes, "LDS of the output pass");
+      __builtin_amdgcn_s_waitcnt(big::waitcnt_imm(0, 0));
+      barrier();
+      float* own = reinterpret_cast<float*>(lds) + wave * 32 * kPitch;
+      uint16_t* d = static_cast<uint16_t*>(ext.d);
+      const int64_t col0 = n0 + wn * kWaveN;
+      constexpr int kLanes = kWaveN / 8;                       // lanes along a row, 8 columns each
+      const int cl = lane % kLanes * 8, rl = lane / kLanes;
+      // 8 columns at a time where every array allows it and the tile's last 8 are whole
+      const bool vec = ext.act.vec && (n1 - n0) % 8 == 0;
+      float bias[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) bias[q] = vec && col0 + cl + q < n1 ? bias_at(ext.act, col0 + cl + q) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kFragsM; ++i) {
+#pragma unroll
+        for (int j = 0; j < kFragsN; ++j)
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            own[(8 * (q >> 2) + 4 * h + (q & 3)) * kPitch + 32 * j + r] = acc[i][j][q] * alpha;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the wave's LDS writes before its reads
+        const int64_t row0 = m0 + wm * kWaveM + 32 * i;
+        if (vec) {
+#pragma unroll 2
+          for (int rr = rl; rr < 32; rr += 64 / kLanes) {
+            if (row0 + rr < m1 && col0 + cl < n1) {
+              float v[8];
+#pragma unroll
+              for (int q = 0; q < 8; ++q) v[q] = own[rr * kPitch + cl + q];
+              mx = fmaxf(mx, put_act8<KIND - kOutAct>(ext.act, d, ext.ldd, row0 + rr, col0 + cl, v, bias));
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int e = lane; e < 32 * kWaveN; e += 64) {
+            const int rr = e / kWaveN, cc = e % kWaveN;
+            if (row0 + rr < m1 && col0 + cc < n1)
+              mx = fmaxf(mx, put_act<KIND - kOutAct>(ext.act, d, ext.ldd, row0 + rr, col0 + cc, own[rr * kPitch + cc]));
+          }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      }
+      if (ext.amax != nullptr) group_amax(mx, ext.amax);
+      return;
+    }
+  }
   // Plain FP32 and BF16 outputs, and FP32 D += tile without an amax output (not a K-split
   // tile's partial sums), go through a buffer resource from the tile's corner to its last
   // element in the output (row m1 - 1, column n1 - 1): stores and atomics to rows past m1 fall
@@ -654,7 +761,7 @@ __device__ __forceinline__ void gemm_tile_big(Operand A, Operand B, int64_t m0, 
     // (D += tile without an amax output adds by float atomics, fire and forget; the FP32
     // outputs with an amax keep the path further below: with this one their kernels spill
     // registers, holding the loaded old values)
-    constexpr bool kFast = !EXT || KIND == kOutBF16 || KIND == kOutF32Add;
+    constexpr bool kFast = !EXT || KIND == kOutBF16 || KIND == kOutF32Add;   // (kOutAct: above)
     const int64_t ldo = EXT ? ext.ldd : ldd;
     const bool no_amax_add = !(EXT && KIND == kOutF32Add) || ext.amax == nullptr;
     if (kFast && !accumulate && no_amax_add && ldo <= (int64_t(1) << 20)) {
@@ -816,7 +923,7 @@ __device__ __forceinline__ void gemm_tile_big(Operand A, Operand B, int64_t m0, 
             else __builtin_nontemporal_store(v, &D[row * ldd + col]);
           } else if (accumulate) {
             __builtin_nontemporal_store(v, &ext.part[(row - m0) * C::kBlockN + (col - n0)]);
-          } else {
+          } else if constexpr (!is_act(KIND)) {
             mx = fmaxf(mx, put_out<KIND>(ext.d, ext.ldd, row, col, v));
           }
         }
@@ -921,7 +1028,7 @@ template <int KIND>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void k_gemm_big_ext(Operand A, const float* __restrict__ ag, Operand B, const float* __restrict__ bg,
                     int64_t K, void* D, int64_t ldd, float* amax, float* part, int64_t tail_first,
-                    int splits) {
+                    int splits, ActOut act) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds_dyn[];
   using namespace big;
   const int64_t tiles_m = (A.rows + kBlockM - 1) / kBlockM;
@@ -937,7 +1044,7 @@ void k_gemm_big_ext(Operand A, const float* __restrict__ ag, Operand B, const fl
     if (n0 >= B.rows) return;                        // a narrower last column tile
     const int64_t m1 = m0 + kBlockM < A.rows ? m0 + kBlockM : A.rows;
     const int64_t n1 = n0 + NTail::kBlockN < B.rows ? n0 + NTail::kBlockN : B.rows;
-    const ExtOut ext{D, ldd, nullptr, amax};
+    const ExtOut ext{D, ldd, nullptr, amax, act};
     gemm_tile_big<NTail, false, KIND, true>(A, B, m0, m1, n0, n1, K, 0, K, false, ag[0] * bg[0], nullptr,
                                             ldd, lds_dyn, ext);
     return;
@@ -957,7 +1064,7 @@ void k_gemm_big_ext(Operand A, const float* __restrict__ ag, Operand B, const fl
   const int64_t n1 = n0 + kBlockN < B.rows ? n0 + kBlockN : B.rows;
   const int64_t k_end = s1 * kStepK < K ? s1 * kStepK : K;
   const ExtOut ext{D, ldd, split ? part + (blockIdx.x - tail_first) * (int64_t)(kBlockM * kBlockN) : nullptr,
-                   amax};
+                   amax, act};
   gemm_tile_big<Full, false, KIND, true>(A, B, m0, m1, n0, n1, K, s0 * kStepK, k_end, split,
                                          ag[0] * bg[0], nullptr, ldd, lds_dyn, ext);
 }
@@ -968,7 +1075,7 @@ void k_gemm_big_ext(Operand A, const float* __restrict__ ag, Operand B, const fl
 template <int KIND>
 __global__ __launch_bounds__(kThreads) void k_split_fixup(int64_t M, int64_t N, void* D, int64_t ldd,
                                                           const float* __restrict__ part,
-                                                          int64_t tail_first, float* amax) {
+                                                          int64_t tail_first, float* amax, ActOut act) {
   using namespace big;
   constexpr int64_t kTile = (int64_t)kBlockM * kBlockN;
   const int64_t tiles_m = (M + kBlockM - 1) / kBlockM;
@@ -992,7 +1099,10 @@ __global__ __launch_bounds__(kThreads) void k_split_fixup(int64_t M, int64_t N, 
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int64_t col = tn * kBlockN + c4 + q;
-      if (col < N) mx = fmaxf(mx, put_out<KIND>(D, ldd, row, col, v[q]));
+      if (col < N) {
+        if constexpr (is_act(KIND)) mx = fmaxf(mx, put_act<KIND - kOutAct>(act, static_cast<uint16_t*>(D), ldd, row, col, v[q]));
+        else mx = fmaxf(mx, put_out<KIND>(D, ldd, row, col, v[q]));
+      }
     }
   }
   if (amax != nullptr) group_amax(mx, amax);
@@ -1095,7 +1205,7 @@ void k_grouped_gemm_k_big(int64_t G, const int64_t* __restrict__ koff, Operand A
     }
     const float alpha = ag[t.g] * bg[t.g];
     float* Dg = D + t.g * A.rows * ldd;
-    const ExtOut none{nullptr, 0, nullptr, nullptr};
+    const ExtOut none{nullptr, 0, nullptr, nullptr, {}};
     if (t.shape == 2)
       gemm_tile_big<MTail, true>(A, B, t.m0, t.m1, t.n0, t.n1, K, t.k0, t.k1, false, alpha, Dg, ldd, lds_dyn,
                                  none, nx, prefetched);
@@ -1146,7 +1256,7 @@ template <int KIND = kOutF32, bool EXT = false>
 __device__ __forceinline__ void gemm_tile_small(Operand A, Operand B, int64_t m0, int64_t m1,
                                                 int64_t n0, int64_t n1, int64_t K, float alpha,
                                                 float* __restrict__ D, int64_t ldd,
-                                                const ExtOut ext = ExtOut{nullptr, 0, nullptr, nullptr}) {
+                                                const ExtOut ext = ExtOut{nullptr, 0, nullptr, nullptr, {}}) {
   using namespace small;
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
@@ -1217,7 +1327,9 @@ __device__ __forceinline__ void gemm_tile_small(Operand A, Operand B, int64_t m0
       for (int q = 0; q < 4; ++q) {
         const int64_t row = wm0 + 16 * i + 4 * g + q;
         if (row < m1) {
-          if constexpr (EXT) mx = fmaxf(mx, put_out<KIND>(ext.d, ext.ldd, row, col, acc[i][j][q] * alpha));
+          if constexpr (EXT && is_act(KIND))
+            mx = fmaxf(mx, put_act<KIND - kOutAct>(ext.act, static_cast<uint16_t*>(ext.d), ext.ldd, row, col, acc[i][j][q] * alpha));
+          else if constexpr (EXT) mx = fmaxf(mx, put_out<KIND>(ext.d, ext.ldd, row, col, acc[i][j][q] * alpha));
           else D[row * ldd + col] = acc[i][j][q] * alpha;
         }
       }
@@ -1245,7 +1357,7 @@ void k_gemm_small(Operand A, const float* __restrict__ ag, Operand B, const floa
 template <int KIND>
 __global__ __launch_bounds__(kThreads)
 void k_gemm_small_ext(Operand A, const float* __restrict__ ag, Operand B, const float* __restrict__ bg,
-                      int64_t K, void* D, int64_t ldd, float* amax) {
+                      int64_t K, void* D, int64_t ldd, float* amax, ActOut act) {
   using namespace small;
   const int64_t tiles_m = (A.rows + kBlockM - 1) / kBlockM;
   const int64_t tiles_n = (B.rows + kBlockN - 1) / kBlockN;
@@ -1255,7 +1367,7 @@ void k_gemm_small_ext(Operand A, const float* __restrict__ ag, Operand B, const 
   const int64_t m1 = m0 + kBlockM < A.rows ? m0 + kBlockM : A.rows;
   const int64_t n1 = n0 + kBlockN < B.rows ? n0 + kBlockN : B.rows;
   gemm_tile_small<KIND, true>(A, B, m0, m1, n0, n1, K, ag[0] * bg[0], nullptr, ldd,
-                              ExtOut{D, ldd, nullptr, amax});
+                              ExtOut{D, ldd, nullptr, amax, act});
 }
 
 __global__ __launch_bounds__(kThreads)
@@ -1515,7 +1627,10 @@ hipError_t enable_big_lds() {
                                        hipFuncAttributeMaxDynamicSharedMemorySize, big::kLdsBytes);
     if (e != hipSuccess) return e;
     for (const void* f : {(const void*)k_gemm_big_ext<kOutF32>, (const void*)k_gemm_big_ext<kOutF32Add>,
-                          (const void*)k_gemm_big_ext<kOutBF16>}) {
+                          (const void*)k_gemm_big_ext<kOutBF16>, (const void*)k_gemm_big_ext<kOutAct + kActNone>,
+                          (const void*)k_gemm_big_ext<kOutAct + kActRelu2>,
+                          (const void*)k_gemm_big_ext<kOutAct + kActGelu>,
+                          (const void*)k_gemm_big_ext<kOutAct + kActSilu>}) {
       e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, big::kLdsBytes);
       if (e != hipSuccess) return e;
     }
@@ -1609,40 +1724,59 @@ size_t gemm_ex_workspace_bytes(int64_t M, int64_t N) {
   return (size_t)(tiles - tail_first) * (size_t)splits * big::kBlockM * big::kBlockN * sizeof(float);
 }
 
-hipError_t launch_gemm_ex(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int kind,
-                          void* D, int64_t ldd, float* amax, float* ws, hipStream_t stream) {
-  if (amax) {
-    const hipError_t e = launch_fill(amax, 1, 0.0f, stream);
-    if (e != hipSuccess) return e;
-  }
-  if (M == 0 || N == 0) return hipGetLastError();
-  const Operand A{a.codes, a.scales, M}, B{b.codes, b.scales, N};
+template <int KIND>
+void launch_ext(const Operand& A, const float* ag, const Operand& B, const float* bg, int64_t K, void* D,
+                int64_t ldd, float* amax, float* ws, const ActOut& act, hipStream_t stream) {
+  const int64_t M = A.rows, N = B.rows;
   if (use_big(K)) {
-    const hipError_t e = enable_big_lds();
-    if (e != hipSuccess) return e;
     const int64_t tiles = big_tiles(M, N);
     int64_t tail_first, splits;
     split_plan(tiles, K, tail_first, splits);
     const int64_t grid = tail_first + (tiles - tail_first) * (splits < 0 ? 4 : splits);
-#define NVFP4_GX(KD)                                                                                  \
-  hipLaunchKernelGGL(k_gemm_big_ext<KD>, dim3((unsigned)grid), dim3(kThreads), big::kLdsBytes, stream, \
-                     A, a.global_scale, B, b.global_scale, K, D, ldd, amax, ws, tail_first, (int)splits); \
-  if (tail_first < tiles && splits > 0)                                                               \
-    hipLaunchKernelGGL(k_split_fixup<KD>, dim3((unsigned)((tiles - tail_first) * kZeroParts)),         \
-                       dim3(kThreads), 0, stream, M, N, D, ldd, ws, tail_first, amax)
-    if (kind == kOutBF16) { NVFP4_GX(kOutBF16); }
-    else if (kind == kOutF32Add) { NVFP4_GX(kOutF32Add); }
-    else { NVFP4_GX(kOutF32); }
-#undef NVFP4_GX
+    hipLaunchKernelGGL(k_gemm_big_ext<KIND>, dim3((unsigned)grid), dim3(kThreads), big::kLdsBytes, stream, A, ag, B,
+                       bg, K, D, ldd, amax, ws, tail_first, (int)splits, act);
+    if (tail_first < tiles && splits > 0)
+      hipLaunchKernelGGL(k_split_fixup<KIND>, dim3((unsigned)((tiles - tail_first) * kZeroParts)), dim3(kThreads), 0,
+                         stream, M, N, D, ldd, ws, tail_first, amax, act);
   } else {
     const int64_t tiles = ((M + small::kBlockM - 1) / small::kBlockM) * ((N + small::kBlockN - 1) / small::kBlockN);
-#define NVFP4_GS(KD) hipLaunchKernelGGL(k_gemm_small_ext<KD>, dim3((unsigned)tiles), dim3(kThreads), 0, stream, \
-                                        A, a.global_scale, B, b.global_scale, K, D, ldd, amax)
-    if (kind == kOutBF16) NVFP4_GS(kOutBF16);
-    else if (kind == kOutF32Add) NVFP4_GS(kOutF32Add);
-    else NVFP4_GS(kOutF32);
-#undef NVFP4_GS
+    hipLaunchKernelGGL(k_gemm_small_ext<KIND>, dim3((unsigned)tiles), dim3(kThreads), 0, stream, A, ag, B, bg, K, D,
+                       ldd, amax, act);
   }
+}
+
+hipError_t launch_gemm_ex(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int kind,
+                          void* D, int64_t ldd, float* amax, float* ws, hipStream_t stream) {
+  hipError_t e = amax ? launch_fill(amax, 1, 0.0f, stream) : hipSuccess;
+  if (e != hipSuccess) return e;
+  if (M == 0 || N == 0) return hipGetLastError();
+  if (use_big(K) && (e = enable_big_lds()) != hipSuccess) return e;
+  const Operand A{a.codes, a.scales, M}, B{b.codes, b.scales, N};
+  const ActOut none{};
+  if (kind == kOutBF16) launch_ext<kOutBF16>(A, a.global_scale, B, b.global_scale, K, D, ldd, amax, ws, none, stream);
+  else if (kind == kOutF32Add) launch_ext<kOutF32Add>(A, a.global_scale, B, b.global_scale, K, D, ldd, amax, ws, none, stream);
+  else launch_ext<kOutF32>(A, a.global_scale, B, b.global_scale, K, D, ldd, amax, ws, none, stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_gemm_act(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int act_kind, ActOut act,
+                           uint16_t* D, int64_t ldd, float* amax, float* ws, hipStream_t stream) {
+  hipError_t e = amax ? launch_fill(amax, 1, 0.0f, stream) : hipSuccess;
+  if (e != hipSuccess) return e;
+  if (M == 0 || N == 0) return hipGetLastError();
+  if (use_big(K) && (e = enable_big_lds()) != hipSuccess) return e;
+  const Operand A{a.codes, a.scales, M}, B{b.codes, b.scales, N};
+  auto ok = [](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; };
+  act.vec = ok(D, ldd) && ok(act.residual, act.residual ? act.ldr : 0) && ok(act.preact, act.preact ? act.ldp : 0);
+#define NVFP4_GA(KD) \
+  launch_ext<kOutAct + KD>(A, a.global_scale, B, b.global_scale, K, D, ldd, amax, ws, act, stream)
+  switch (act_kind) {
+    case kActRelu2: NVFP4_GA(kActRelu2); break;
+    case kActGelu: NVFP4_GA(kActGelu); break;
+    case kActSilu: NVFP4_GA(kActSilu); break;
+    default: NVFP4_GA(kActNone); break;
+  }
+#undef NVFP4_GA
   return hipGetLastError();
 }
 

@@ -122,6 +122,25 @@ size_t gemm_ex_workspace_bytes(int64_t M, int64_t N);
 hipError_t launch_gemm_ex(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int kind,
                           void* D, int64_t ldd, float* amax, float* ws, hipStream_t stream);
 
+// D = BF16(act(A B^T + bias) + residual), act_kind an ActKind; preact (optional) gets BF16(A B^T +
+// bias). ws as launch_gemm_ex. vec is set by the launcher.
+struct ActOut {
+  const void* bias;             // BF16 or FP32 [N], or null
+  const uint16_t* residual;     // BF16 [M, N], row stride ldr, or null
+  uint16_t* preact;             // BF16 [M, N], row stride ldp, or null
+  int64_t ldr, ldp;
+  bool bias_f32, vec;
+};
+hipError_t launch_gemm_act(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int act_kind, ActOut act,
+                           uint16_t* D, int64_t ldd, float* amax, float* ws, hipStream_t stream);
+
+// dz = BF16(dy act'(z)) (or null), dbias (FP32 [N], or null) = or += its column sums; ws holds
+// act_grad_workspace_bytes(M, N) bytes where dbias is asked for.
+size_t act_grad_workspace_bytes(int64_t M, int64_t N);
+hipError_t launch_act_grad(const void* dy, bool fp32, int64_t ldy, const uint16_t* z, int64_t ldz, int act,
+                           uint16_t* dz, int64_t lddz, float* dbias, bool accumulate, int64_t M, int64_t N,
+                           float* ws, hipStream_t stream);
+
 hipError_t launch_grouped_gemm(int64_t G, const int64_t* m_offsets, GemmOperand a, GemmOperand b,
                                int64_t total_m, int64_t N, int64_t K, float* D, int64_t ldd,
                                hipStream_t stream);

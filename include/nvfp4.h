@@ -61,7 +61,8 @@ typedef enum { NVFP4_BLOCK_1X16 = 0, NVFP4_BLOCK_16X16 = 1 } nvfp4_block;
 typedef enum { NVFP4_ROUND_RN = 0, NVFP4_ROUND_SR = 1 } nvfp4_round;
 typedef enum {
   NVFP4_OP_QUANTIZE = 0, NVFP4_OP_RHT_QUANTIZE = 1, NVFP4_OP_GEMM = 2,
-  NVFP4_OP_GROUPED_GEMM = 3, NVFP4_OP_AMAX_PAIR = 4, NVFP4_OP_GEMM_EX = 5, NVFP4_OP_ADAMW = 6
+  NVFP4_OP_GROUPED_GEMM = 3, NVFP4_OP_AMAX_PAIR = 4, NVFP4_OP_GEMM_EX = 5, NVFP4_OP_ADAMW = 6,
+  NVFP4_OP_GEMM_ACT = 7, NVFP4_OP_ACT_GRAD = 8
 } nvfp4_op;
 /* Output of nvfp4_gemm_ex: FP32, FP32 added to what D holds, or BF16. */
 typedef enum { NVFP4_OUT_FP32 = 0, NVFP4_OUT_FP32_ACCUMULATE = 1, NVFP4_OUT_BF16 = 2 } nvfp4_out;
@@ -293,6 +294,56 @@ int nvfp4_gemm(const nvfp4_tensor* A, const nvfp4_tensor* B, float* D, int64_t l
  */
 int nvfp4_gemm_ex(const nvfp4_tensor* A, const nvfp4_tensor* B, void* D, int64_t ldd, nvfp4_out out_kind,
                   float* amax_out, void* workspace, size_t ws_bytes, void* hip_stream);
+
+/* Element functions of nvfp4_gemm_act and nvfp4_act_grad. RELU2 max(z, 0)^2; GELU in its tanh
+ * form, z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))); SILU z / (1 + exp(-z)). */
+typedef enum { NVFP4_ACT_NONE = 0, NVFP4_ACT_RELU2 = 1, NVFP4_ACT_GELU = 2, NVFP4_ACT_SILU = 3 } nvfp4_act;
+
+/*
+ * nvfp4_gemm_act - a linear layer's forward product with what follows it, in the GEMM's epilogue
+ * (artiverse.ca "NVIDIA's 4-bit floating point pushes AI training limits", paragraph on which
+ * parts run in 4-bit: the GEMM takes NVFP4 operands; bias, activation and residual stay in higher
+ * precision):
+ *   Z = s_A s_B A B^T + bias (FP32);   D = BF16(act(Z) + residual)
+ *   A, B       as nvfp4_gemm (rows M and N, same K, % 16 == 0). M may be a whole batch or the few
+ *              rows of a generation step.
+ *   D          device BF16 bits [M, N], row stride ldd >= N.
+ *   bias       NULL, or device BF16 or FP32 (bias_dt) [N].
+ *   residual   NULL, or device BF16 [M, N], row stride ldr >= N; may be D itself (same stride).
+ *   preact     NULL, or device BF16 [M, N], row stride ldp >= N, receiving BF16(Z): what
+ *              nvfp4_act_grad needs. Overlaps no other argument.
+ *   amax_out   NULL, or device float[1] receiving max|D| over the values as stored (the amax_in of
+ *              D's next quantization). The library clears it.
+ *   workspace  nvfp4_workspace_size(NVFP4_OP_GEMM_ACT, M, N, 1) bytes, 256-byte aligned (NULL
+ *              allowed for 0 bytes).
+ * The result is deterministic for a given device. Errors: NVFP4_ERR_INVALID (null pointers, K
+ * mismatch, K % 16, a stride below N, bad enum, misaligned buffers), NVFP4_ERR_UNSUPPORTED
+ * (operand size), NVFP4_ERR_WORKSPACE, NVFP4_ERR_HIP.
+ */
+int nvfp4_gemm_act(const nvfp4_tensor* A, const nvfp4_tensor* B, uint16_t* D, int64_t ldd, const void* bias,
+                   nvfp4_dtype bias_dt, nvfp4_act act, const uint16_t* residual, int64_t ldr, uint16_t* preact,
+                   int64_t ldp, float* amax_out, void* workspace, size_t ws_bytes, void* hip_stream);
+
+/*
+ * nvfp4_act_grad - the backward of nvfp4_gemm_act's bias and activation (artiverse.ca "NVIDIA's
+ * 4-bit floating point pushes AI training limits", as above) from one read of the gradient; the
+ * residual's gradient is dY itself, and dZ feeds the two gradient GEMMs:
+ *   dZ = BF16(dY * act'(Z));   dbias[n] = sum over m of dY * act'(Z)   (FP32, before the rounding)
+ *   dy         device BF16 or FP32 (dt) [M, N], row stride ldy >= N.
+ *   z          the forward's preact, device BF16 [M, N], row stride ldz >= N; NULL with
+ *              NVFP4_ACT_NONE.
+ *   dz         NULL (the bias gradient alone), or device BF16 [M, N], row stride lddz >= N,
+ *              overlapping no input.
+ *   dbias      NULL, or device float[N]: overwritten, or with accumulate != 0 added to (one FP32
+ *              addition per element). The sums run in a fixed order.
+ *   workspace  nvfp4_workspace_size(NVFP4_OP_ACT_GRAD, M, N, 1) bytes, 256-byte aligned; may be
+ *              NULL without dbias.
+ * Errors: NVFP4_ERR_INVALID (null pointers, shapes, strides, enums, misaligned buffers, neither dz
+ * nor dbias), NVFP4_ERR_WORKSPACE, NVFP4_ERR_HIP.
+ */
+int nvfp4_act_grad(const void* dy, nvfp4_dtype dt, int64_t M, int64_t N, int64_t ldy, const uint16_t* z,
+                   int64_t ldz, nvfp4_act act, uint16_t* dz, int64_t lddz, float* dbias, int accumulate,
+                   void* workspace, size_t ws_bytes, void* hip_stream);
 
 /*
  * nvfp4_grouped_gemm - one GEMM per group (mixture-of-experts expert GEMMs; "Nemotron

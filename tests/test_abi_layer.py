@@ -74,3 +74,58 @@ def test_adamw_validation(lib):
     assert call(ws=None) == WORKSPACE
     assert call(ws_n=100) == WORKSPACE
     assert lib.nvfp4_adamw(FAKE, 1, 1, 0, None, None, None, None, 0, None) == INVALID
+
+
+def _t(rows, cols):
+    return ctypes.byref(nv._CTensor(FAKE, FAKE, FAKE, rows, cols))
+
+
+def test_gemm_act_validation(lib):
+    def call(A=_t(64, 128), B=_t(32, 128), D=FAKE, ldd=32, bias=None, bdt=0, act=0, res=None, ldr=0, pre=None, ldp=0,
+             amax=None, ws=None, ws_n=0):
+        return lib.nvfp4_gemm_act(A, B, D, ldd, bias, bdt, act, res, ldr, pre, ldp, amax, ws, ws_n, None)
+
+    assert call(A=None) == INVALID
+    assert call(B=_t(32, 96)) == INVALID
+    assert call(A=_t(64, 100), B=_t(32, 100)) == INVALID
+    assert call(D=None) == INVALID
+    assert call(D=FAKE + 1) == INVALID
+    assert call(ldd=31) == INVALID
+    assert call(act=4) == INVALID
+    assert call(act=-1) == INVALID
+    assert call(bias=FAKE, bdt=2) == INVALID
+    assert call(bias=FAKE + 2, bdt=1) == INVALID
+    assert call(res=FAKE, ldr=31) == INVALID
+    assert call(res=FAKE + 1, ldr=32) == INVALID
+    assert call(pre=FAKE, ldp=31) == INVALID
+    assert call(amax=FAKE + 2) == INVALID
+    need = lib.nvfp4_workspace_size(nv.OP_GEMM_ACT, 8192, 5120, 1)
+    assert need > 0
+    big = dict(A=_t(8192, 128), B=_t(5120, 128), ldd=5120)
+    assert call(**big) == WORKSPACE
+    assert call(**big, ws=FAKE, ws_n=need - 1) == WORKSPACE
+    assert call(**big, ws=FAKE + 16, ws_n=need) == WORKSPACE
+    assert call(A=_t(1 << 20, 8192), B=_t(32, 8192)) == UNSUPPORTED
+
+
+def test_act_grad_validation(lib):
+    def call(dy=FAKE, dt=0, M=100, N=32, ldy=32, z=FAKE, ldz=32, act=1, dz=FAKE, lddz=32, dbias=FAKE, acc=0, ws=FAKE,
+             ws_n=1 << 20):
+        return lib.nvfp4_act_grad(dy, dt, M, N, ldy, z, ldz, act, dz, lddz, dbias, acc, ws, ws_n, None)
+
+    assert call(dy=None) == INVALID
+    assert call(z=None) == INVALID
+    assert call(dt=2) == INVALID
+    assert call(act=7) == INVALID
+    assert call(M=-1) == INVALID
+    assert call(ldy=31) == INVALID
+    assert call(ldz=31) == INVALID
+    assert call(lddz=31) == INVALID
+    assert call(dz=None, dbias=None) == INVALID
+    assert call(dy=FAKE + 2, dt=1) == INVALID
+    assert call(dz=FAKE + 1) == INVALID
+    assert call(dbias=FAKE + 2) == INVALID
+    assert call(ws=None, ws_n=0) == WORKSPACE
+    assert call(ws=FAKE + 64) == WORKSPACE
+    assert lib.nvfp4_workspace_size(nv.OP_ACT_GRAD, 8, 32, 1) == 0          # one run of rows: no partial sums
+    assert lib.nvfp4_workspace_size(nv.OP_ACT_GRAD, 100, 32, 1) > 0
