@@ -7,7 +7,7 @@ still succeeds but every call raises, so nothing can silently fall back to anoth
 
 Names follow the C entry points: quantize, quantize_noalloc, rht_quantize, rht_rows_quantize,
 gemm, gemm_ex, grouped_gemm, grouped_gemm_k, amax, amax_pair, mx_quantize, mx_quantize_columns, mx_gemm, dequantize,
-gemm_act, act_grad, adamw.
+gemm_act, act_grad, moe_tokens, adamw.
 """
 from __future__ import annotations
 
@@ -29,6 +29,7 @@ _BLOCK = {"1x16": 0, "16x16": 1}
 _ROUND = {"rn": 0, "sr": 1}
 OP_QUANTIZE, OP_RHT_QUANTIZE, OP_GEMM, OP_GROUPED_GEMM, OP_AMAX_PAIR, OP_GEMM_EX = 0, 1, 2, 3, 4, 5
 OP_ADAMW, OP_GEMM_ACT, OP_ACT_GRAD = 6, 7, 8
+SCORES = {"softmax": 0, "sigmoid": 1}
 ACTIVATIONS = {"none": 0, "relu2": 1, "gelu": 2, "silu": 3}
 OUT_FP32, OUT_FP32_ACCUMULATE, OUT_BF16 = 0, 1, 2
 
@@ -36,7 +37,8 @@ EXPORTED = ("nvfp4_quantize", "nvfp4_quantize_noalloc", "nvfp4_rht_quantize", "n
             "mxfp4_quantize", "mxfp4_quantize_columns", "mxfp4_gemm", "nvfp4_rht_rows_quantize",
             "nvfp4_grouped_gemm_k",
             "nvfp4_amax", "nvfp4_amax_pair", "nvfp4_workspace_size", "nvfp4_last_error",
-            "nvfp4_dequantize", "nvfp4_gemm_act", "nvfp4_act_grad", "nvfp4_adamw", "nvfp4_adamw_table", "nvfp4_adamw_table_size")
+            "nvfp4_dequantize", "nvfp4_gemm_act", "nvfp4_act_grad", "nvfp4_moe_tokens",
+            "nvfp4_moe_workspace_size", "nvfp4_adamw", "nvfp4_adamw_table", "nvfp4_adamw_table_size")
 
 
 class NVFP4Error(RuntimeError):
@@ -52,6 +54,13 @@ class _CTensor(ctypes.Structure):
 class _CMXTensor(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
                 ("cols", ctypes.c_int64)]
+
+
+class _CMoE(ctypes.Structure):
+    _fields_ = [("experts", ctypes.c_int64), ("hidden", ctypes.c_int64), ("ffn", ctypes.c_int64),
+                ("top_k", ctypes.c_int64), ("router", ctypes.c_void_p), ("router_dt", ctypes.c_int),
+                ("w1", _CTensor), ("w2", _CTensor), ("act", ctypes.c_int), ("gated", ctypes.c_int),
+                ("score", ctypes.c_int), ("renormalize", ctypes.c_int), ("routed_scale", ctypes.c_float)]
 
 
 class _CAdamWTensor(ctypes.Structure):
@@ -105,12 +114,15 @@ def _load():
     lib.nvfp4_workspace_size.restype = sz
     lib.nvfp4_last_error.restype = ctypes.c_char_p
     lib.nvfp4_dequantize.argtypes = [pt, vp, i64, vp, vp]
+    lib.nvfp4_moe_tokens.argtypes = [ctypes.POINTER(_CMoE), vp, i64, i64, vp, i64, vp, vp, vp, sz, vp]
+    lib.nvfp4_moe_workspace_size.argtypes = [ctypes.POINTER(_CMoE), i64]
+    lib.nvfp4_moe_workspace_size.restype = sz
     lib.nvfp4_adamw_table_size.argtypes = [ctypes.POINTER(_CAdamWTensor), i64]
     lib.nvfp4_adamw_table_size.restype = sz
     lib.nvfp4_adamw_table.argtypes = [ctypes.POINTER(_CAdamWTensor), i64, ctypes.c_int, vp, sz, ctypes.POINTER(i64)]
     lib.nvfp4_adamw.argtypes = [vp, i64, i64, ctypes.c_int, ctypes.POINTER(_CAdamWHyper), vp, vp, vp, sz, vp]
     for name in EXPORTED:
-        if name not in ("nvfp4_workspace_size", "nvfp4_last_error", "nvfp4_adamw_table_size"):
+        if name not in ("nvfp4_workspace_size", "nvfp4_last_error", "nvfp4_adamw_table_size", "nvfp4_moe_workspace_size"):
             getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -639,6 +651,71 @@ def dequantize(q: NVFP4Tensor, segments: torch.Tensor | None = None, stream=None
     qc = q.c()
     _check(lib.nvfp4_dequantize(ctypes.byref(qc), _ptr(segments), nseg, _ptr(y), _stream(stream)))
     return y
+
+
+@dataclass
+class MoEWeights:
+    """A mixture-of-experts layer's weights and routing rule (nvfp4_moe): router [experts, hidden],
+    bfloat16 or float32; w1 [experts*ffn, hidden] (gated: [experts*2*ffn, hidden], each expert's gate
+    rows before its up rows) and w2 [experts*hidden, ffn] with one global_scale per expert."""
+    router: torch.Tensor
+    w1: NVFP4Tensor
+    w2: NVFP4Tensor
+    top_k: int
+    activation: str = "relu2"
+    gated: bool = False
+    score: str = "softmax"
+    renormalize: bool = True
+    routed_scale: float = 1.0
+
+    def c(self) -> _CMoE:
+        r = self.router
+        if r.dtype not in _DTYPE or r.dim() != 2 or not r.is_contiguous() or r.device.type != "cuda":
+            raise NVFP4Error("router must be a contiguous 2-D bfloat16 or float32 GPU tensor")
+        if self.score not in SCORES:
+            raise NVFP4Error(f"unknown score {self.score!r}: one of {', '.join(SCORES)}")
+        _check_q(self.w1, r.shape[0], "w1")
+        _check_q(self.w2, r.shape[0], "w2")
+        return _CMoE(r.shape[0], r.shape[1], self.w2.cols, self.top_k, r.data_ptr(), _DTYPE[r.dtype], self.w1.c(),
+                     self.w2.c(), _activation(self.activation), int(self.gated), SCORES[self.score],
+                     int(self.renormalize), self.routed_scale)
+
+
+def moe_workspace(weights: MoEWeights, tokens: int) -> torch.Tensor:
+    """A workspace for moe_tokens with up to `tokens` tokens, its counters zero."""
+    n = _load().nvfp4_moe_workspace_size(ctypes.byref(weights.c()), tokens)
+    if n == 0:
+        raise NVFP4Error(f"no expert layer for {tokens} tokens: {_load().nvfp4_last_error().decode()}")
+    return torch.zeros((n,), dtype=torch.uint8, device=weights.router.device)
+
+
+@_on_stream
+def moe_tokens(x: torch.Tensor, weights: MoEWeights, out: torch.Tensor | None = None,
+               ids_out: torch.Tensor | None = None, weights_out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """nvfp4_moe_tokens: the whole expert layer for x [tokens <= 64, hidden] (bfloat16). ids_out
+    (int32) and weights_out (float32), both [tokens, top_k], receive the routing. workspace: one of
+    moe_workspace's, kept between calls (calls that share one have to be ordered)."""
+    lib = _load()
+    if x.dtype != torch.bfloat16:
+        raise NVFP4Error("x must be bfloat16")
+    _, tokens, hidden, _ = _input(x)
+    layer = weights.c()
+    if hidden != layer.hidden:
+        raise NVFP4Error(f"x has {hidden} columns, the layer's hidden size is {layer.hidden}")
+    if out is None:
+        out = torch.empty((tokens, hidden), dtype=torch.bfloat16, device=x.device)
+    _check_out(out, tokens, hidden, torch.bfloat16)
+    for t, dtype, what in ((ids_out, torch.int32, "ids_out"), (weights_out, torch.float32, "weights_out")):
+        if t is not None and (t.dtype != dtype or t.numel() < tokens * weights.top_k or not t.is_contiguous()
+                              or t.device.type != "cuda"):
+            raise NVFP4Error(f"{what} must be a contiguous {dtype} GPU tensor of at least {tokens * weights.top_k} elements")
+    if workspace is None and 0 < tokens:
+        workspace = moe_workspace(weights, tokens)
+    _check(lib.nvfp4_moe_tokens(ctypes.byref(layer), _ptr(x), tokens, _row_stride(x), _ptr(out), _row_stride(out),
+                                _ptr(ids_out), _ptr(weights_out), _ptr(workspace),
+                                0 if workspace is None else workspace.numel(), _stream(stream)))
+    return out
 
 
 @dataclass

@@ -17,11 +17,6 @@ constexpr int kThreads = 256;
 constexpr int kCols = 512;                                    // 64 lanes x 8
 constexpr int kWaves = kThreads / 64;
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f32{a, b}, bf16x2));
-}
-
 // VEC: a lane holds 8 consecutive columns, moved as whole vectors (N, the row strides and the
 // pointers are multiples of 8 elements); otherwise columns lane, lane + 64, ..., one element each.
 template <bool VEC>
@@ -90,12 +85,12 @@ __global__ __launch_bounds__(kThreads) void k_act_grad(const void* __restrict__ 
       if constexpr (VEC) {
         if (c0 + lane * 8 < N)
           *reinterpret_cast<v4u32*>(dz + r * lddz + c0 + lane * 8) =
-              v4u32{bf16_pair(g[0], g[1]), bf16_pair(g[2], g[3]), bf16_pair(g[4], g[5]), bf16_pair(g[6], g[7])};
+              v4u32{bf16_rn_pair(g[0], g[1]), bf16_rn_pair(g[2], g[3]), bf16_rn_pair(g[4], g[5]), bf16_rn_pair(g[6], g[7])};
       } else {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           const int64_t c = col_of<false>(c0, lane, q);
-          if (c < N) dz[r * lddz + c] = (uint16_t)bf16_pair(g[q], 0.0f);
+          if (c < N) dz[r * lddz + c] = (uint16_t)bf16_rn_pair(g[q], 0.0f);
         }
       }
     }

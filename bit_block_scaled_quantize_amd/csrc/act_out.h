@@ -1,0 +1,68 @@
+// The output of nvfp4_gemm_act, shared by its kernels: z = product + bias (FP32); the pre-activation
+// BF16(z) where asked for; d = BF16(act(z) + residual). act takes the unrounded z.
+#pragma once
+
+#include "activation.h"
+#include "launch.h"
+
+namespace nvfp4 {
+
+__device__ __forceinline__ float bias_at(const ActOut& o, int64_t col) {
+  if (o.bias == nullptr) return 0.0f;
+  return o.bias_f32 ? static_cast<const float*>(o.bias)[col] : bf16_lo(static_cast<const uint16_t*>(o.bias)[col]);
+}
+
+// Element (row, col); returns |stored d|.
+template <int ACT>
+__device__ __forceinline__ float put_act(const ActOut& o, uint16_t* d, int64_t ldd, int64_t row, int64_t col, float v) {
+  const float z = v + bias_at(o, col);
+  if (o.preact != nullptr) o.preact[row * o.ldp + col] = (uint16_t)bf16_rn_bits(z);
+  float y = act<ACT>(z);
+  if (o.residual != nullptr) y += bf16_lo(o.residual[row * o.ldr + col]);
+  const uint32_t b = bf16_rn_bits(y);
+  d[row * ldd + col] = (uint16_t)b;
+  return fabsf(__uint_as_float(b << 16));
+}
+
+// The same with the kind known at run time (uniform).
+__device__ __forceinline__ float put_act_of(int act, const ActOut& o, uint16_t* d, int64_t ldd, int64_t row,
+                                            int64_t col, float v) {
+  switch (act) {
+    case kActRelu2: return put_act<kActRelu2>(o, d, ldd, row, col, v);
+    case kActGelu: return put_act<kActGelu>(o, d, ldd, row, col, v);
+    case kActSilu: return put_act<kActSilu>(o, d, ldd, row, col, v);
+    default: return put_act<kActNone>(o, d, ldd, row, col, v);
+  }
+}
+
+// Eight consecutive elements of a row, every array moved as one 16-byte vector.
+template <int ACT>
+__device__ __forceinline__ float put_act8(const ActOut& o, uint16_t* d, int64_t ldd, int64_t row, int64_t col,
+                                          const float (&v)[8], const float (&bias)[8]) {
+  float z[8], y[8];
+  v4u32 res = {0, 0, 0, 0};
+  if (o.residual != nullptr) res = ld_u32x4(o.residual + row * o.ldr + col);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    z[q] = v[q] + bias[q];
+    y[q] = act<ACT>(z[q]);
+  }
+  if (o.preact != nullptr)
+    *reinterpret_cast<v4u32*>(o.preact + row * o.ldp + col) =
+        v4u32{bf16_rn_pair(z[0], z[1]), bf16_rn_pair(z[2], z[3]), bf16_rn_pair(z[4], z[5]), bf16_rn_pair(z[6], z[7])};
+  v4u32 w;
+  float mx = 0.0f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (o.residual != nullptr) {
+      y[2 * q] += bf16_lo(res[q]);
+      y[2 * q + 1] += bf16_hi(res[q]);
+    }
+    w[q] = bf16_rn_pair(y[2 * q], y[2 * q + 1]);
+    mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[q])), fabsf(bf16_hi(w[q]))));
+  }
+  *reinterpret_cast<v4u32*>(d + row * ldd + col) = w;
+  return mx;
+}
+
+}  // namespace nvfp4

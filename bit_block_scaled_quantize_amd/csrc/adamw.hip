@@ -79,18 +79,13 @@ __device__ __forceinline__ Elems load_grad(const void* p, bool bf16, int64_t i, 
   return e;
 }
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f32{a, b}, bf16x2));
-}
-
 // Stores e rounded to BF16; returns the largest stored magnitude.
 __device__ __forceinline__ float store_bf16(uint16_t* p, int64_t i, int64_t n, bool vec, const Elems& e) {
   v4u32 w;
   float mx = 0.0f;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    w[q] = bf16_pair(e.v[2 * q], e.v[2 * q + 1]);
+    w[q] = bf16_rn_pair(e.v[2 * q], e.v[2 * q + 1]);
     mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[q])), fabsf(bf16_hi(w[q]))));
   }
   if (vec && i + kPer <= n) {

@@ -107,6 +107,40 @@ int check_act(nvfp4_act act) {
   return NVFP4_OK;
 }
 
+// The layer's own description, without its weights' addresses.
+int check_moe_shape(const nvfp4_moe* m) {
+  if (!m) return fail(NVFP4_ERR_INVALID, "moe is NULL");
+  if (m->experts < 1 || m->hidden < 16 || m->hidden % 16 || m->ffn < 16 || m->ffn % 16 || m->top_k < 1 ||
+      m->top_k > m->experts)
+    return fail(NVFP4_ERR_INVALID, "bad expert layer: %lld experts, hidden %lld, ffn %lld, top_k %lld",
+                (long long)m->experts, (long long)m->hidden, (long long)m->ffn, (long long)m->top_k);
+  if (m->experts > nvfp4::kMoeMaxExperts || m->top_k > nvfp4::kMoeMaxTopK)
+    return fail(NVFP4_ERR_UNSUPPORTED, "at most %lld experts and top_k %lld (got %lld, %lld)",
+                (long long)nvfp4::kMoeMaxExperts, (long long)nvfp4::kMoeMaxTopK, (long long)m->experts, (long long)m->top_k);
+  if (m->hidden > (int64_t(1) << 24) || m->ffn > (int64_t(1) << 24))
+    return fail(NVFP4_ERR_UNSUPPORTED, "hidden (%lld) or ffn (%lld) above 2^24", (long long)m->hidden, (long long)m->ffn);
+  return NVFP4_OK;
+}
+
+nvfp4::MoeArgs moe_args(const nvfp4_moe& m, int64_t tokens) {
+  nvfp4::MoeArgs a{};
+  a.hidden = m.hidden;
+  a.ffn = m.ffn;
+  a.router = m.router;
+  a.w1 = nvfp4::GemmOperand{m.w1.codes, m.w1.scales, m.w1.global_scale};
+  a.w2 = nvfp4::GemmOperand{m.w2.codes, m.w2.scales, m.w2.global_scale};
+  a.tokens = (int)tokens;
+  a.experts = (int)m.experts;
+  a.top_k = (int)m.top_k;
+  a.act = (int)m.act;
+  a.routed_scale = m.routed_scale;
+  a.router_f32 = m.router_dt == NVFP4_IN_FP32;
+  a.gated = m.gated != 0;
+  a.sigmoid = m.score == NVFP4_SCORE_SIGMOID;
+  a.renormalize = m.renormalize != 0;
+  return a;
+}
+
 }  // namespace
 
 extern "C" {
@@ -472,6 +506,7 @@ int nvfp4_gemm_act(const nvfp4_tensor* A, const nvfp4_tensor* B, uint16_t* D, in
   if (!aligned(D, 2) || !aligned(residual, 2) || !aligned(preact, 2) ||
       !aligned(bias, bias_dt == NVFP4_IN_FP32 ? 4 : 2) || !aligned(amax_out, 4))
     return fail(NVFP4_ERR_INVALID, "a buffer is not aligned to its element size");
+  if (!aligned(A->scales, 4) || !aligned(B->scales, 4)) return fail(NVFP4_ERR_INVALID, "scales must be 4-byte aligned");
   const size_t need = nvfp4_workspace_size(NVFP4_OP_GEMM_ACT, A->rows, N, 1);
   if (need && (!workspace || ws_bytes < need || !aligned(workspace, kWsAlign)))
     return fail(NVFP4_ERR_WORKSPACE, "workspace of %zu bytes (256-byte aligned) required, got %zu", need, workspace ? ws_bytes : (size_t)0);
@@ -660,6 +695,50 @@ int nvfp4_adamw(const void* table, int64_t count, int64_t chunks, nvfp4_state st
   return hip_status(nvfp4::launch_adamw(table, count, chunks, state == NVFP4_STATE_8BIT, d, clip,
                                         static_cast<double*>(workspace), norm_out, amax_out, (hipStream_t)hip_stream),
                     "adamw");
+}
+
+size_t nvfp4_moe_workspace_size(const nvfp4_moe* moe, int64_t tokens) {
+  if (check_moe_shape(moe) || tokens < 0 || tokens > nvfp4::kMoeMaxTokens) return 0;
+  return tokens == 0 ? round_up(nvfp4::moe_counter_bytes(moe->hidden), kWsAlign)
+                     : nvfp4::moe_layout(moe_args(*moe, tokens), nullptr, nullptr);
+}
+
+int nvfp4_moe_tokens(const nvfp4_moe* moe, const uint16_t* x, int64_t tokens, int64_t ldx, uint16_t* y, int64_t ldy,
+                     int32_t* ids_out, float* weights_out, void* workspace, size_t ws_bytes, void* hip_stream) {
+  int st;
+  if ((st = check_moe_shape(moe))) return st;
+  const nvfp4_moe& m = *moe;
+  if (m.router_dt != NVFP4_IN_BF16 && m.router_dt != NVFP4_IN_FP32) return fail(NVFP4_ERR_INVALID, "bad router dtype %d", (int)m.router_dt);
+  if ((st = check_act(m.act))) return st;
+  if (m.score != NVFP4_SCORE_SOFTMAX && m.score != NVFP4_SCORE_SIGMOID) return fail(NVFP4_ERR_INVALID, "bad score %d", (int)m.score);
+  if (!std::isfinite(m.routed_scale)) return fail(NVFP4_ERR_INVALID, "routed_scale is not finite");
+  const int64_t rows1 = m.experts * m.ffn * (m.gated ? 2 : 1), rows2 = m.experts * m.hidden;
+  if (m.w1.rows != rows1 || m.w1.cols != m.hidden || m.w2.rows != rows2 || m.w2.cols != m.ffn)
+    return fail(NVFP4_ERR_INVALID, "w1 must be [%lld, %lld] and w2 [%lld, %lld]", (long long)rows1, (long long)m.hidden,
+                (long long)rows2, (long long)m.ffn);
+  if (!m.router || !m.w1.codes || !m.w1.scales || !m.w1.global_scale || !m.w2.codes || !m.w2.scales || !m.w2.global_scale)
+    return fail(NVFP4_ERR_INVALID, "a NULL router or weight pointer");
+  if (!aligned(m.router, m.router_dt == NVFP4_IN_FP32 ? 4 : 2) || !aligned(m.w1.codes, 16) || !aligned(m.w2.codes, 16) ||
+      !aligned(m.w1.scales, 4) || !aligned(m.w2.scales, 4) || !aligned(m.w1.global_scale, 4) || !aligned(m.w2.global_scale, 4))
+    return fail(NVFP4_ERR_INVALID, "router or weights misaligned (codes 16 bytes, scales 4)");
+  if (tokens < 0) return fail(NVFP4_ERR_INVALID, "tokens = %lld", (long long)tokens);
+  if (tokens > nvfp4::kMoeMaxTokens) return fail(NVFP4_ERR_UNSUPPORTED, "%lld tokens: at most %lld", (long long)tokens, (long long)nvfp4::kMoeMaxTokens);
+  if (tokens == 0) return NVFP4_OK;
+  if (!x || !y) return fail(NVFP4_ERR_INVALID, "x or y is NULL");
+  if (ldx < m.hidden || ldy < m.hidden) return fail(NVFP4_ERR_INVALID, "ldx (%lld) or ldy (%lld) < hidden (%lld)", (long long)ldx, (long long)ldy, (long long)m.hidden);
+  if (!aligned(x, 2) || !aligned(y, 2) || !aligned(ids_out, 4) || !aligned(weights_out, 4))
+    return fail(NVFP4_ERR_INVALID, "a buffer is not aligned to its element size");
+  nvfp4::MoeArgs a = moe_args(m, tokens);
+  const size_t need = nvfp4::moe_layout(a, nullptr, nullptr);
+  if (!workspace || ws_bytes < need || !aligned(workspace, kWsAlign))
+    return fail(NVFP4_ERR_WORKSPACE, "workspace of %zu bytes (256-byte aligned) required, got %zu", need, workspace ? ws_bytes : (size_t)0);
+  a.x = x;
+  a.ldx = ldx;
+  a.y = y;
+  a.ldy = ldy;
+  a.ids_out = ids_out;
+  a.weights_out = weights_out;
+  return hip_status(nvfp4::launch_moe(a, static_cast<uint8_t*>(workspace), (hipStream_t)hip_stream), "moe_tokens");
 }
 
 }  // extern "C"

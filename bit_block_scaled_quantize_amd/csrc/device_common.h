@@ -33,6 +33,14 @@ __device__ __forceinline__ v4f32 ld_f32x4(const T* p) { return *reinterpret_cast
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// BF16 bits of v and w rounded to nearest, ties to even (low and high half; one
+// v_cvt_pk_bf16_f32).
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bf16_rn_pair(float v, float w) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f32{v, w}, bf16x2));
+}
+__device__ __forceinline__ uint32_t bf16_rn_bits(float v) { return bf16_rn_pair(v, 0.0f) & 0xFFFFu; }
+
 // ---- tensor scales ---------------------------------------------------------------------
 // Encode multiplier s_enc = rn32(2688 / amax) (FLT_MAX if that overflows), 1 for amax == 0.
 __device__ __forceinline__ float tensor_encode_scale(float amax) {

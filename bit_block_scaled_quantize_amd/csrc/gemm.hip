@@ -32,7 +32,7 @@
 //    operands loaded straight into registers one K step ahead.
 // In both, scale bytes at or past K are forced to 0, which zeroes whatever codes sit in a
 // partial last step.
-#include "activation.h"
+#include "act_out.h"
 #include "launch.h"
 
 namespace nvfp4 {
@@ -287,64 +287,6 @@ struct TileNext {
   bool valid;
   int64_t m0, n0, k_begin, k_end;
 };
-
-// BF16 bits of v and w rounded to nearest, ties to even (low and high half; one
-// v_cvt_pk_bf16_f32).
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t bf16_rn_pair(float v, float w) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f32{v, w}, bf16x2));
-}
-__device__ __forceinline__ uint32_t bf16_rn_bits(float v) { return bf16_rn_pair(v, 0.0f) & 0xFFFFu; }
-
-// ---- nvfp4_gemm_act's output -------------------------------------------------------------
-// z = product + bias (FP32); the pre-activation BF16(z) where asked for; d = BF16(act(z) +
-// residual). act takes the unrounded z.
-__device__ __forceinline__ float bias_at(const ActOut& o, int64_t col) {
-  if (o.bias == nullptr) return 0.0f;
-  return o.bias_f32 ? static_cast<const float*>(o.bias)[col] : bf16_lo(static_cast<const uint16_t*>(o.bias)[col]);
-}
-
-// Element (row, col); returns |stored d|.
-template <int ACT>
-__device__ __forceinline__ float put_act(const ActOut& o, uint16_t* d, int64_t ldd, int64_t row, int64_t col, float v) {
-  const float z = v + bias_at(o, col);
-  if (o.preact != nullptr) o.preact[row * o.ldp + col] = (uint16_t)bf16_rn_bits(z);
-  float y = act<ACT>(z);
-  if (o.residual != nullptr) y += bf16_lo(o.residual[row * o.ldr + col]);
-  const uint32_t b = bf16_rn_bits(y);
-  d[row * ldd + col] = (uint16_t)b;
-  return fabsf(__uint_as_float(b << 16));
-}
-
-// Eight consecutive elements of a row, every array moved as one 16-byte vector.
-template <int ACT>
-__device__ __forceinline__ float put_act8(const ActOut& o, uint16_t* d, int64_t ldd, int64_t row, int64_t col,
-                                          const float (&v)[8], const float (&bias)[8]) {
-  float z[8], y[8];
-  v4u32 res = {0, 0, 0, 0};
-  if (o.residual != nullptr) res = ld_u32x4(o.residual + row * o.ldr + col);
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    z[q] = v[q] + bias[q];
-    y[q] = act<ACT>(z[q]);
-  }
-  if (o.preact != nullptr)
-    *reinterpret_cast<v4u32*>(o.preact + row * o.ldp + col) =
-        v4u32{bf16_rn_pair(z[0], z[1]), bf16_rn_pair(z[2], z[3]), bf16_rn_pair(z[4], z[5]), bf16_rn_pair(z[6], z[7])};
-  v4u32 w;
-  float mx = 0.0f;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if (o.residual != nullptr) {
-      y[2 * q] += bf16_lo(res[q]);
-      y[2 * q + 1] += bf16_hi(res[q]);
-    }
-    w[q] = bf16_rn_pair(y[2 * q], y[2 * q + 1]);
-    mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[q])), fabsf(bf16_hi(w[q]))));
-  }
-  *reinterpret_cast<v4u32*>(d + row * ldd + col) = w;
-  return mx;
-}
 
 // Stores v as output element (row, col); returns |stored value|.
 template <int KIND>
@@ -1764,6 +1706,7 @@ hipError_t launch_gemm_act(GemmOperand a, GemmOperand b, int64_t M, int64_t N, i
   hipError_t e = amax ? launch_fill(amax, 1, 0.0f, stream) : hipSuccess;
   if (e != hipSuccess) return e;
   if (M == 0 || N == 0) return hipGetLastError();
+  if (M <= kSkinnyRows && K > 0) return launch_gemm_skinny(a, b, M, N, K, act_kind, act, D, ldd, amax, stream);
   if (use_big(K) && (e = enable_big_lds()) != hipSuccess) return e;
   const Operand A{a.codes, a.scales, M}, B{b.codes, b.scales, N};
   auto ok = [](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; };

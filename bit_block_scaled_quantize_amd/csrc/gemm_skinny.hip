@@ -1,0 +1,106 @@
+// nvfp4_gemm_act for at most 64 rows of A (the tokens of a generation step): D = act(A B^T + bias) +
+// residual with B's rows as the matrix instruction's rows and A's rows as its columns (skinny.h).
+// Bound by reading B: N K * 9/16 bytes.
+#include "act_out.h"
+#include "launch.h"
+#include "skinny.h"
+
+namespace nvfp4 {
+namespace {
+
+using namespace skinny;
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+
+// Columns from NVFP4 rows: decoded like the weights.
+template <int C, bool K32>
+struct TokensNvfp4 {
+  typedef Run Raw;
+  const uint8_t* codes[C];
+  const uint8_t* scales[C];
+  bool live[C];
+  int64_t K;
+  __device__ __forceinline__ Raw load(int c, int64_t k) const {
+    Run r = load_run<K32>(codes[c], scales[c], K, k);
+    r.scales = live[c] ? r.scales : 0u;
+    return r;
+  }
+  __device__ __forceinline__ half8 octet(int, const Raw& r, int t) const { return skinny::octet(r, t); }
+};
+
+template <int R, int C, bool K32>
+__global__ __launch_bounds__(kThreads) void k_gemm_skinny(GemmOperand A, GemmOperand B, int64_t M, int64_t N,
+                                                          int64_t K, int act, ActOut out, uint16_t* __restrict__ D,
+                                                          int64_t ldd, float* __restrict__ amax) {
+  __shared__ __attribute__((aligned(16))) float red[kWaves * R * C * 64 * 4];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * R);
+  const uint8_t *rc[R], *rs[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int64_t n = n0 + 16 * i + r < N ? n0 + 16 * i + r : n0;     // rows past N: not stored
+    rc[i] = B.codes + n * (K >> 1);
+    rs[i] = B.scales + n * (K >> 4);
+  }
+  TokensNvfp4<C, K32> tok;
+  tok.K = K;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int64_t m = 16 * c + r;
+    tok.live[c] = m < M;
+    tok.codes[c] = A.codes + (m < M ? m : 0) * (K >> 1);
+    tok.scales[c] = A.scales + (m < M ? m : 0) * (K >> 4);
+  }
+  float4v acc[R][C];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[i][c] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+  accumulate<R, C, K32>(rc, rs, K, wave, kWaves, tok, acc);
+  put<R, C>(red, wave, acc);
+  __syncthreads();
+  const float alpha = A.global_scale[0] * B.global_scale[0];
+  float mx = 0.0f;
+#pragma unroll 1
+  for (int f = wave; f < R * C; f += kWaves) {
+    const int i = f / C, c = f % C;
+    const float4v v = take<kWaves, R, C>(red, i, c);
+    const int64_t m = 16 * c + r, n = n0 + 16 * i + 4 * g;
+    if (m < M) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (n + q < N) mx = fmaxf(mx, put_act_of(act, out, D, ldd, m, n + q, v[q] * alpha));
+    }
+  }
+  if (amax != nullptr) {                                      // uniform
+    mx = wave_max(mx);
+    if (lane == 0) atomic_max_nonneg(amax, mx);
+  }
+}
+
+template <int R, int C>
+void launch_rc(const GemmOperand& a, const GemmOperand& b, int64_t M, int64_t N, int64_t K, int act, const ActOut& out,
+               uint16_t* D, int64_t ldd, float* amax, hipStream_t stream) {
+  const dim3 grid((unsigned)((N + 16 * R - 1) / (16 * R)));
+  if (K % 32 == 0)
+    hipLaunchKernelGGL((k_gemm_skinny<R, C, true>), grid, dim3(kThreads), 0, stream, a, b, M, N, K, act, out, D, ldd, amax);
+  else
+    hipLaunchKernelGGL((k_gemm_skinny<R, C, false>), grid, dim3(kThreads), 0, stream, a, b, M, N, K, act, out, D, ldd, amax);
+}
+
+}  // namespace
+
+hipError_t launch_gemm_skinny(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int act, const ActOut& out,
+                              uint16_t* D, int64_t ldd, float* amax, hipStream_t stream) {
+#define NVFP4_SK(R, C) launch_rc<R, C>(a, b, M, N, K, act, out, D, ldd, amax, stream)
+  if (M <= 16) NVFP4_SK(2, 1);
+  else if (M <= 32) NVFP4_SK(2, 2);
+  else NVFP4_SK(2, 4);
+#undef NVFP4_SK
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

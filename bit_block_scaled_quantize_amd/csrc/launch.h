@@ -134,6 +134,36 @@ struct ActOut {
 hipError_t launch_gemm_act(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int act_kind, ActOut act,
                            uint16_t* D, int64_t ldd, float* amax, float* ws, hipStream_t stream);
 
+// The same for M <= kSkinnyRows rows of A, any K % 16 == 0, without a workspace.
+constexpr int64_t kSkinnyRows = 64;
+hipError_t launch_gemm_skinny(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int act_kind,
+                              const ActOut& act, uint16_t* D, int64_t ldd, float* amax, hipStream_t stream);
+
+// A mixture-of-experts layer for at most kMoeMaxTokens tokens (csrc/moe.hip).
+constexpr int64_t kMoeMaxTokens = 64, kMoeMaxExperts = 512, kMoeMaxTopK = 16;
+struct MoeArgs {
+  const uint16_t* x;            // BF16 [tokens, hidden], row stride ldx
+  uint16_t* y;                  // BF16 [tokens, hidden], row stride ldy
+  int64_t ldx, ldy, hidden, ffn;
+  const void* router;           // BF16 or FP32 [experts, hidden]
+  GemmOperand w1, w2;           // [experts * ffn (2 ffn gated), hidden], [experts * hidden, ffn]
+  int* ids_out;                 // [tokens, top_k] or null
+  float* weights_out;           // [tokens, top_k] or null
+  int tokens, experts, top_k, act;
+  float routed_scale;
+  bool router_f32, gated, sigmoid, renormalize;
+};
+struct MoeWork {
+  int *counters, *used, *expert, *begin, *order, *ids;
+  float *weights, *logits, *x_inv;
+  uint32_t* h_top;
+  _Float16* x16;
+  float *h, *part;
+};
+size_t moe_layout(const MoeArgs& a, uint8_t* base, MoeWork* w);          // bytes; fills *w where given
+size_t moe_counter_bytes(int64_t hidden);                                // zero before the first call
+hipError_t launch_moe(const MoeArgs& a, uint8_t* ws, hipStream_t stream);
+
 // dz = BF16(dy act'(z)) (or null), dbias (FP32 [N], or null) = or += its column sums; ws holds
 // act_grad_workspace_bytes(M, N) bytes where dbias is asked for.
 size_t act_grad_workspace_bytes(int64_t M, int64_t N);

@@ -418,6 +418,55 @@ int nvfp4_amax_pair(const void* x, nvfp4_dtype dt, int64_t tokens, int64_t cols,
                     uint16_t sign_mask, float* amax_out, void* workspace, size_t ws_bytes,
                     void* hip_stream);
 
+/* How a routed expert's score comes from the router's logits. */
+typedef enum { NVFP4_SCORE_SOFTMAX = 0, NVFP4_SCORE_SIGMOID = 1 } nvfp4_score;
+
+/* A mixture-of-experts layer: the router and the experts' NVFP4 weights, quantized along their
+ * columns with one tensor scale per expert (nvfp4_quantize with segments, 1x16 or 16x16). */
+typedef struct nvfp4_moe {
+  int64_t experts, hidden, ffn;  /* experts 1 .. 512; hidden, ffn multiples of 16               */
+  int64_t top_k;                 /* experts per token, 1 .. min(16, experts)                    */
+  const void* router;            /* device BF16 or FP32 (router_dt) [experts, hidden]           */
+  nvfp4_dtype router_dt;
+  nvfp4_tensor w1;               /* [experts*ffn, hidden]; gated: [experts*2*ffn, hidden], each
+                                    expert's ffn gate rows before its ffn up rows               */
+  nvfp4_tensor w2;               /* [experts*hidden, ffn]; global_scale[experts], as w1's       */
+  nvfp4_act act;
+  int gated;                     /* h = act(gate x) * (up x) instead of act(w1 x)               */
+  nvfp4_score score;
+  int renormalize;               /* scores divided by their sum over the token's experts        */
+  float routed_scale;            /* factor on every routing weight                              */
+} nvfp4_moe;
+
+/*
+ * nvfp4_moe_tokens - a whole mixture-of-experts layer for a few tokens, a generation step's batch
+ * ("Nemotron NVFP4" explainer, "The model underneath": expert layers, and "The honest part: this is
+ * not end-to-end FP4": the expert weights are what runs in NVFP4). Activations stay in BF16:
+ *   l = x router^T (FP32);  the top_k largest of a token's l pick its experts, ties the lowest
+ *   s = softmax(l) over all experts, or 1 / (1 + exp(-l));  w = s * routed_scale, or with
+ *   renormalize s / (sum over the token's experts of s + 1e-20) * routed_scale
+ *   y = BF16(sum over the token's experts of w * w2 h),  h = act(w1 x) or act(gate x) * (up x)
+ *   x          device BF16 [tokens, hidden], row stride ldx >= hidden; tokens 0 .. 64 (larger batches:
+ *              nvfp4_quantize with segments and nvfp4_grouped_gemm).
+ *   y          device BF16 [tokens, hidden], row stride ldy >= hidden; overlaps no input.
+ *   ids_out, weights_out   NULL, or device int32 / float [tokens, top_k]: the experts, largest logit
+ *              first, and w.
+ *   workspace  nvfp4_moe_workspace_size(moe, tokens) bytes (that of more tokens serves fewer),
+ *              256-byte aligned. Its first nvfp4_moe_workspace_size(moe, 0) bytes have to be zero
+ *              before the first call and are zero again after each; calls that share a workspace
+ *              have to be ordered.
+ * A token's result does not depend on the other tokens of the call, nor on the order in which
+ * workgroups finish. Non-finite values of one token stay with that token. Errors:
+ * NVFP4_ERR_INVALID (null or misaligned pointers, shapes, strides, enums), NVFP4_ERR_UNSUPPORTED
+ * (more than 64 tokens, 512 experts or top_k 16), NVFP4_ERR_WORKSPACE, NVFP4_ERR_HIP.
+ */
+int nvfp4_moe_tokens(const nvfp4_moe* moe, const uint16_t* x, int64_t tokens, int64_t ldx, uint16_t* y, int64_t ldy,
+                     int32_t* ids_out, float* weights_out, void* workspace, size_t ws_bytes, void* hip_stream);
+
+/* Bytes of nvfp4_moe_tokens' workspace for `tokens` tokens; with tokens = 0 those that have to be
+ * zero at first. 0 for a bad argument. */
+size_t nvfp4_moe_workspace_size(const nvfp4_moe* moe, int64_t tokens);
+
 /* How the two running means of AdamW are held: FP32, or 8 bits (below). */
 typedef enum { NVFP4_STATE_FP32 = 0, NVFP4_STATE_8BIT = 1 } nvfp4_state;
 

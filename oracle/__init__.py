@@ -37,6 +37,7 @@ from .hadamard import (rht_columnwise, rht_columnwise_f64, hadamard_matrix_from_
 from .mx import (MX_BLOCK, e8m0_decode, mx_shared_exponent, quantize_mxfp4, dequantize_mxfp4)
 from .adamw import (adamw64, state_scale_exponents, state_random, state_codes, state_values)
 from .activation import act64, act_slope64, act_error, act_slope_error
+from .moe import moe64
 from .gemm import (gemm_fp64, gemm_bound, grouped_gemm_fp64, grouped_gemm_bound, grouped_gemm_k_fp64,
                    grouped_gemm_k_bound, round_bf16, gemm_bf16_bound, gemm_accumulate_fp64,
                    gemm_accumulate_bound)
@@ -54,5 +55,6 @@ __all__ = [
     "gemm_accumulate_fp64", "gemm_accumulate_bound",
     "adamw64", "state_scale_exponents", "state_random", "state_codes", "state_values",
     "act64", "act_slope64", "act_error", "act_slope_error",
+    "moe64",
     "MX_BLOCK", "e8m0_decode", "mx_shared_exponent", "quantize_mxfp4", "dequantize_mxfp4",
 ]

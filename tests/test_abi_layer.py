@@ -129,3 +129,40 @@ def test_act_grad_validation(lib):
     assert call(ws=FAKE + 64) == WORKSPACE
     assert lib.nvfp4_workspace_size(nv.OP_ACT_GRAD, 8, 32, 1) == 0          # one run of rows: no partial sums
     assert lib.nvfp4_workspace_size(nv.OP_ACT_GRAD, 100, 32, 1) > 0
+
+
+def _moe(**kw):
+    f = dict(experts=8, hidden=64, ffn=32, top_k=2, router=FAKE, router_dt=0, act=1, gated=0, score=0, renormalize=1,
+             routed_scale=1.0)
+    w1 = kw.pop("w1", nv._CTensor(FAKE, FAKE, FAKE, 8 * 32, 64))
+    w2 = kw.pop("w2", nv._CTensor(FAKE, FAKE, FAKE, 8 * 64, 32))
+    f.update(kw)
+    return nv._CMoE(w1=w1, w2=w2, **f)
+
+
+def test_moe_validation(lib):
+    def call(moe=None, x=FAKE, tokens=4, ldx=64, y=FAKE, ldy=64, ids=None, wts=None, ws=FAKE, ws_n=1 << 20, **kw):
+        m = _moe(**kw)
+        return lib.nvfp4_moe_tokens(ctypes.byref(m), x, tokens, ldx, y, ldy, ids, wts, ws, ws_n, None)
+
+    assert lib.nvfp4_moe_tokens(None, FAKE, 1, 64, FAKE, 64, None, None, FAKE, 1 << 20, None) == INVALID
+    assert call(tokens=0, x=None, y=None, ws=None) == 0                       # nothing to do
+    for kw in (dict(experts=0), dict(hidden=72), dict(ffn=8), dict(top_k=0), dict(top_k=9), dict(router=None),
+               dict(router=FAKE + 2, router_dt=1), dict(router_dt=3), dict(act=9), dict(score=2), dict(gated=1),
+               dict(routed_scale=float("inf")), dict(w1=nv._CTensor(FAKE, FAKE, FAKE, 256, 48)),
+               dict(w2=nv._CTensor(FAKE, FAKE, FAKE, 511, 32)), dict(w1=nv._CTensor(None, FAKE, FAKE, 256, 64)),
+               dict(w2=nv._CTensor(FAKE + 8, FAKE, FAKE, 512, 32)), dict(w2=nv._CTensor(FAKE, FAKE + 1, FAKE, 512, 32)),
+               dict(x=None), dict(y=None), dict(x=FAKE + 1), dict(ldx=63), dict(ldy=63), dict(tokens=-1),
+               dict(ids=FAKE + 2), dict(wts=FAKE + 2)):
+        assert call(**kw) == INVALID, kw
+    assert call(tokens=65) == UNSUPPORTED
+    assert call(experts=513, w1=nv._CTensor(FAKE, FAKE, FAKE, 513 * 32, 64),
+                w2=nv._CTensor(FAKE, FAKE, FAKE, 513 * 64, 32)) == UNSUPPORTED
+    assert call(experts=32, top_k=17) == UNSUPPORTED
+    assert call(ws=None) == WORKSPACE
+    assert call(ws=FAKE + 128) == WORKSPACE
+    need = [lib.nvfp4_moe_workspace_size(ctypes.byref(_moe()), t) for t in (0, 1, 2, 64)]
+    assert need == sorted(need) and 0 < need[0] < need[1]
+    assert call(ws_n=need[1]) == WORKSPACE
+    assert lib.nvfp4_moe_workspace_size(ctypes.byref(_moe()), 65) == 0
+    assert lib.nvfp4_moe_workspace_size(ctypes.byref(_moe(top_k=9)), 1) == 0
