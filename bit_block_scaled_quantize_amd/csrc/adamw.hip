@@ -310,7 +310,7 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const AdamWEntry* __restrict
   }
   if (amax_out != nullptr) {                                  // uniform
     mx = wave_max(mx);
-    if ((threadIdx.x & 63) == 0) atomic_max_nonneg(&amax_out[ti], mx);
+    if ((threadIdx.x & 63) == 0) atomic_raise_nonneg(&amax_out[ti], mx);
   }
 }
 

@@ -117,8 +117,11 @@ int check_moe_shape(const nvfp4_moe* m) {
   if (m->experts > nvfp4::kMoeMaxExperts || m->top_k > nvfp4::kMoeMaxTopK)
     return fail(NVFP4_ERR_UNSUPPORTED, "at most %lld experts and top_k %lld (got %lld, %lld)",
                 (long long)nvfp4::kMoeMaxExperts, (long long)nvfp4::kMoeMaxTopK, (long long)m->experts, (long long)m->top_k);
-  if (m->hidden > (int64_t(1) << 24) || m->ffn > (int64_t(1) << 24))
-    return fail(NVFP4_ERR_UNSUPPORTED, "hidden (%lld) or ffn (%lld) above 2^24", (long long)m->hidden, (long long)m->ffn);
+  // the kernels address an expert's matrix and the tokens' rows through 32-bit buffer offsets
+  if (m->hidden > (int64_t(1) << 18) || m->ffn > (int64_t(1) << 18) ||
+      m->hidden * m->ffn * (m->gated ? 2 : 1) / 2 > (int64_t)0x7FFFFFFF)
+    return fail(NVFP4_ERR_UNSUPPORTED, "hidden (%lld) or ffn (%lld) above 2^18, or an expert's codes above 2 GiB",
+                (long long)m->hidden, (long long)m->ffn);
   return NVFP4_OK;
 }
 

@@ -10,23 +10,20 @@ namespace {
 
 using namespace skinny;
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 
 // Columns from NVFP4 rows: decoded like the weights.
 template <int C, bool K32>
 struct TokensNvfp4 {
-  typedef Run Raw;
-  const uint8_t* codes[C];
-  const uint8_t* scales[C];
-  bool live[C];
-  int64_t K;
-  __device__ __forceinline__ Raw load(int c, int64_t k) const {
-    Run r = load_run<K32>(codes[c], scales[c], K, k);
-    r.scales = live[c] ? r.scales : 0u;
-    return r;
+  typedef Run<K32> Raw;
+  Matrix a;
+  uint32_t rows, r;                                           // r: the lane's column of a fragment
+  __device__ __forceinline__ Raw load(int c, uint32_t k) const {
+    const uint32_t m = 16u * (uint32_t)c + r;
+    return load_run<K32>(a, m, m < rows, k);
   }
-  __device__ __forceinline__ half8 octet(int, const Raw& r, int t) const { return skinny::octet(r, t); }
+  __device__ __forceinline__ half8 octet(const Raw& x, uint32_t, int t) const { return octet_of(x, t); }
 };
 
 template <int R, int C, bool K32>
@@ -38,28 +35,19 @@ __global__ __launch_bounds__(kThreads) void k_gemm_skinny(GemmOperand A, GemmOpe
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * (16 * R);
-  const uint8_t *rc[R], *rs[R];
+  const Matrix weights(B.codes, B.scales, N, K);
+  uint32_t row[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int64_t n = n0 + 16 * i + r < N ? n0 + 16 * i + r : n0;     // rows past N: not stored
-    rc[i] = B.codes + n * (K >> 1);
-    rs[i] = B.scales + n * (K >> 4);
-  }
-  TokensNvfp4<C, K32> tok;
-  tok.K = K;
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int64_t m = 16 * c + r;
-    tok.live[c] = m < M;
-    tok.codes[c] = A.codes + (m < M ? m : 0) * (K >> 1);
-    tok.scales[c] = A.scales + (m < M ? m : 0) * (K >> 4);
-  }
+  for (int i = 0; i < R; ++i) row[i] = (uint32_t)(n0 + 16 * i + r < N ? n0 + 16 * i + r : n0);   // rows past N: not stored
+  const TokensNvfp4<C, K32> tok{Matrix(A.codes, A.scales, M, K), (uint32_t)M, (uint32_t)r};
   float4v acc[R][C];
 #pragma unroll
   for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[i][c] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-  accumulate<R, C, K32>(rc, rs, K, wave, kWaves, tok, acc);
+  Pipe<R, C, K32, TokensNvfp4<C, K32>> pipe;
+  pipe.start(weights, row, tok, wave, kWaves);
+  pipe.run(weights, row, tok, wave, kWaves, (int)((K + kStep - 1) / kStep), acc);
   put<R, C>(red, wave, acc);
   __syncthreads();
   const float alpha = A.global_scale[0] * B.global_scale[0];
@@ -75,9 +63,9 @@ __global__ __launch_bounds__(kThreads) void k_gemm_skinny(GemmOperand A, GemmOpe
         if (n + q < N) mx = fmaxf(mx, put_act_of(act, out, D, ldd, m, n + q, v[q] * alpha));
     }
   }
-  if (amax != nullptr) {                                      // uniform
-    mx = wave_max(mx);
-    if (lane == 0) atomic_max_nonneg(amax, mx);
+  if (amax != nullptr && wave < R * C) {                      // uniform
+    mx = wave_fold_max(mx);
+    if (lane == 0) atomic_raise_nonneg(amax, mx);
   }
 }
 

@@ -154,9 +154,8 @@ struct MoeArgs {
   bool router_f32, gated, sigmoid, renormalize;
 };
 struct MoeWork {
-  int *counters, *used, *expert, *begin, *order, *ids;
-  float *weights, *logits, *x_inv;
-  uint32_t* h_top;
+  int *counters, *used, *expert, *count, *order, *ids;
+  float *weights, *logits, *x_inv, *h_top;
   _Float16* x16;
   float *h, *part;
 };

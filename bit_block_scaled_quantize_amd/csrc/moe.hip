@@ -10,7 +10,7 @@
 //  1. k_route: logits (a wave per expert, 8 tokens at a time), x in FP16; the last workgroup of a
 //     token group to finish picks its tokens' experts, the last group to finish sorts the
 //     (token, expert) pairs by expert.
-//  2. k_expert<UP>: 16 R rows of one used expert times its tokens (skinny.h), the activation, h.
+//  2. k_expert<UP>: 32 rows of one used expert times its tokens (skinny.h), the activation, h.
 //  3. k_expert<DOWN>: the same over W2, the routing weight, one partial result per pair; the last
 //     workgroup of a row tile to finish adds the k partials of each token in order.
 // "The last to finish" is found with a counter that the last one resets: nothing waits for
@@ -30,8 +30,9 @@ namespace {
 
 using namespace skinny;
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
+
+constexpr int kRouteThreads = 256, kRouteWaves = 4;
+constexpr int kRouteExperts = 4;                              // per workgroup of k_route
 constexpr int kGroupTokens = 8;                               // tokens per workgroup of k_route
 
 // 2^e with max |v| 2^e in [2^14, 2^15); 1 for a zero or non-finite maximum. Exponents are kept
@@ -45,27 +46,34 @@ __device__ __forceinline__ float half_scale(float top) {
 
 __device__ __forceinline__ half2v half_pair(float a, float b) { return half2v{(_Float16)a, (_Float16)b}; }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
+// What one workgroup writes and another of the same launch reads goes past the caches that are not
+// shared (each XCD has its own L2) by device-scope accesses of single words; a release fence
+// instead would write back the whole L2, once per workgroup (5400 of them took 0.4 ms).
+template <class T>
+__device__ __forceinline__ void put_shared(T* p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <class T>
+__device__ __forceinline__ T get_shared(const T* p) {
+  return __hip_atomic_load(const_cast<T*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // True in the workgroup that is the last of `total` to call this with `counter`, which it resets.
-// What the others wrote before is visible to it afterwards. All threads call.
+// What the others had put_shared before is there for its get_shared: every wave waits until its
+// stores have been acknowledged, then the workgroup meets, then it is counted. All threads call.
 __device__ __forceinline__ bool last_to_finish(int* counter, int total) {
   __shared__ int last;
-  __threadfence();
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
+  if (total == 1) return true;                                // uniform: nobody else
   if (threadIdx.x == 0) {
-    const int before = atomicAdd(counter, 1);
+    const int before = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     last = before == total - 1;
-    if (last) atomicExch(counter, 0);
+    if (last) put_shared(counter, 0);
   }
   __syncthreads();
   const bool is_last = last != 0;
   __syncthreads();
-  if (is_last) __threadfence();
   return is_last;
 }
 
@@ -97,30 +105,32 @@ __device__ __forceinline__ void load8(const void* row, int64_t i, int64_t n, boo
   }
 }
 
-// The k largest logits of one token (one wave), ties to the lowest expert, NaN last; ids and weights.
-// At most kMoeMaxExperts experts: lane l holds experts l, l + 64, ...
-__device__ __forceinline__ void pick_experts(const MoeArgs& a, const MoeWork& w, int t) {
+// The k largest logits of one token (one wave), ties to the lowest expert; its experts and weights.
+// At most kMoeMaxExperts experts: lane l holds experts l, l + 64, ... A NaN logit ranks last, and one
+// anywhere makes every weight of the token NaN.
+__device__ __forceinline__ void pick_experts(const MoeArgs& a, const MoeWork& w, int t, int* ids) {
   constexpr int kPer = (int)(kMoeMaxExperts / 64);
   const int lane = threadIdx.x & 63;
   const float* logits = w.logits + (int64_t)t * a.experts;
   float key[kPer];
   float top = -INFINITY;
+  bool bad = false;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int e = lane + 64 * j;
-    const float l = e < a.experts ? logits[e] : -INFINITY;
+    const float l = e < a.experts ? get_shared(&logits[e]) : -INFINITY;
+    bad |= l != l;
     key[j] = l == l ? l : -INFINITY;
-    top = fmaxf(top, l);
+    top = fmaxf(top, key[j]);
   }
+  bad = __any(bad);
+  top = wave_fold_max(top);
   float denom = 0.0f;                                         // of the softmax over all experts
   if (!a.sigmoid) {
-    top = wave_max(top);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int e = lane + 64 * j;
-      if (e < a.experts) denom += expf(logits[e] - top);
-    }
-    denom = wave_sum(denom);
+    for (int j = 0; j < kPer; ++j)
+      if (64 * j < a.experts) denom += lane + 64 * j < a.experts ? expf(key[j] - top) : 0.0f;
+    denom = wave_fold_sum(denom);
   }
   uint32_t taken = 0;                                         // bit j: this lane's expert j
   float mine = 0.0f, total = 0.0f;                            // lane j keeps pick j's score
@@ -134,16 +144,10 @@ __device__ __forceinline__ void pick_experts(const MoeArgs& a, const MoeWork& w,
         best = key[q];
         at = q;
       }
-    const float m = wave_max(at < 0 ? -INFINITY : best);
-    // among the lanes that hold it, the lowest expert: lowest q, then lowest lane
-    int e = at >= 0 && best == m ? lane + 64 * at : 0x7FFFFFFF;
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) {
-      const int other = __shfl_xor(e, o, 64);
-      e = other < e ? other : e;
-    }
+    const float l = wave_fold_max(best);                      // the pick's logit
+    // among the lanes that hold it the lowest expert; top_k <= experts: one is left
+    const int e = (int)wave_fold_min(at >= 0 && best == l ? (uint32_t)(lane + 64 * at) : 0xFFFFFFFFu);
     if ((e & 63) == lane) taken |= 1u << (e >> 6);
-    const float l = logits[e];
     const float s = a.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top) / denom;
     total += s;
     if (lane == j) {
@@ -152,308 +156,338 @@ __device__ __forceinline__ void pick_experts(const MoeArgs& a, const MoeWork& w,
     }
   }
   if (lane < a.top_k) {
-    const float wt = (a.renormalize ? mine / (total + 1e-20f) : mine) * a.routed_scale;
+    float wt = (a.renormalize ? mine / (total + 1e-20f) : mine) * a.routed_scale;
+    if (bad) wt = __uint_as_float(0x7FC00000u);
     const int64_t p = (int64_t)t * a.top_k + lane;
-    w.ids[p] = id;
+    put_shared(&ids[p], id);
     w.weights[p] = wt;
     if (a.ids_out) a.ids_out[p] = id;
     if (a.weights_out) a.weights_out[p] = wt;
   }
 }
 
-// The pairs (token t, pick j), numbered t * top_k + j, sorted by expert: w.order[w.begin[u] ..
-// w.begin[u + 1]) are those of the u-th used expert w.expert[u]. The order within an expert is that
-// of arrival; a pair's place decides which column it takes and nothing of its result.
+// The pairs (token t, pick j), numbered t * top_k + j, by expert: those of the u-th used expert
+// w.expert[u] are w.order[u * 64 .. + w.count[u]) (a token has an expert at most once). Which slot a
+// pair gets decides the column it takes and nothing of its result.
 __device__ __forceinline__ void sort_pairs(const MoeArgs& a, const MoeWork& w) {
-  __shared__ int count[kMoeMaxExperts], start[kMoeMaxExperts], used_before[kMoeMaxExperts];
-  const int pairs = a.tokens * a.top_k;
-  for (int e = threadIdx.x; e < a.experts; e += kThreads) count[e] = 0;
+  const int pairs = a.tokens * a.top_k;                       // a.experts or this many counts are read
+  if (a.tokens == 1) {
+    if ((int)threadIdx.x < pairs) {
+      w.expert[threadIdx.x] = get_shared(&w.ids[threadIdx.x]);
+      w.count[threadIdx.x] = 1;
+      w.order[threadIdx.x * kMoeMaxTokens] = threadIdx.x;
+    }
+    if (threadIdx.x == 0) *w.used = pairs;
+    return;
+  }
+  __shared__ int count[kMoeMaxExperts], place[kMoeMaxExperts];
+  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) count[e] = 0;
+  constexpr int kMine = (int)(kMoeMaxTokens * kMoeMaxTopK / kRouteThreads);
+  int id[kMine], slot[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int p = threadIdx.x + i * kRouteThreads;
+    id[i] = p < pairs ? get_shared(&w.ids[p]) : -1;
+  }
   __syncthreads();
-  for (int p = threadIdx.x; p < pairs; p += kThreads) atomicAdd(&count[w.ids[p]], 1);
+#pragma unroll
+  for (int i = 0; i < kMine; ++i)
+    if (id[i] >= 0) slot[i] = atomicAdd(&count[id[i]], 1);
   __syncthreads();
-  if (threadIdx.x < 64) {                                     // one wave: exclusive sums over the experts
-    int pos = 0, used = 0;
+  if (threadIdx.x < 64) {                                     // one wave numbers the used experts
+    int used = 0;
     for (int e0 = 0; e0 < a.experts; e0 += 64) {
       const int e = e0 + threadIdx.x;
       const int c = e < a.experts ? count[e] : 0;
-      int sum = c;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int y = __shfl_up(sum, d);
-        if ((int)threadIdx.x >= d) sum += y;
-      }
       const uint64_t have = __ballot(c > 0);
-      if (e < a.experts) {
-        start[e] = pos + sum - c;
-        used_before[e] = used + __popcll(have & ((1ull << threadIdx.x) - 1));
+      const int u = used + __popcll(have & ((1ull << threadIdx.x) - 1));
+      if (c > 0) {
+        place[e] = u;
+        w.expert[u] = e;
+        w.count[u] = c;
       }
-      pos += __shfl(sum, 63);
       used += __popcll(have);
     }
-    if (threadIdx.x == 0) {
-      *w.used = used;
-      w.begin[used] = pairs;
-    }
+    if (threadIdx.x == 0) *w.used = used;
+    for (int u = used + (int)threadIdx.x; u < a.experts; u += 64) w.count[u] = 0;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.experts; e += kThreads) {
-    if (count[e] > 0) {
-      w.expert[used_before[e]] = e;
-      w.begin[used_before[e]] = start[e];
-    }
-  }
-  __syncthreads();
-  for (int p = threadIdx.x; p < pairs; p += kThreads) w.order[atomicAdd(&start[w.ids[p]], 1)] = p;
+#pragma unroll
+  for (int i = 0; i < kMine; ++i)
+    if (id[i] >= 0) w.order[place[id[i]] * kMoeMaxTokens + slot[i]] = threadIdx.x + i * kRouteThreads;
 }
 
-// Grid: x = blocks of 4 experts, then one more block that brings the group's tokens to FP16; y =
-// groups of 8 tokens.
-template <bool F32>
-__global__ __launch_bounds__(kThreads) void k_route(MoeArgs a, MoeWork w, bool vec_x, bool vec_r) {
+// Grid: x = blocks of 4 experts, then 8 blocks that bring one token each to FP16; y = groups of 8
+// tokens. A logit block's waves split the hidden dimension, so that a row's loads are in flight
+// together. NT: tokens of a group computed (1, or 8 with the surplus repeating the first).
+template <bool F32, int NT>
+__global__ __launch_bounds__(kRouteThreads) void k_route(MoeArgs a, MoeWork w, bool vec_x, bool vec_r) {
+  __shared__ float red[kRouteWaves][kRouteExperts * NT];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t0 = blockIdx.y * kGroupTokens;
   const int nt = a.tokens - t0 < kGroupTokens ? a.tokens - t0 : kGroupTokens;
-  const int blocks = (int)gridDim.x - 1;
+  const int blocks = (int)gridDim.x - kGroupTokens;
   const int64_t H = a.hidden;
-  if ((int)blockIdx.x == blocks) {
-    for (int q = wave; q < nt; q += kWaves) {
-      const int t = t0 + q;
-      const uint16_t* row = a.x + (int64_t)t * a.ldx;
-      float top = 0.0f;
-      for (int64_t i = lane * 8; i < H; i += 512) {
-        float v[8];
-        load8<false>(row, i, H, vec_x, v);
+  if ((int)blockIdx.x >= blocks) {
+    const int q = (int)blockIdx.x - blocks;
+    if (q >= nt) return;
+    const int t = t0 + q;
+    const uint16_t* row = a.x + (int64_t)t * a.ldx;
+    float top = 0.0f;
+#pragma unroll 2
+    for (int64_t i = threadIdx.x * 8; i < H; i += kRouteThreads * 8) {
+      float v[8];
+      load8<false>(row, i, H, vec_x, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
-      }
-      const float s = half_scale(wave_max(top));
-      for (int64_t i = lane * 8; i < H; i += 512) {            // H is a multiple of 16
-        float v[8];
-        load8<false>(row, i, H, vec_x, v);
-        half8 o;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = (_Float16)(v[j] * s);
-        *reinterpret_cast<half8*>(w.x16 + (int64_t)t * H + i) = o;
-      }
-      if (lane == 0) w.x_inv[t] = 1.0f / s;                   // a power of two: exact
-      if (lane < a.top_k) w.h_top[(int64_t)t * a.top_k + lane] = 0u;
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
     }
+    top = wave_fold_max(top);
+    if (lane == 0) red[wave][0] = top;
+    __syncthreads();
+    const float s = half_scale(fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0])));
+#pragma unroll 2
+    for (int64_t i = threadIdx.x * 8; i < H; i += kRouteThreads * 8) {       // H is a multiple of 16
+      float v[8];
+      load8<false>(row, i, H, vec_x, v);
+      half8 o;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = (_Float16)(v[j] * s);
+      *reinterpret_cast<half8*>(w.x16 + (int64_t)t * H + i) = o;
+    }
+    if (threadIdx.x == 0) w.x_inv[t] = 1.0f / s;              // a power of two: exact
     return;
   }
-  const int e = blockIdx.x * kWaves + wave;
-  if (e < a.experts) {
-    const void* row = static_cast<const uint8_t*>(a.router) + (int64_t)e * H * (F32 ? 4 : 2);
-    float acc[kGroupTokens] = {};
-    for (int64_t i = lane * 8; i < H; i += 512) {
-      float r[8];
-      load8<F32>(row, i, H, vec_r, r);
+  const int e0 = blockIdx.x * kRouteExperts;
+  const void* row[kRouteExperts];
 #pragma unroll
-      for (int q = 0; q < kGroupTokens; ++q) {
-        if (q < nt) {                                         // uniform
-          float v[8];
-          load8<false>(a.x + (int64_t)(t0 + q) * a.ldx, i, H, vec_x, v);
+  for (int e = 0; e < kRouteExperts; ++e)
+    row[e] = static_cast<const uint8_t*>(a.router) + (int64_t)(e0 + e < a.experts ? e0 + e : e0) * H * (F32 ? 4 : 2);
+  float acc[kRouteExperts][NT] = {};
+#pragma unroll 2
+  for (int64_t i = threadIdx.x * 8; i < H; i += kRouteThreads * 8) {
+    float r[kRouteExperts][8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[q] = __builtin_fmaf(r[j], v[j], acc[q]);
-        }
-      }
-    }
+    for (int e = 0; e < kRouteExperts; ++e) load8<F32>(row[e], i, H, vec_r, r[e]);
 #pragma unroll
-    for (int q = 0; q < kGroupTokens; ++q) {
-      if (q < nt) {
-        const float l = wave_sum(acc[q]);
-        if (lane == 0) w.logits[(int64_t)(t0 + q) * a.experts + e] = l;
-      }
+    for (int q = 0; q < NT; ++q) {
+      float v[8];
+      load8<false>(a.x + (int64_t)(t0 + (q < nt ? q : 0)) * a.ldx, i, H, vec_x, v);
+#pragma unroll
+      for (int e = 0; e < kRouteExperts; ++e)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[e][q] = __builtin_fmaf(r[e][j], v[j], acc[e][q]);
     }
   }
+#pragma unroll
+  for (int e = 0; e < kRouteExperts; ++e)
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+      const float s = wave_fold_sum(acc[e][q]);
+      if (lane == 0) red[wave][e * NT + q] = s;
+    }
+  __syncthreads();
+  if (threadIdx.x < kRouteExperts * NT) {
+    const int e = threadIdx.x / NT, q = threadIdx.x % NT;
+    if (e0 + e < a.experts && q < nt)
+      put_shared(&w.logits[(int64_t)(t0 + q) * a.experts + e0 + e],
+                 (red[0][threadIdx.x] + red[1][threadIdx.x]) + (red[2][threadIdx.x] + red[3][threadIdx.x]));
+  }
   if (!last_to_finish(&w.counters[1 + blockIdx.y], blocks)) return;
-  for (int q = wave; q < nt; q += kWaves) pick_experts(a, w, t0 + q);
+  for (int q = wave; q < nt; q += kRouteWaves) pick_experts(a, w, t0 + q, w.ids);
   if (!last_to_finish(&w.counters[0], (int)gridDim.y)) return;
   sort_pairs(a, w);
 }
 
-// Columns of the up product: FP16 rows of x.
-template <int C>
-struct TokensHalf {
-  struct Raw { half8 v[4]; };
-  const _Float16* row[C];
-  bool live[C];
-  int64_t K;
-  __device__ __forceinline__ Raw load(int c, int64_t k) const {
-    Raw r;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      r.v[t] = half8{};
-      if (live[c] && k + 8 * t < K) r.v[t] = *reinterpret_cast<const half8*>(row[c] + k + 8 * t);
-    }
-    return r;
-  }
-  __device__ __forceinline__ half8 octet(int, const Raw& r, int t) const { return r.v[t]; }
-};
-
-// Columns of the down product: FP32 rows of h, scaled into FP16.
-template <int C>
-struct TokensFloat {
-  struct Raw { v4f32 v[8]; };
-  const float* row[C];
-  float scale[C];                                             // a power of two per column
-  bool live[C];
-  int64_t K;
-  __device__ __forceinline__ Raw load(int c, int64_t k) const {
-    Raw r;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      r.v[2 * t] = r.v[2 * t + 1] = v4f32{};
-      if (live[c] && k + 8 * t < K) {
-        r.v[2 * t] = ld_f32x4(row[c] + k + 8 * t);
-        r.v[2 * t + 1] = ld_f32x4(row[c] + k + 8 * t + 4);
-      }
-    }
-    return r;
-  }
-  __device__ __forceinline__ half8 octet(int c, const Raw& r, int t) const {
-    const v4f32 a = r.v[2 * t] * scale[c], b = r.v[2 * t + 1] * scale[c];
-    return half8{(_Float16)a[0], (_Float16)a[1], (_Float16)a[2], (_Float16)a[3],
-                 (_Float16)b[0], (_Float16)b[1], (_Float16)b[2], (_Float16)b[3]};
+// Columns staged in LDS as FP16: kCols rows of `pitch` bytes and one run of zeros for the lanes
+// without a token. Nothing of them is loaded in the loop over K, whose only loads are the weights'.
+constexpr int kCols = 8;                                      // tokens of an expert at a time
+constexpr int kChunk = 4096;                                  // elements of K staged at a time
+struct TokensLds {
+  struct Raw {};
+  const uint8_t* at;                                          // of the lane's row
+  uint32_t k0, K, mask;                                       // first element staged; 0 for the zeros
+  __device__ __forceinline__ Raw load(int, uint32_t) const { return Raw{}; }
+  __device__ __forceinline__ half8 octet(const Raw&, uint32_t k, int t) const {
+    // past K the weights' scales are zero, and what LDS holds there is finite
+    return *reinterpret_cast<const half8*>(at + ((2 * (k - k0)) & mask) + 16 * t);
   }
 };
 
-// 16 R weight rows of one used expert times its tokens, 16 C at a time (the weights' second and
+// 16 R weight rows of one used expert times its tokens, kCols at a time (the weights' second and
 // later readings come from the cache). Grid: used experts (as many as there can be; the surplus
 // leaves at once) x row tiles, tiles of one expert next to each other.
 // UP: rows of W1, K = hidden -> h[pair][f]. GATED: fragments 0 .. R/2 - 1 hold the gate's rows, the
 // others the same rows of U. DOWN: rows of W2, K = ffn -> part[pair][n], then y.
-template <bool UP, bool GATED, int R, int C, bool K32>
-__global__ __launch_bounds__(kThreads) void k_expert(MoeArgs a, MoeWork w, int tiles) {
+template <bool UP, bool GATED, int R, int W, bool K32>
+__global__ __launch_bounds__(64 * W) void k_expert(MoeArgs a, MoeWork w, int tiles, int cols, uint32_t pitch) {
+  constexpr int kWaves = W, kThreads = 64 * W;
+  static_assert(!GATED || R % 2 == 0, "a gated tile holds as many gate as up fragments");
+  static_assert(R <= W, "a wave per fragment of output rows");
   constexpr int RO = GATED ? R / 2 : R;                       // fragments of output rows
-  __shared__ __attribute__((aligned(16))) float red[kWaves * R * C * 64 * 4];
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  float* red = reinterpret_cast<float*>(lds);                 // kWaves R fragments
+  uint8_t* const zeros = lds + kWaves * R * 64 * 16;          // 64 bytes
+  uint8_t* const tokens = zeros + 64;                         // cols rows of pitch bytes
   const int u = blockIdx.x / tiles, tile = blockIdx.x % tiles;
-  const int used = *w.used;
-  if (u >= used) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int e = w.expert[u];
-  const int p0 = w.begin[u], p1 = w.begin[u + 1];
+  // one round trip for all of the routing that does not depend on more of it (slots past the
+  // count hold anything and are not followed; the count is 0 past the used experts)
+  int mine = w.order[u * (int)kMoeMaxTokens + (r & (kCols - 1))];
+  const int e = w.expert[u], count = w.count[u];
+  if (count == 0) return;
   const int64_t K = UP ? a.hidden : a.ffn, N = UP ? a.ffn : a.hidden;
   const int64_t n0 = (int64_t)tile * (16 * RO);
   const GemmOperand& m = UP ? a.w1 : a.w2;
-  const uint8_t *rc[R], *rs[R];
+  const int64_t rows = GATED ? 2 * N : N;                     // of one expert
+  const Matrix weights(m.codes + e * rows * (K >> 1), m.scales + e * rows * (K >> 4), rows, K);
+  uint32_t row[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    int64_t n = n0 + 16 * (i % RO) + r;
-    n = n < N ? n : n0;                                       // rows past N: not stored
-    const int64_t row = (int64_t)e * (GATED ? 2 * N : N) + (i >= RO ? N : 0) + n;
-    rc[i] = m.codes + row * (K >> 1);
-    rs[i] = m.scales + row * (K >> 4);
+    const int64_t n = n0 + 16 * (i % RO) + r;
+    row[i] = (uint32_t)((i >= RO ? N : 0) + (n < N ? n : n0));      // rows past N: not stored
   }
+  if (threadIdx.x < 16) reinterpret_cast<uint32_t*>(zeros)[threadIdx.x] = 0u;
   const float gs = m.global_scale[e];
-  for (int q0 = p0; q0 < p1; q0 += 16 * C) {
-    int pair[C];
-    bool live[C];
-    float4v acc[R][C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int q = q0 + 16 * c + r;
-      live[c] = q < p1;
-      pair[c] = w.order[live[c] ? q : q0];
-#pragma unroll
-      for (int i = 0; i < R; ++i) acc[i][c] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-    float inv[C];                                             // undoes the column's power of two
+  for (int q0 = 0; q0 < count; q0 += cols) {
+    const int nc = count - q0 < cols ? count - q0 : cols;     // columns of this round
+    if (q0 > 0) mine = w.order[u * (int)kMoeMaxTokens + q0 + (r < nc ? r : 0)];
+    const bool live = r < nc;
+    const int pair = __shfl(mine, live ? r : 0);              // dead lanes: column 0's
+    float inv;                                                // undoes the column's power of two
+    float scale = 1.0f;
     if constexpr (UP) {
-      TokensHalf<C> tok;
-      tok.K = K;
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int t = pair[c] / a.top_k;
-        tok.row[c] = w.x16 + (int64_t)t * K;
-        tok.live[c] = live[c];
-        inv[c] = w.x_inv[t];
-      }
-      accumulate<R, C, K32>(rc, rs, K, wave, kWaves, tok, acc);
+      inv = w.x_inv[pair / a.top_k];
     } else {
-      TokensFloat<C> tok;
-      tok.K = K;
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const float s = half_scale(__uint_as_float(w.h_top[pair[c]]));
-        tok.row[c] = w.h + (int64_t)pair[c] * K;
-        tok.scale[c] = s;
-        tok.live[c] = live[c];
-        inv[c] = w.weights[pair[c]] / s;                      // s a power of two: exact
-      }
-      accumulate<R, C, K32>(rc, rs, K, wave, kWaves, tok, acc);
-    }
-    if (q0 != p0) __syncthreads();                            // the last round's sums have been read
-    put<R, C>(red, wave, acc);
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
+      // the columns' maxima over the fragments of h, column c's in lane c
       float top = 0.0f;
-#pragma unroll 1
-      for (int i = wave; i < RO; i += kWaves) {
-        const int64_t n = n0 + 16 * i + 4 * g;                // N % 16 == 0: all four rows or none
-        float4v v = take<kWaves, R, C>(red, i, c);
-        const float f = gs * inv[c];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] *= f;
-        if constexpr (UP) {
-          float4v z = v;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = act_of(a.act, z[q]);
-          if constexpr (GATED) {
-            const float4v up = take<kWaves, R, C>(red, i + RO, c);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] *= up[q] * f;
-          }
-#pragma unroll
-          for (int q = 0; q < 4; ++q) top = fmaxf(top, n < N ? fabsf(v[q]) : 0.0f);
-        }
-        float* out = (UP ? w.h : w.part) + (int64_t)pair[c] * N + n;
-        if (live[c] && n < N) *reinterpret_cast<float4v*>(out) = v;
+      for (int c = 0; c < nc; ++c) {
+        const float* frag = w.h_top + (int64_t)__builtin_amdgcn_readlane(pair, c) * (K / 16);
+        float t = 0.0f;
+        for (int64_t i = lane; i < K / 16; i += 64) t = fmaxf(t, frag[i]);
+        t = wave_fold_max(t);
+        top = r == c ? t : top;
       }
+      scale = half_scale(top);
+      inv = w.weights[pair] / scale;                          // a power of two: exact
+    }
+    float4v acc[R][1];
+#pragma unroll
+    for (int i = 0; i < R; ++i) acc[i][0] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+    Pipe<R, 1, K32, TokensLds> pipe;
+    for (int64_t k0 = 0; k0 < K; k0 += kChunk) {
+      const int64_t len = K - k0 < kChunk ? K - k0 : kChunk;
+      const int first = (int)(k0 / kStep) + wave;
+      TokensLds tok{live ? tokens + r * pitch : zeros, (uint32_t)k0, (uint32_t)K, live ? 0xFFFFFFFFu : 0u};
+      pipe.start(weights, row, tok, first, kWaves);
+      if (k0 > 0 || q0 > 0) __syncthreads();                  // the columns staged before have been read
+      // the columns' elements, 8 at a time, zeros up to a whole step; column c's pair and scale
+      // are in lane c of every wave
+      const int octets = (int)((len + kStep - 1) / kStep) * (kStep / 8);
+      for (int c = 0; c < nc; ++c) {
+        const int p = __builtin_amdgcn_readlane(pair, c);
+        const float s = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(scale), c));
+#pragma unroll 2
+        for (int o = threadIdx.x; o < octets; o += kThreads) {
+          half8 v{};
+          if (8 * o < len) {
+            if constexpr (UP) {
+              v = *reinterpret_cast<const half8*>(w.x16 + (int64_t)(p / a.top_k) * K + k0 + 8 * o);
+            } else {
+              const float* h = w.h + (int64_t)p * K + k0 + 8 * o;
+              const v4f32 x = ld_f32x4(h) * s, y = ld_f32x4(h + 4) * s;
+              v = half8{(_Float16)x[0], (_Float16)x[1], (_Float16)x[2], (_Float16)x[3],
+                        (_Float16)y[0], (_Float16)y[1], (_Float16)y[2], (_Float16)y[3]};
+            }
+          }
+          *reinterpret_cast<half8*>(tokens + c * pitch + 16 * o) = v;
+        }
+      }
+      __syncthreads();
+      pipe.run(weights, row, tok, first, kWaves, (int)((k0 + len + kStep - 1) / kStep), acc);
+    }
+    put<R, 1>(red, wave, acc);
+    __syncthreads();
+    if (wave < RO) {                                          // a wave per fragment of output rows
+      const int64_t n = n0 + 16 * wave + 4 * g;               // N % 16 == 0: all four rows or none
+      const float f = gs * inv;
+      float4v v = take<kWaves, R, 1>(red, wave, 0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] *= f;
       if constexpr (UP) {
-        // NaN is dropped by the maximum and stays in h; an infinite maximum gives scale 1
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = act_of(a.act, v[q]);
+        if constexpr (GATED) {
+          const float4v up = take<kWaves, R, 1>(red, wave + RO, 0);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] *= up[q] * f;
+        }
+        // this fragment's maximum; NaN is dropped by it and stays in h, an infinite one gives scale 1
+        float top = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) top = fmaxf(top, fabsf(v[q]));
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
-        if (live[c] && g == 0 && top > 0.0f) atomicMax(&w.h_top[pair[c]], __float_as_uint(top));
+        if (live && n < N) {
+          *reinterpret_cast<float4v*>(w.h + (int64_t)pair * N + n) = v;
+          if (g == 0) w.h_top[(int64_t)pair * (N / 16) + n / 16] = top;
+        }
+      } else if (live && n < N) {
+        uint64_t* out = reinterpret_cast<uint64_t*>(w.part + (int64_t)pair * N + n);
+        put_shared(out, (uint64_t)__float_as_uint(v[0]) | (uint64_t)__float_as_uint(v[1]) << 32);
+        put_shared(out + 1, (uint64_t)__float_as_uint(v[2]) | (uint64_t)__float_as_uint(v[3]) << 32);
       }
     }
+    // (the next round's first barrier, after its pipe.start, keeps put from overtaking take)
   }
   if constexpr (!UP) {
-    if (!last_to_finish(&w.counters[1 + kMoeMaxTokens / kGroupTokens + tile], used)) return;
-    const int rows = (int)(N - n0 < 16 * R ? N - n0 : 16 * R);
+    if (!last_to_finish(&w.counters[1 + kMoeMaxTokens / kGroupTokens + tile], *w.used)) return;
+    const int out_rows = (int)(N - n0 < 16 * R ? N - n0 : 16 * R);
     for (int i = threadIdx.x; i < a.tokens * 16 * R; i += kThreads) {
       const int t = i / (16 * R), n = i % (16 * R);
-      if (n >= rows) continue;
+      if (n >= out_rows) continue;
       const float* part = w.part + (int64_t)t * a.top_k * N + n0 + n;
       float s = 0.0f;
-      for (int j = 0; j < a.top_k; ++j) s += part[(int64_t)j * N];
+#pragma unroll 4
+      for (int j = 0; j < a.top_k; ++j) s += get_shared(&part[(int64_t)j * N]);
       a.y[(int64_t)t * a.ldy + n0 + n] = (uint16_t)bf16_rn_bits(s);
     }
   }
 }
 
-constexpr int kRows = 4;                                      // fragments of 16 rows per workgroup
+constexpr int kWideTokens = 4;
+constexpr int kRows = 2;                                      // fragments of 16 rows per workgroup
+constexpr int kMostLds = 8 * kRows * 64 * 16 + 64 + kCols * (2 * kChunk + 16);
 
 int64_t tiles_of(int64_t rows, int frags) { return (rows + 16 * frags - 1) / (16 * frags); }
 
-template <bool UP, bool GATED>
-void launch_expert(const MoeArgs& a, const MoeWork& w, hipStream_t stream) {
+template <bool UP, bool GATED, int W, bool K32>
+hipError_t launch_expert_as(const MoeArgs& a, const MoeWork& w, hipStream_t stream) {
+  // the staged columns can take more LDS than a launch may by default
+  static const hipError_t ready = hipFuncSetAttribute((const void*)k_expert<UP, GATED, kRows, W, K32>,
+                                                      hipFuncAttributeMaxDynamicSharedMemorySize, kMostLds);
+  if (ready != hipSuccess) return ready;
   const int64_t K = UP ? a.hidden : a.ffn, N = UP ? a.ffn : a.hidden;
   const int64_t pairs = (int64_t)a.tokens * a.top_k;
   const int64_t most = pairs < a.experts ? pairs : a.experts;
   const int tiles = (int)tiles_of(N, GATED ? kRows / 2 : kRows);
-  const dim3 grid((unsigned)(most * tiles));
-#define NVFP4_EX(C, K32) \
-  hipLaunchKernelGGL((k_expert<UP, GATED, kRows, C, K32>), grid, dim3(kThreads), 0, stream, a, w, tiles)
-  if (a.tokens <= 16) {
-    if (K % 32 == 0) NVFP4_EX(1, true); else NVFP4_EX(1, false);
-  } else {
-    if (K % 32 == 0) NVFP4_EX(2, true); else NVFP4_EX(2, false);
-  }
-#undef NVFP4_EX
+  const int cols = a.tokens < kCols ? a.tokens : kCols;
+  const int64_t staged = K < kChunk ? (K + kStep - 1) / kStep * kStep : kChunk;
+  const uint32_t pitch = (uint32_t)(2 * staged + 16);         // rows start 4 banks apart
+  const size_t bytes = (size_t)W * kRows * 64 * 16 + 64 + (size_t)cols * pitch;
+  hipLaunchKernelGGL((k_expert<UP, GATED, kRows, W, K32>), dim3((unsigned)(most * tiles)), dim3(64 * W), bytes, stream,
+                     a, w, tiles, cols, pitch);
+  return hipSuccess;
+}
+
+template <bool UP, bool GATED>
+hipError_t launch_expert(const MoeArgs& a, const MoeWork& w, hipStream_t stream) {
+  const bool k32 = (UP ? a.hidden : a.ffn) % 32 == 0;
+  const bool wide = a.tokens <= kWideTokens;
+  if (wide) return k32 ? launch_expert_as<UP, GATED, 8, true>(a, w, stream) : launch_expert_as<UP, GATED, 8, false>(a, w, stream);
+  return k32 ? launch_expert_as<UP, GATED, 4, true>(a, w, stream) : launch_expert_as<UP, GATED, 4, false>(a, w, stream);
 }
 
 }  // namespace
@@ -472,13 +506,13 @@ size_t moe_layout(const MoeArgs& a, uint8_t* base, MoeWork* w) {
   x.counters = reinterpret_cast<int*>(part(moe_counter_bytes(a.hidden)));
   x.used = reinterpret_cast<int*>(part(4));
   x.expert = reinterpret_cast<int*>(part(4 * E));
-  x.begin = reinterpret_cast<int*>(part(4 * (E + 1)));
-  x.order = reinterpret_cast<int*>(part(4 * P));
+  x.count = reinterpret_cast<int*>(part(4 * E));
+  x.order = reinterpret_cast<int*>(part(4 * (P < E ? P : E) * (size_t)kMoeMaxTokens));
   x.ids = reinterpret_cast<int*>(part(4 * P));
   x.weights = reinterpret_cast<float*>(part(4 * P));
   x.logits = reinterpret_cast<float*>(part(4 * T * E));
   x.x_inv = reinterpret_cast<float*>(part(4 * T));
-  x.h_top = reinterpret_cast<uint32_t*>(part(4 * P));
+  x.h_top = reinterpret_cast<float*>(part(4 * P * (size_t)a.ffn / 16));
   x.x16 = reinterpret_cast<_Float16*>(part(2 * T * (size_t)a.hidden));
   x.h = reinterpret_cast<float*>(part(4 * P * (size_t)a.ffn));
   x.part = reinterpret_cast<float*>(part(4 * P * (size_t)a.hidden));
@@ -497,13 +531,18 @@ hipError_t launch_moe(const MoeArgs& a, uint8_t* ws, hipStream_t stream) {
   moe_layout(a, ws, &w);
   const bool vec_x = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx % 8 == 0;
   const bool vec_r = reinterpret_cast<uintptr_t>(a.router) % 16 == 0;      // hidden % 16 == 0
-  const dim3 grid((unsigned)((a.experts + kWaves - 1) / kWaves + 1),
+  const dim3 grid((unsigned)((a.experts + kRouteExperts - 1) / kRouteExperts + kGroupTokens),
                   (unsigned)((a.tokens + kGroupTokens - 1) / kGroupTokens));
-  if (a.router_f32) hipLaunchKernelGGL(k_route<true>, grid, dim3(kThreads), 0, stream, a, w, vec_x, vec_r);
-  else hipLaunchKernelGGL(k_route<false>, grid, dim3(kThreads), 0, stream, a, w, vec_x, vec_r);
-  if (a.gated) launch_expert<true, true>(a, w, stream);
-  else launch_expert<true, false>(a, w, stream);
-  launch_expert<false, false>(a, w, stream);
+#define NVFP4_RT(F32, NT) \
+  hipLaunchKernelGGL((k_route<F32, NT>), grid, dim3(kRouteThreads), 0, stream, a, w, vec_x, vec_r)
+  if (a.tokens == 1) {
+    if (a.router_f32) NVFP4_RT(true, 1); else NVFP4_RT(false, 1);
+  } else {
+    if (a.router_f32) NVFP4_RT(true, 8); else NVFP4_RT(false, 8);
+  }
+#undef NVFP4_RT
+  hipError_t e = a.gated ? launch_expert<true, true>(a, w, stream) : launch_expert<true, false>(a, w, stream);
+  if (e != hipSuccess || (e = launch_expert<false, false>(a, w, stream)) != hipSuccess) return e;
   return hipGetLastError();
 }
 

@@ -10,10 +10,11 @@
 // result holds column l % 16, rows 4 g .. 4 g + 3. Codes decode to FP16 exactly (e2m1 * e4m3 has at
 // most 6 significant bits in [2^-10, 2688]), products are exact, sums FP32.
 //
-// A workgroup takes 16 R rows; its waves share them and split K, every wave the next step in
-// turn (together they read whole 256-byte runs of each row), and add up through LDS in a fixed
-// order. Everything goes straight from memory to registers, the next step's loads ahead of this
-// step's arithmetic: no element is used twice in a workgroup.
+// A workgroup takes 16 R rows; its W waves share them and split K, every wave the next step in
+// turn (together they read whole runs of each row), and add up through LDS in a fixed order.
+// Everything goes straight from memory to registers, kAhead steps of the weights in flight per
+// wave: no element is used twice in a workgroup, and what such a product waits for is HBM's
+// latency (about 2 us under load, so 5 TB/s want 40 KB in flight on every CU).
 #pragma once
 
 #include "device_common.h"
@@ -26,6 +27,7 @@ typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float float4v __attribute__((ext_vector_type(4)));
 
 constexpr int kStep = 128;
+constexpr int kAhead = 4;
 
 // FP16 pair (S * 2^-8 twice) of an E4M3 scale code, and 8 codes as e2m1 * S (the conversion's own
 // scale operand returns the 2^8).
@@ -39,78 +41,124 @@ __device__ __forceinline__ half8 decode8(uint32_t codes, half2v s2) {
   return half8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// The 32 codes of one row at element k (a multiple of 32) and their two scale bytes, with zero
-// scales at and past K, which zero whatever the codes are. k past K reads the row's start instead.
-struct Run { v4u32 codes; uint32_t scales; };
+// Loads go through a buffer resource over a matrix (below 2 GiB) with one 32-bit offset a lane: a lane
+// without an element gives an offset past any buffer and gets zeros, so there are no branches
+// around the loads and nothing to clear afterwards.
+constexpr uint32_t kBeyond = 0x80000000u;
 
-// K32: K is a multiple of 32 (rows of codes start on 16 bytes, of scales on 2).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int64_t bytes) {
+  // base and size made scalar: they are uniform, which the compiler cannot always see
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(((uint64_t)hi << 32) | lo), (short)0,
+                                           (int)__builtin_amdgcn_readfirstlane((uint32_t)bytes), 0x00020000);
+}
+
+__device__ __forceinline__ v4u32 load16(__amdgpu_buffer_rsrc_t b, uint32_t at) {
+  return __builtin_bit_cast(v4u32, __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, 0));
+}
+
+// An NVFP4 matrix [rows, K].
+struct Matrix {
+  __amdgpu_buffer_rsrc_t codes, scales;
+  uint32_t K;
+  __device__ __forceinline__ Matrix(const uint8_t* c, const uint8_t* s, int64_t rows, int64_t k)
+      : codes(buffer(c, rows * (k >> 1))), scales(buffer(s, rows * (k >> 4))), K((uint32_t)k) {}
+};
+
+// The 32 codes of one row at element k (a multiple of 32) and their two scale bytes: zeros at and
+// past K and without a row.
+// K32: K is a multiple of 32 (rows of codes start on 16 bytes, of scales on 2). Values are kept as
+// they are loaded: arithmetic on one, even a widening, would wait for it where it is loaded.
 template <bool K32>
-__device__ __forceinline__ Run load_run(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                                        int64_t K, int64_t k) {
-  Run r;
+struct Run {
+  v4u32 codes;
+  uint16_t scales;                                            // both
+};
+template <>
+struct Run<false> {
+  v2u32 lo, hi;
+  uint8_t s0, s1;
+};
+
+template <bool K32>
+__device__ __forceinline__ Run<K32> load_run(const Matrix& m, uint32_t row, bool live, uint32_t k) {
+  Run<K32> r;
+  const uint32_t c = row * (m.K >> 1) + (k >> 1), s = row * (m.K >> 4) + (k >> 4);
+  const bool a = live && k < m.K;
   if constexpr (K32) {
-    const int64_t at = k < K ? k : 0;
-    r.codes = ld_u32x4(codes + (at >> 1));
-    const uint32_t s = *reinterpret_cast<const uint16_t*>(scales + (at >> 4));
-    r.scales = k < K ? s : 0u;
+    r.codes = load16(m.codes, a ? c : kBeyond);
+    r.scales = __builtin_amdgcn_raw_buffer_load_b16(m.scales, a ? s : kBeyond, 0, 0);
   } else {
-    const int64_t a = k < K ? k : 0, b = k + 16 < K ? k + 16 : 0;
-    const v2u32 lo = *reinterpret_cast<const v2u32*>(codes + (a >> 1));
-    const v2u32 hi = *reinterpret_cast<const v2u32*>(codes + (b >> 1));
-    r.codes = v4u32{lo.x, lo.y, hi.x, hi.y};
-    const uint32_t s0 = scales[a >> 4], s1 = scales[b >> 4];
-    r.scales = (k < K ? s0 : 0u) | (k + 16 < K ? s1 << 8 : 0u);
+    const bool b = live && k + 16 < m.K;
+    r.lo = __builtin_bit_cast(v2u32, __builtin_amdgcn_raw_buffer_load_b64(m.codes, a ? c : kBeyond, 0, 0));
+    r.hi = __builtin_bit_cast(v2u32, __builtin_amdgcn_raw_buffer_load_b64(m.codes, b ? c + 8 : kBeyond, 0, 0));
+    r.s0 = __builtin_amdgcn_raw_buffer_load_b8(m.scales, a ? s : kBeyond, 0, 0);
+    r.s1 = __builtin_amdgcn_raw_buffer_load_b8(m.scales, b ? s + 1 : kBeyond, 0, 0);
   }
   return r;
 }
 
-__device__ __forceinline__ half8 octet(const Run& r, int t) {
-  return decode8(r.codes[t], scale_pair((r.scales >> (8 * (t >> 1))) & 0xFFu));
+__device__ __forceinline__ half8 octet_of(const Run<true>& r, int t) {
+  return decode8(r.codes[t], scale_pair((uint32_t)(r.scales >> (8 * (t >> 1))) & 0xFFu));
+}
+__device__ __forceinline__ half8 octet_of(const Run<false>& r, int t) {
+  return decode8(t < 2 ? r.lo[t & 1] : r.hi[t & 1], scale_pair(t < 2 ? r.s0 : r.s1));
 }
 
 // acc[i][c] += rows 16 i .. + 15 of the tile times token columns 16 c .. + 15, over the steps
-// first, first + stride, ... below K. row_codes / row_scales: this lane's row of each fragment.
-// Tok: load(c, k) -> Raw (the lane's 32 elements of column 16 c + l % 16 at element k, 0 past K or
-// without a token), octet(c, raw, t) -> half8.
+// first, first + stride, ... below `steps` (of kStep elements from element 0). row: this lane's row
+// of each fragment. Tok: load(c, k) -> Raw, what the lane needs of column 16 c + l % 16 for its 32
+// elements at k; octet(raw, k, t) -> half8, zeros past K or without a token.
+// Loads return in the order of issue and the wait counts the younger ones, so a step's loads stay
+// together and in step order (the scheduling barriers), the tokens as far ahead as the weights.
 template <int R, int C, bool K32, class Tok>
-__device__ __forceinline__ void accumulate(const uint8_t* const (&row_codes)[R], const uint8_t* const (&row_scales)[R],
-                                           int64_t K, int first, int stride, const Tok& tok, float4v (&acc)[R][C]) {
-  const int g = (threadIdx.x & 63) >> 4;
-  const int steps = (int)((K + kStep - 1) / kStep);
-  Run w[R];
-  typename Tok::Raw x[C];
-  int64_t k = (int64_t)first * kStep + g * 32;
+struct Pipe {
+  Run<K32> w[kAhead][R];
+  typename Tok::Raw x[kAhead][C];
+
+  __device__ __forceinline__ void load(const Matrix& m, const uint32_t (&row)[R], const Tok& tok, int d, int s) {
+    const uint32_t k = (uint32_t)s * kStep + ((threadIdx.x & 63) >> 4) * 32;
 #pragma unroll
-  for (int i = 0; i < R; ++i) w[i] = load_run<K32>(row_codes[i], row_scales[i], K, k);
+    for (int c = 0; c < C; ++c) x[d][c] = tok.load(c, k);
 #pragma unroll
-  for (int c = 0; c < C; ++c) x[c] = tok.load(c, k);
+    for (int i = 0; i < R; ++i) w[d][i] = load_run<K32>(m, row[i], true, k);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  __device__ __forceinline__ void start(const Matrix& m, const uint32_t (&row)[R], const Tok& tok, int first, int stride) {
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) load(m, row, tok, d, first + d * stride);
+  }
+
+  __device__ __forceinline__ void run(const Matrix& m, const uint32_t (&row)[R], const Tok& tok, int first, int stride,
+                                      int steps, float4v (&acc)[R][C]) {
 #pragma unroll 1
-  for (int s = first; s < steps; s += stride) {
-    k += (int64_t)stride * kStep;                             // past K: the loads below give zeros
-    Run wn[R];
-    typename Tok::Raw xn[C];
+    for (int s0 = first; s0 < steps; s0 += kAhead * stride) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) wn[i] = load_run<K32>(row_codes[i], row_scales[i], K, k);
+      for (int d = 0; d < kAhead; ++d) {
+        const int s = s0 + d * stride;
+        if (s >= steps) return;                               // uniform (a break would look like another turn)
+        const uint32_t k = (uint32_t)s * kStep + ((threadIdx.x & 63) >> 4) * 32;
 #pragma unroll
-    for (int c = 0; c < C; ++c) xn[c] = tok.load(c, k);
+        for (int t = 0; t < 4; ++t) {
+          half8 b[C];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      half8 b[C];
+          for (int c = 0; c < C; ++c) b[c] = tok.octet(x[d][c], k, t);
 #pragma unroll
-      for (int c = 0; c < C; ++c) b[c] = tok.octet(c, x[c], t);
+          for (int i = 0; i < R; ++i) {
+            const half8 a = octet_of(w[d][i], t);
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const half8 a = octet(w[i], t);
-#pragma unroll
-        for (int c = 0; c < C; ++c) acc[i][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b[c], acc[i][c], 0, 0, 0);
+            for (int c = 0; c < C; ++c)
+              acc[i][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b[c], acc[i][c], 0, 0, 0);
+          }
+        }
+        load(m, row, tok, d, s + kAhead * stride);
       }
     }
-#pragma unroll
-    for (int i = 0; i < R; ++i) w[i] = wn[i];
-#pragma unroll
-    for (int c = 0; c < C; ++c) x[c] = xn[c];
   }
-}
+};
 
 // Each wave's sums into LDS (W waves x R C fragments of 64 x 4 floats), then fragment f summed over
 // the waves in order. All threads call put, then a barrier, then take.

@@ -458,7 +458,8 @@ typedef struct nvfp4_moe {
  * A token's result does not depend on the other tokens of the call, nor on the order in which
  * workgroups finish. Non-finite values of one token stay with that token. Errors:
  * NVFP4_ERR_INVALID (null or misaligned pointers, shapes, strides, enums), NVFP4_ERR_UNSUPPORTED
- * (more than 64 tokens, 512 experts or top_k 16), NVFP4_ERR_WORKSPACE, NVFP4_ERR_HIP.
+ * (more than 64 tokens, 512 experts or top_k 16, hidden or ffn above 2^18, an expert matrix's codes
+ * above 2 GiB), NVFP4_ERR_WORKSPACE, NVFP4_ERR_HIP.
  */
 int nvfp4_moe_tokens(const nvfp4_moe* moe, const uint16_t* x, int64_t tokens, int64_t ldx, uint16_t* y, int64_t ldy,
                      int32_t* ids_out, float* weights_out, void* workspace, size_t ws_bytes, void* hip_stream);
