@@ -7,6 +7,8 @@
 // keeps 8 columns' sums in registers. The waves' sums meet in LDS, the row runs' sums in the
 // workspace (or go straight to dbias where one run covers all rows), both added in a fixed
 // order, so the sums do not change from run to run.
+#include <type_traits>
+
 #include "activation.h"
 #include "launch.h"
 
@@ -17,48 +19,35 @@ constexpr int kThreads = 256;
 constexpr int kCols = 512;                                    // 64 lanes x 8
 constexpr int kWaves = kThreads / 64;
 
-// VEC: a lane holds 8 consecutive columns, moved as whole vectors (N, the row strides and the
-// pointers are multiples of 8 elements); otherwise columns lane, lane + 64, ..., one element each.
-template <bool VEC>
-__device__ __forceinline__ int64_t col_of(int64_t c0, int lane, int q) {
-  return VEC ? c0 + lane * 8 + q : c0 + lane + 64 * q;
-}
-
-template <bool F32, bool VEC>
-__device__ __forceinline__ void load_row(const void* p, int64_t row, int64_t ld, int64_t c0, int64_t N, int lane,
-                                         float (&v)[8]) {
-  if constexpr (VEC) {
-    const int64_t c = c0 + lane * 8;
-    if (c >= N) {
+// Eight consecutive columns of a row, WHOLE: as whole vectors from wherever the row starts; else the
+// last `left` < 8 columns of a row one by one, 0 past them.
+template <bool F32, bool WHOLE>
+__device__ __forceinline__ void load_row(const void* p, int64_t at, int left, float (&v)[8]) {
+  if constexpr (WHOLE && F32) {
+    const float* f = static_cast<const float*>(p) + at;
+    const v4f32 a = *reinterpret_cast<const v4f32_any*>(f), b = *reinterpret_cast<const v4f32_any*>(f + 4);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = 0.0f;
-    } else if constexpr (F32) {
-      const float* f = static_cast<const float*>(p) + row * ld + c;
-      const v4f32 a = ld_f32x4(f), b = ld_f32x4(f + 4);
+    for (int q = 0; q < 4; ++q) {
+      v[q] = a[q];
+      v[q + 4] = b[q];
+    }
+  } else if constexpr (WHOLE) {
+    const v4u32 w = *reinterpret_cast<const v4u32_any*>(static_cast<const uint16_t*>(p) + at);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        v[q] = a[q];
-        v[q + 4] = b[q];
-      }
-    } else {
-      const v4u32 w = ld_u32x4(static_cast<const uint16_t*>(p) + row * ld + c);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        v[2 * q] = bf16_lo(w[q]);
-        v[2 * q + 1] = bf16_hi(w[q]);
-      }
+    for (int q = 0; q < 4; ++q) {
+      v[2 * q] = bf16_lo(w[q]);
+      v[2 * q + 1] = bf16_hi(w[q]);
     }
   } else {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const int64_t c = col_of<false>(c0, lane, q);
-      if constexpr (F32) v[q] = c < N ? static_cast<const float*>(p)[row * ld + c] : 0.0f;
-      else v[q] = c < N ? bf16_lo(static_cast<const uint16_t*>(p)[row * ld + c]) : 0.0f;
+      v[q] = 0.0f;
+      if (q < left) v[q] = F32 ? static_cast<const float*>(p)[at + q] : bf16_lo(static_cast<const uint16_t*>(p)[at + q]);
     }
   }
 }
 
-template <int ACT, bool F32, bool VEC>
+template <int ACT, bool F32>
 __global__ __launch_bounds__(kThreads) void k_act_grad(const void* __restrict__ dy, int64_t ldy,
                                                        const uint16_t* __restrict__ z, int64_t ldz,
                                                        uint16_t* __restrict__ dz, int64_t lddz, int64_t M, int64_t N,
@@ -69,35 +58,41 @@ __global__ __launch_bounds__(kThreads) void k_act_grad(const void* __restrict__ 
   const int64_t c0 = (int64_t)blockIdx.x * kCols;
   const int64_t r0 = (int64_t)blockIdx.y * rows, r1 = r0 + rows < M ? r0 + rows : M;
   float sum[8] = {};
+  const int64_t c = c0 + lane * 8;
+  auto walk = [&](auto whole) {
+    constexpr bool WHOLE = decltype(whole)::value;
+    const int left = (int)(N - c < 8 ? N - c : 8);
 #pragma unroll 4
-  for (int64_t r = r0 + wave; r < r1; r += kWaves) {
-    float g[8];
-    load_row<F32, VEC>(dy, r, ldy, c0, N, lane, g);
-    if constexpr (ACT != kActNone) {
-      float x[8];
-      load_row<false, VEC>(z, r, ldz, c0, N, lane, x);
+    for (int64_t r = r0 + wave; r < r1; r += kWaves) {
+      float g[8];
+      load_row<F32, WHOLE>(dy, r * ldy + c, left, g);
+      if constexpr (ACT != kActNone) {
+        float x[8];
+        load_row<false, WHOLE>(z, r * ldz + c, left, x);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) g[q] *= act_slope<ACT>(x[q]);
-    }
+        for (int q = 0; q < 8; ++q) g[q] *= act_slope<ACT>(x[q]);
+      }
 #pragma unroll
-    for (int q = 0; q < 8; ++q) sum[q] += g[q];
-    if (dz != nullptr) {
-      if constexpr (VEC) {
-        if (c0 + lane * 8 < N)
-          *reinterpret_cast<v4u32*>(dz + r * lddz + c0 + lane * 8) =
-              v4u32{bf16_rn_pair(g[0], g[1]), bf16_rn_pair(g[2], g[3]), bf16_rn_pair(g[4], g[5]), bf16_rn_pair(g[6], g[7])};
-      } else {
+      for (int q = 0; q < 8; ++q) sum[q] += g[q];
+      if (dz != nullptr) {
+        const v4u32 w = {bf16_rn_pair(g[0], g[1]), bf16_rn_pair(g[2], g[3]), bf16_rn_pair(g[4], g[5]),
+                         bf16_rn_pair(g[6], g[7])};
+        uint16_t* out = dz + r * lddz + c;
+        if constexpr (WHOLE) {
+          *reinterpret_cast<v4u32_any*>(out) = w;
+        } else {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int64_t c = col_of<false>(c0, lane, q);
-          if (c < N) dz[r * lddz + c] = (uint16_t)bf16_rn_pair(g[q], 0.0f);
+          for (int q = 0; q < 8; ++q)
+            if (q < left) out[q] = (uint16_t)(w[q >> 1] >> (16 * (q & 1)));
         }
       }
     }
-  }
+  };
+  if (c + 8 <= N) walk(std::true_type{});
+  else if (c < N) walk(std::false_type{});
   if (sums == nullptr) return;                                // uniform
 #pragma unroll
-  for (int q = 0; q < 8; ++q) red[wave][VEC ? lane * 8 + q : lane + 64 * q] = sum[q];
+  for (int q = 0; q < 8; ++q) red[wave][lane * 8 + q] = sum[q];
   __syncthreads();
   for (int i = threadIdx.x; i < kCols; i += kThreads) {
     if (c0 + i < N) {
@@ -157,12 +152,9 @@ hipError_t launch_act_grad(const void* dy, bool fp32, int64_t ldy, const uint16_
   const int64_t rows = rows_per_run(M, N), runs = (M + rows - 1) / rows;
   float* sums = dbias ? (runs > 1 ? ws : dbias) : nullptr;
   const int add = accumulate && runs == 1;
-  auto ok = [&](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; };
-  const bool vec = N % 8 == 0 && ok(dy, ldy) && ok(z, z ? ldz : 0) && ok(dz, dz ? lddz : 0);
   const dim3 grid((unsigned)((N + kCols - 1) / kCols), (unsigned)runs);
-#define NVFP4_AG3(A, F, V) \
-  hipLaunchKernelGGL((k_act_grad<A, F, V>), grid, dim3(kThreads), 0, stream, dy, ldy, z, ldz, dz, lddz, M, N, rows, sums, add)
-#define NVFP4_AG2(A, F) do { if (vec) NVFP4_AG3(A, F, true); else NVFP4_AG3(A, F, false); } while (0)
+#define NVFP4_AG2(A, F) \
+  hipLaunchKernelGGL((k_act_grad<A, F>), grid, dim3(kThreads), 0, stream, dy, ldy, z, ldz, dz, lddz, M, N, rows, sums, add)
 #define NVFP4_AG(A) do { if (fp32) NVFP4_AG2(A, true); else NVFP4_AG2(A, false); } while (0)
   switch (act) {
     case kActRelu2: NVFP4_AG(kActRelu2); break;
@@ -172,7 +164,6 @@ hipError_t launch_act_grad(const void* dy, bool fp32, int64_t ldy, const uint16_
   }
 #undef NVFP4_AG
 #undef NVFP4_AG2
-#undef NVFP4_AG3
   if (dbias && runs > 1)
     hipLaunchKernelGGL(k_column_sums, dim3((unsigned)((N + 63) / 64)), dim3(kThreads), 0, stream, ws, runs, N, dbias,
                        accumulate ? 1 : 0);

@@ -33,11 +33,11 @@ constexpr int64_t kPass = (int64_t)kThreads * kPer;
 
 struct Elems { float v[kPer]; };
 
-// Elements [i, i + 8) of a tensor of n (0 past its end). vec: aligned for whole-vector access.
-__device__ __forceinline__ Elems load_f32(const float* p, int64_t i, int64_t n, bool vec) {
+// Elements [i, i + 8) of a tensor of n, as whole vectors from any element boundary; 0 past its end.
+__device__ __forceinline__ Elems load_f32(const float* p, int64_t i, int64_t n) {
   Elems e;
-  if (vec && i + kPer <= n) {
-    const v4f32 a = ld_f32x4(p + i), b = ld_f32x4(p + i + 4);
+  if (i + kPer <= n) {
+    const v4f32 a = *reinterpret_cast<const v4f32_any*>(p + i), b = *reinterpret_cast<const v4f32_any*>(p + i + 4);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       e.v[q] = a[q];
@@ -50,10 +50,10 @@ __device__ __forceinline__ Elems load_f32(const float* p, int64_t i, int64_t n, 
   return e;
 }
 
-__device__ __forceinline__ void store_f32(float* p, int64_t i, int64_t n, bool vec, const Elems& e) {
-  if (vec && i + kPer <= n) {
-    *reinterpret_cast<v4f32*>(p + i) = v4f32{e.v[0], e.v[1], e.v[2], e.v[3]};
-    *reinterpret_cast<v4f32*>(p + i + 4) = v4f32{e.v[4], e.v[5], e.v[6], e.v[7]};
+__device__ __forceinline__ void store_f32(float* p, int64_t i, int64_t n, const Elems& e) {
+  if (i + kPer <= n) {
+    *reinterpret_cast<v4f32_any*>(p + i) = v4f32{e.v[0], e.v[1], e.v[2], e.v[3]};
+    *reinterpret_cast<v4f32_any*>(p + i + 4) = v4f32{e.v[4], e.v[5], e.v[6], e.v[7]};
   } else {
 #pragma unroll
     for (int q = 0; q < kPer; ++q)
@@ -61,12 +61,12 @@ __device__ __forceinline__ void store_f32(float* p, int64_t i, int64_t n, bool v
   }
 }
 
-__device__ __forceinline__ Elems load_grad(const void* p, bool bf16, int64_t i, int64_t n, bool vec) {
-  if (!bf16) return load_f32(static_cast<const float*>(p), i, n, vec);
+__device__ __forceinline__ Elems load_grad(const void* p, bool bf16, int64_t i, int64_t n) {
+  if (!bf16) return load_f32(static_cast<const float*>(p), i, n);
   Elems e;
   const uint16_t* h = static_cast<const uint16_t*>(p);
-  if (vec && i + kPer <= n) {
-    const v4u32 w = ld_u32x4(h + i);
+  if (i + kPer <= n) {
+    const v4u32 w = *reinterpret_cast<const v4u32_any*>(h + i);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       e.v[2 * q] = bf16_lo(w[q]);
@@ -80,7 +80,7 @@ __device__ __forceinline__ Elems load_grad(const void* p, bool bf16, int64_t i, 
 }
 
 // Stores e rounded to BF16; returns the largest stored magnitude.
-__device__ __forceinline__ float store_bf16(uint16_t* p, int64_t i, int64_t n, bool vec, const Elems& e) {
+__device__ __forceinline__ float store_bf16(uint16_t* p, int64_t i, int64_t n, const Elems& e) {
   v4u32 w;
   float mx = 0.0f;
 #pragma unroll
@@ -88,8 +88,8 @@ __device__ __forceinline__ float store_bf16(uint16_t* p, int64_t i, int64_t n, b
     w[q] = bf16_rn_pair(e.v[2 * q], e.v[2 * q + 1]);
     mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[q])), fabsf(bf16_hi(w[q]))));
   }
-  if (vec && i + kPer <= n) {
-    *reinterpret_cast<v4u32*>(p + i) = w;
+  if (i + kPer <= n) {
+    *reinterpret_cast<v4u32_any*>(p + i) = w;
   } else {
 #pragma unroll
     for (int q = 0; q < kPer; ++q)
@@ -101,9 +101,9 @@ __device__ __forceinline__ float store_bf16(uint16_t* p, int64_t i, int64_t n, b
 // ---- 8-bit states ----------------------------------------------------------------------------
 struct Codes { uint32_t lo, hi; };                            // 8 codes, element 0 in the low byte
 
-__device__ __forceinline__ Codes load_codes(const uint8_t* p, int64_t i, int64_t n, bool vec) {
-  if (vec && i + kPer <= n) {
-    const v2u32 w = *reinterpret_cast<const v2u32*>(p + i);
+__device__ __forceinline__ Codes load_codes(const uint8_t* p, int64_t i, int64_t n) {
+  if (i + kPer <= n) {
+    const v2u32 w = *reinterpret_cast<const v2u32_any*>(p + i);
     return Codes{w.x, w.y};
   }
   Codes c{0, 0};
@@ -115,9 +115,9 @@ __device__ __forceinline__ Codes load_codes(const uint8_t* p, int64_t i, int64_t
   return c;
 }
 
-__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int64_t n, bool vec, Codes c) {
-  if (vec && i + kPer <= n) {
-    *reinterpret_cast<v2u32*>(p + i) = v2u32{c.lo, c.hi};
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int64_t n, Codes c) {
+  if (i + kPer <= n) {
+    *reinterpret_cast<v2u32_any*>(p + i) = v2u32{c.lo, c.hi};
   } else {
 #pragma unroll
     for (int q = 0; q < kPer; ++q)
@@ -205,13 +205,13 @@ __global__ __launch_bounds__(kThreads) void k_grad_norm(const AdamWEntry* __rest
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     const AdamWEntry& t = table[chunk_of[c]];
     const int64_t n = t.n, c0 = (c - t.first_chunk) * kAdamWChunk;
-    const bool vec = t.flags & kAdamWAligned, bf16 = t.flags & kAdamWGradBf16;
+    const bool bf16 = t.flags & kAdamWGradBf16;
     float s = 0.0f;
 #pragma unroll
     for (int64_t o = 0; o < kAdamWChunk; o += kPass) {
       const int64_t i = c0 + o + (int64_t)threadIdx.x * kPer;
       if (i < n) {
-        const Elems g = load_grad(t.grad, bf16, i, n, vec);
+        const Elems g = load_grad(t.grad, bf16, i, n);
 #pragma unroll
         for (int q = 0; q < kPer; ++q) s += g.v[q] * g.v[q];
       }
@@ -230,7 +230,7 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const AdamWEntry* __restrict
   const int32_t ti = chunk_of[blockIdx.x];
   const AdamWEntry& t = table[ti];
   const int64_t n = t.n, c0 = ((int64_t)blockIdx.x - t.first_chunk) * kAdamWChunk;
-  const bool vec = t.flags & kAdamWAligned, bf16 = t.flags & kAdamWGradBf16;
+  const bool bf16 = t.flags & kAdamWGradBf16;
   float clip = 1.0f;
   bool skip = false;                                          // uniform
   if (parts > 0) {
@@ -246,14 +246,14 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const AdamWEntry* __restrict
 #pragma unroll 1
   for (int64_t o = 0; o < kAdamWChunk && c0 + o < n; o += kPass) {
     const int64_t i = c0 + o + (int64_t)threadIdx.x * kPer;   // lanes past n carry zeros to the shuffles
-    Elems p = load_f32(t.p, i, n, vec);
-    const Elems grad = load_grad(t.grad, bf16, i, n, vec);
+    Elems p = load_f32(t.p, i, n);
+    const Elems grad = load_grad(t.grad, bf16, i, n);
     Elems m, v;
     Codes mc{0, 0}, rc{0, 0};
     uint32_t ms = 0, rs = 0;
     if constexpr (EIGHT) {
-      mc = load_codes(static_cast<const uint8_t*>(t.m), i, n, vec);
-      rc = load_codes(static_cast<const uint8_t*>(t.v), i, n, vec);
+      mc = load_codes(static_cast<const uint8_t*>(t.m), i, n);
+      rc = load_codes(static_cast<const uint8_t*>(t.v), i, n);
       if (i < n) {
         ms = t.m_scale[i >> 5];
         rs = t.v_scale[i >> 5];
@@ -261,8 +261,8 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const AdamWEntry* __restrict
       m = decode_codes(mc, e8m0_value(ms));
       v = decode_codes(rc, e8m0_value(rs));
     } else {
-      m = load_f32(static_cast<const float*>(t.m), i, n, vec);
-      v = load_f32(static_cast<const float*>(t.v), i, n, vec);
+      m = load_f32(static_cast<const float*>(t.m), i, n);
+      v = load_f32(static_cast<const float*>(t.v), i, n);
     }
     if (!skip) {
       Elems r;
@@ -286,25 +286,25 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const AdamWEntry* __restrict
       }
     }
     if (i < n) {
-      store_f32(t.p_out, i, n, vec, p);
+      store_f32(t.p_out, i, n, p);
       float big = 0.0f;
       if (t.w_out != nullptr) {
-        big = store_bf16(t.w_out, i, n, vec, p);
+        big = store_bf16(t.w_out, i, n, p);
       } else {
 #pragma unroll
         for (int q = 0; q < kPer; ++q) big = fmaxf(big, fabsf(p.v[q]));
       }
       mx = fmaxf(mx, big);
       if constexpr (EIGHT) {
-        store_codes(static_cast<uint8_t*>(t.m_out), i, n, vec, mc);
-        store_codes(static_cast<uint8_t*>(t.v_out), i, n, vec, rc);
+        store_codes(static_cast<uint8_t*>(t.m_out), i, n, mc);
+        store_codes(static_cast<uint8_t*>(t.v_out), i, n, rc);
         if ((i & 31) == 0) {
           t.m_scale_out[i >> 5] = (uint8_t)ms;
           t.v_scale_out[i >> 5] = (uint8_t)rs;
         }
       } else {
-        store_f32(static_cast<float*>(t.m_out), i, n, vec, m);
-        store_f32(static_cast<float*>(t.v_out), i, n, vec, v);
+        store_f32(static_cast<float*>(t.m_out), i, n, m);
+        store_f32(static_cast<float*>(t.v_out), i, n, v);
       }
     }
   }

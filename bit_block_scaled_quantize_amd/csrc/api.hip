@@ -515,7 +515,7 @@ int nvfp4_gemm_act(const nvfp4_tensor* A, const nvfp4_tensor* B, uint16_t* D, in
     return fail(NVFP4_ERR_WORKSPACE, "workspace of %zu bytes (256-byte aligned) required, got %zu", need, workspace ? ws_bytes : (size_t)0);
   const nvfp4::GemmOperand a{A->codes, A->scales, A->global_scale};
   const nvfp4::GemmOperand b{B->codes, B->scales, B->global_scale};
-  const nvfp4::ActOut out{bias, residual, preact, ldr, ldp, bias_dt == NVFP4_IN_FP32, false};
+  const nvfp4::ActOut out{bias, residual, preact, ldr, ldp, bias_dt == NVFP4_IN_FP32};
   return hip_status(nvfp4::launch_gemm_act(a, b, A->rows, N, A->cols, (int)act, out, D, ldd, amax_out,
                                            static_cast<float*>(workspace), (hipStream_t)hip_stream), "gemm_act");
 }
@@ -649,11 +649,7 @@ int nvfp4_adamw_table(const nvfp4_adamw_tensor* tensors, int64_t count, nvfp4_st
     e.m_scale_out = t.m_scale_out;
     e.v_scale_out = t.v_scale_out;
     e.weight_decay = t.weight_decay;
-    // whole-vector access: 8 elements of every array start on 16 bytes (8 for the codes)
-    const size_t sa = eight ? 8 : 16;
-    const bool vec = aligned(t.grad, 16) && aligned(t.p, 16) && aligned(t.p_out, 16) && aligned(t.w_out, 16) &&
-                     aligned(t.m, sa) && aligned(t.v, sa) && aligned(t.m_out, sa) && aligned(t.v_out, sa);
-    e.flags = (vec ? nvfp4::kAdamWAligned : 0) | (t.grad_dt == NVFP4_IN_BF16 ? nvfp4::kAdamWGradBf16 : 0);
+    e.flags = t.grad_dt == NVFP4_IN_BF16 ? nvfp4::kAdamWGradBf16 : 0;
     memcpy(entry + (size_t)i * sizeof(e), &e, sizeof(e));
     const int32_t id = (int32_t)i;
     for (int64_t k = 0; k < (t.n + nvfp4::kAdamWChunk - 1) / nvfp4::kAdamWChunk; ++k, ++c)

@@ -24,6 +24,12 @@ typedef uint32_t v2u32 __attribute__((ext_vector_type(2)));
 typedef float v4f32 __attribute__((ext_vector_type(4)));
 typedef float v2f32 __attribute__((ext_vector_type(2)));
 
+// The same from and to any element boundary (global memory takes unaligned vectors; a wave's 1 KB
+// then touches one line more).
+typedef uint32_t v4u32_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef float v4f32_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t v2u32_any __attribute__((ext_vector_type(2), aligned(1)));
+
 template <typename T>
 __device__ __forceinline__ v4u32 ld_u32x4(const T* p) { return *reinterpret_cast<const v4u32*>(p); }
 template <typename T>

@@ -651,11 +651,9 @@ __device__ __forceinline__ void gemm_tile_big(Operand A, Operand B, int64_t m0, 
       const int64_t col0 = n0 + wn * kWaveN;
       constexpr int kLanes = kWaveN / 8;                       // lanes along a row, 8 columns each
       const int cl = lane % kLanes * 8, rl = lane / kLanes;
-      // 8 columns at a time where every array allows it and the tile's last 8 are whole
-      const bool vec = ext.act.vec && (n1 - n0) % 8 == 0;
       float bias[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) bias[q] = vec && col0 + cl + q < n1 ? bias_at(ext.act, col0 + cl + q) : 0.0f;
+      for (int q = 0; q < 8; ++q) bias[q] = col0 + cl + q < n1 ? bias_at(ext.act, col0 + cl + q) : 0.0f;
 #pragma unroll
       for (int i = 0; i < kFragsM; ++i) {
 #pragma unroll
@@ -665,23 +663,23 @@ __device__ __forceinline__ void gemm_tile_big(Operand A, Operand B, int64_t m0, 
             own[(8 * (q >> 2) + 4 * h + (q & 3)) * kPitch + 32 * j + r] = acc[i][j][q] * alpha;
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the wave's LDS writes before its reads
         const int64_t row0 = m0 + wm * kWaveM + 32 * i;
-        if (vec) {
+        if (col0 + cl + 8 <= n1) {
 #pragma unroll 2
           for (int rr = rl; rr < 32; rr += 64 / kLanes) {
-            if (row0 + rr < m1 && col0 + cl < n1) {
+            if (row0 + rr < m1) {
               float v[8];
 #pragma unroll
               for (int q = 0; q < 8; ++q) v[q] = own[rr * kPitch + cl + q];
               mx = fmaxf(mx, put_act8<KIND - kOutAct>(ext.act, d, ext.ldd, row0 + rr, col0 + cl, v, bias));
             }
           }
-        } else {
+        } else {                                               // the last columns of an N that is not a multiple of 8
 #pragma unroll 1
-          for (int e = lane; e < 32 * kWaveN; e += 64) {
-            const int rr = e / kWaveN, cc = e % kWaveN;
-            if (row0 + rr < m1 && col0 + cc < n1)
-              mx = fmaxf(mx, put_act<KIND - kOutAct>(ext.act, d, ext.ldd, row0 + rr, col0 + cc, own[rr * kPitch + cc]));
-          }
+          for (int rr = rl; rr < 32; rr += 64 / kLanes)
+#pragma unroll 1
+            for (int q = 0; q < 8; ++q)
+              if (row0 + rr < m1 && col0 + cl + q < n1)
+                mx = fmaxf(mx, put_act<KIND - kOutAct>(ext.act, d, ext.ldd, row0 + rr, col0 + cl + q, own[rr * kPitch + cl + q]));
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       }
@@ -1701,7 +1699,7 @@ hipError_t launch_gemm_ex(GemmOperand a, GemmOperand b, int64_t M, int64_t N, in
   return hipGetLastError();
 }
 
-hipError_t launch_gemm_act(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int act_kind, ActOut act,
+hipError_t launch_gemm_act(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int act_kind, const ActOut& act,
                            uint16_t* D, int64_t ldd, float* amax, float* ws, hipStream_t stream) {
   hipError_t e = amax ? launch_fill(amax, 1, 0.0f, stream) : hipSuccess;
   if (e != hipSuccess) return e;
@@ -1709,8 +1707,6 @@ hipError_t launch_gemm_act(GemmOperand a, GemmOperand b, int64_t M, int64_t N, i
   if (M <= kSkinnyRows && K > 0) return launch_gemm_skinny(a, b, M, N, K, act_kind, act, D, ldd, amax, stream);
   if (use_big(K) && (e = enable_big_lds()) != hipSuccess) return e;
   const Operand A{a.codes, a.scales, M}, B{b.codes, b.scales, N};
-  auto ok = [](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; };
-  act.vec = ok(D, ldd) && ok(act.residual, act.residual ? act.ldr : 0) && ok(act.preact, act.preact ? act.ldp : 0);
 #define NVFP4_GA(KD) \
   launch_ext<kOutAct + KD>(A, a.global_scale, B, b.global_scale, K, D, ldd, amax, ws, act, stream)
   switch (act_kind) {

@@ -45,7 +45,7 @@ __global__ __launch_bounds__(kThreads) void k_gemm_skinny(GemmOperand A, GemmOpe
   for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[i][c] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-  Pipe<R, C, K32, TokensNvfp4<C, K32>> pipe;
+  Pipe<R, C, C == 1 ? 4 : C == 2 ? 3 : 2, K32, TokensNvfp4<C, K32>> pipe;
   pipe.start(weights, row, tok, wave, kWaves);
   pipe.run(weights, row, tok, wave, kWaves, (int)((K + kStep - 1) / kStep), acc);
   put<R, C>(red, wave, acc);

@@ -76,7 +76,7 @@ constexpr int kMaxAmaxPartials = 1024;
 // (the entry that the chunk belongs to); a chunk is kAdamWChunk consecutive elements of one tensor.
 constexpr int64_t kAdamWChunk = 8192;
 constexpr int kAdamWMaxParts = 1024;                     // partial sums of the gradient norm
-enum AdamWFlags : int32_t { kAdamWAligned = 1, kAdamWGradBf16 = 2 };
+enum AdamWFlags : int32_t { kAdamWGradBf16 = 1 };
 struct AdamWEntry {
   int64_t n, first_chunk;
   const void* grad;
@@ -123,15 +123,15 @@ hipError_t launch_gemm_ex(GemmOperand a, GemmOperand b, int64_t M, int64_t N, in
                           void* D, int64_t ldd, float* amax, float* ws, hipStream_t stream);
 
 // D = BF16(act(A B^T + bias) + residual), act_kind an ActKind; preact (optional) gets BF16(A B^T +
-// bias). ws as launch_gemm_ex. vec is set by the launcher.
+// bias). ws as launch_gemm_ex.
 struct ActOut {
   const void* bias;             // BF16 or FP32 [N], or null
   const uint16_t* residual;     // BF16 [M, N], row stride ldr, or null
   uint16_t* preact;             // BF16 [M, N], row stride ldp, or null
   int64_t ldr, ldp;
-  bool bias_f32, vec;
+  bool bias_f32;
 };
-hipError_t launch_gemm_act(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int act_kind, ActOut act,
+hipError_t launch_gemm_act(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int act_kind, const ActOut& act,
                            uint16_t* D, int64_t ldd, float* amax, float* ws, hipStream_t stream);
 
 // The same for M <= kSkinnyRows rows of A, any K % 16 == 0, without a workspace.
@@ -156,8 +156,8 @@ struct MoeArgs {
 struct MoeWork {
   int *counters, *used, *expert, *count, *order, *ids;
   float *weights, *logits, *x_inv, *h_top;
-  _Float16* x16;
-  float *h, *part;
+  _Float16 *x16, *h;
+  float* part;
 };
 size_t moe_layout(const MoeArgs& a, uint8_t* base, MoeWork* w);          // bytes; fills *w where given
 size_t moe_counter_bytes(int64_t hidden);                                // zero before the first call

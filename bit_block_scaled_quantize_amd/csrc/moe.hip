@@ -19,7 +19,8 @@
 // The matrix instruction takes FP16 columns: x and h are scaled by a power of two per token (per
 // pair) that brings their largest magnitude into [2^14, 2^15). A BF16 x is then exact down to
 // 2^-28 of that maximum, and what is lost below is under 2^-40 of it; an FP32 h keeps 11 bits,
-// three more than the BF16 result. Non-finite tokens take scale 1 and come out non-finite; other
+// three more than the BF16 result. A pair's maximum is known only when all of its h is, so h is
+// stored with a scale for each 16 rows (its maximum beside it) and brought to the pair's in k_expert<DOWN>. Non-finite tokens take scale 1 and come out non-finite; other
 // tokens' columns do not see them.
 #include "activation.h"
 #include "launch.h"
@@ -77,38 +78,52 @@ __device__ __forceinline__ bool last_to_finish(int* counter, int total) {
   return is_last;
 }
 
-// Eight elements of a BF16 or FP32 row from element i (0 past n).
-template <bool F32>
-__device__ __forceinline__ void load8(const void* row, int64_t i, int64_t n, bool vec, float (&v)[8]) {
-  if (vec && i + 8 <= n) {
-    if constexpr (F32) {
-      const v4f32 a = ld_f32x4(static_cast<const float*>(row) + i), b = ld_f32x4(static_cast<const float*>(row) + i + 4);
+// Eight elements of a BF16 or FP32 row from element i, 0 past n. VEC: as whole vectors through a buffer
+// resource (the row starts on 16 bytes, n is a multiple of 8), which needs no branch past n, so the
+// loads of several rows and places are in flight together.
+struct Row {
+  const void* p;
+  __amdgpu_buffer_rsrc_t b;
+};
+template <bool F32, bool VEC>
+__device__ __forceinline__ Row row_of(const void* p, int64_t n) {
+  Row r;
+  r.p = p;
+  if constexpr (VEC) r.b = buffer(p, n * (F32 ? 4 : 2));
+  return r;
+}
+template <bool F32, bool VEC>
+struct Eight {
+  v4u32 w[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const Row& row, int i, int n) {
+    if constexpr (VEC) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        v[q] = a[q];
-        v[q + 4] = b[q];
-      }
+      for (int q = 0; q < (F32 ? 2 : 1); ++q) w[q] = load16(row.b, (uint32_t)i * (F32 ? 4 : 2) + 16 * q);
     } else {
-      const v4u32 w = ld_u32x4(static_cast<const uint16_t*>(row) + i);
+      uint32_t v[8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        v[2 * q] = bf16_lo(w[q]);
-        v[2 * q + 1] = bf16_hi(w[q]);
+      for (int q = 0; q < 8; ++q) {
+        v[q] = 0u;
+        if (i + q < n) v[q] = F32 ? static_cast<const uint32_t*>(row.p)[i + q] : static_cast<const uint16_t*>(row.p)[i + q];
       }
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      if constexpr (F32) v[q] = i + q < n ? static_cast<const float*>(row)[i + q] : 0.0f;
-      else v[q] = i + q < n ? bf16_lo(static_cast<const uint16_t*>(row)[i + q]) : 0.0f;
+      if constexpr (F32) {
+        w[0] = v4u32{v[0], v[1], v[2], v[3]};
+        w[1] = v4u32{v[4], v[5], v[6], v[7]};
+      } else {
+        w[0] = v4u32{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
+      }
     }
   }
-}
+  __device__ __forceinline__ float operator[](int q) const {
+    if constexpr (F32) return __uint_as_float(w[q >> 2][q & 3]);
+    else return (q & 1) ? bf16_hi(w[0][q >> 1]) : bf16_lo(w[0][q >> 1]);
+  }
+};
 
 // The k largest logits of one token (one wave), ties to the lowest expert; its experts and weights.
 // At most kMoeMaxExperts experts: lane l holds experts l, l + 64, ... A NaN logit ranks last, and one
 // anywhere makes every weight of the token NaN.
-__device__ __forceinline__ void pick_experts(const MoeArgs& a, const MoeWork& w, int t, int* ids) {
+__device__ __forceinline__ void pick_experts(const MoeArgs& a, const MoeWork& w, int t, int* own_ids) {
   constexpr int kPer = (int)(kMoeMaxExperts / 64);
   const int lane = threadIdx.x & 63;
   const float* logits = w.logits + (int64_t)t * a.experts;
@@ -139,11 +154,13 @@ __device__ __forceinline__ void pick_experts(const MoeArgs& a, const MoeWork& w,
     float best = -INFINITY;
     int at = -1;
 #pragma unroll
-    for (int q = kPer - 1; q >= 0; --q)                       // the lowest of equals last
+    for (int q = kPer - 1; q >= 0; --q) {                     // the lowest of equals last
+      if (64 * q >= a.experts) continue;                      // uniform
       if (lane + 64 * q < a.experts && !((taken >> q) & 1u) && (at < 0 || key[q] >= best)) {
         best = key[q];
         at = q;
       }
+    }
     const float l = wave_fold_max(best);                      // the pick's logit
     // among the lanes that hold it the lowest expert; top_k <= experts: one is left
     const int e = (int)wave_fold_min(at >= 0 && best == l ? (uint32_t)(lane + 64 * at) : 0xFFFFFFFFu);
@@ -159,7 +176,8 @@ __device__ __forceinline__ void pick_experts(const MoeArgs& a, const MoeWork& w,
     float wt = (a.renormalize ? mine / (total + 1e-20f) : mine) * a.routed_scale;
     if (bad) wt = __uint_as_float(0x7FC00000u);
     const int64_t p = (int64_t)t * a.top_k + lane;
-    put_shared(&ids[p], id);
+    own_ids[lane] = id;
+    put_shared(&w.ids[p], id);
     w.weights[p] = wt;
     if (a.ids_out) a.ids_out[p] = id;
     if (a.weights_out) a.weights_out[p] = wt;
@@ -169,11 +187,12 @@ __device__ __forceinline__ void pick_experts(const MoeArgs& a, const MoeWork& w,
 // The pairs (token t, pick j), numbered t * top_k + j, by expert: those of the u-th used expert
 // w.expert[u] are w.order[u * 64 .. + w.count[u]) (a token has an expert at most once). Which slot a
 // pair gets decides the column it takes and nothing of its result.
-__device__ __forceinline__ void sort_pairs(const MoeArgs& a, const MoeWork& w) {
-  const int pairs = a.tokens * a.top_k;                       // a.experts or this many counts are read
+// own_ids: all the pairs' experts where one group has every token, else null (they are in w.ids).
+__device__ __forceinline__ void sort_pairs(const MoeArgs& a, const MoeWork& w, const int* own_ids) {
+  const int pairs = a.tokens * a.top_k;
   if (a.tokens == 1) {
     if ((int)threadIdx.x < pairs) {
-      w.expert[threadIdx.x] = get_shared(&w.ids[threadIdx.x]);
+      w.expert[threadIdx.x] = own_ids[threadIdx.x];
       w.count[threadIdx.x] = 1;
       w.order[threadIdx.x * kMoeMaxTokens] = threadIdx.x;
     }
@@ -187,7 +206,7 @@ __device__ __forceinline__ void sort_pairs(const MoeArgs& a, const MoeWork& w) {
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
     const int p = threadIdx.x + i * kRouteThreads;
-    id[i] = p < pairs ? get_shared(&w.ids[p]) : -1;
+    id[i] = p < pairs ? (own_ids ? own_ids[p] : get_shared(&w.ids[p])) : -1;
   }
   __syncthreads();
 #pragma unroll
@@ -218,38 +237,42 @@ __device__ __forceinline__ void sort_pairs(const MoeArgs& a, const MoeWork& w) {
 }
 
 // Grid: x = blocks of 4 experts, then 8 blocks that bring one token each to FP16; y = groups of 8
-// tokens. A logit block's waves split the hidden dimension, so that a row's loads are in flight
-// together. NT: tokens of a group computed (1, or 8 with the surplus repeating the first).
-template <bool F32, int NT>
-__global__ __launch_bounds__(kRouteThreads) void k_route(MoeArgs a, MoeWork w, bool vec_x, bool vec_r) {
+// tokens. A logit block's waves split the hidden dimension, two places a turn, so that a row's loads
+// are in flight together. NT: tokens of a group computed (1, or 8 with the surplus repeating the first).
+// VEC: x's rows and the router's start on 16 bytes.
+template <bool F32, int NT, bool VEC>
+__global__ __launch_bounds__(kRouteThreads) void k_route(MoeArgs a, MoeWork w) {
   __shared__ float red[kRouteWaves][kRouteExperts * NT];
+  __shared__ int own_ids[kGroupTokens * kMoeMaxTopK];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t0 = blockIdx.y * kGroupTokens;
   const int nt = a.tokens - t0 < kGroupTokens ? a.tokens - t0 : kGroupTokens;
   const int blocks = (int)gridDim.x - kGroupTokens;
-  const int64_t H = a.hidden;
+  const int H = (int)a.hidden;
+  constexpr int kTurn = kRouteThreads * 8;
   if ((int)blockIdx.x >= blocks) {
     const int q = (int)blockIdx.x - blocks;
     if (q >= nt) return;
     const int t = t0 + q;
-    const uint16_t* row = a.x + (int64_t)t * a.ldx;
+    const Row row = row_of<false, VEC>(a.x + (int64_t)t * a.ldx, H);
     float top = 0.0f;
-#pragma unroll 2
-    for (int64_t i = threadIdx.x * 8; i < H; i += kRouteThreads * 8) {
-      float v[8];
-      load8<false>(row, i, H, vec_x, v);
+    for (int i = threadIdx.x * 8; i < H; i += 2 * kTurn) {
+      Eight<false, VEC> v[2];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
+      for (int j = 0; j < 2; ++j) v[j].load(row, i + j * kTurn, H);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[j][k]));
     }
     top = wave_fold_max(top);
     if (lane == 0) red[wave][0] = top;
     __syncthreads();
     const float s = half_scale(fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0])));
-#pragma unroll 2
-    for (int64_t i = threadIdx.x * 8; i < H; i += kRouteThreads * 8) {       // H is a multiple of 16
-      float v[8];
-      load8<false>(row, i, H, vec_x, v);
+    for (int i = threadIdx.x * 8; i < H; i += kTurn) {         // H is a multiple of 16
+      Eight<false, VEC> v;
+      v.load(row, i, H);
       half8 o;
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = (_Float16)(v[j] * s);
@@ -259,24 +282,28 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(MoeArgs a, MoeWork w, b
     return;
   }
   const int e0 = blockIdx.x * kRouteExperts;
-  const void* row[kRouteExperts];
-#pragma unroll
-  for (int e = 0; e < kRouteExperts; ++e)
-    row[e] = static_cast<const uint8_t*>(a.router) + (int64_t)(e0 + e < a.experts ? e0 + e : e0) * H * (F32 ? 4 : 2);
   float acc[kRouteExperts][NT] = {};
-#pragma unroll 2
-  for (int64_t i = threadIdx.x * 8; i < H; i += kRouteThreads * 8) {
-    float r[kRouteExperts][8];
+  for (int i = threadIdx.x * 8; i < H; i += 2 * kTurn) {
+    Eight<F32, VEC> r[kRouteExperts][2];
 #pragma unroll
-    for (int e = 0; e < kRouteExperts; ++e) load8<F32>(row[e], i, H, vec_r, r[e]);
+    for (int e = 0; e < kRouteExperts; ++e) {
+      const Row row = row_of<F32, VEC>(static_cast<const uint8_t*>(a.router) +
+                                           (int64_t)(e0 + e < a.experts ? e0 + e : e0) * H * (F32 ? 4 : 2), H);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) r[e][j].load(row, i + j * kTurn, H);
+    }
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
-      float v[8];
-      load8<false>(a.x + (int64_t)(t0 + (q < nt ? q : 0)) * a.ldx, i, H, vec_x, v);
+      const Row row = row_of<false, VEC>(a.x + (int64_t)(t0 + (q < nt ? q : 0)) * a.ldx, H);
+      Eight<false, VEC> v[2];
 #pragma unroll
-      for (int e = 0; e < kRouteExperts; ++e)
+      for (int j = 0; j < 2; ++j) v[j].load(row, i + j * kTurn, H);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[e][q] = __builtin_fmaf(r[e][j], v[j], acc[e][q]);
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < kRouteExperts; ++e)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) acc[e][q] = __builtin_fmaf(r[e][j][k], v[j][k], acc[e][q]);
     }
   }
 #pragma unroll
@@ -294,9 +321,13 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(MoeArgs a, MoeWork w, b
                  (red[0][threadIdx.x] + red[1][threadIdx.x]) + (red[2][threadIdx.x] + red[3][threadIdx.x]));
   }
   if (!last_to_finish(&w.counters[1 + blockIdx.y], blocks)) return;
-  for (int q = wave; q < nt; q += kRouteWaves) pick_experts(a, w, t0 + q, w.ids);
-  if (!last_to_finish(&w.counters[0], (int)gridDim.y)) return;
-  sort_pairs(a, w);
+  for (int q = wave; q < nt; q += kRouteWaves) pick_experts(a, w, t0 + q, own_ids + q * a.top_k);
+  if (gridDim.y == 1) {
+    __syncthreads();
+    sort_pairs(a, w, own_ids);
+  } else if (last_to_finish(&w.counters[0], (int)gridDim.y)) {
+    sort_pairs(a, w, nullptr);
+  }
 }
 
 // Columns staged in LDS as FP16: kCols rows of `pitch` bytes and one run of zeros for the lanes
@@ -361,22 +392,26 @@ __global__ __launch_bounds__(64 * W) void k_expert(MoeArgs a, MoeWork w, int til
     if constexpr (UP) {
       inv = w.x_inv[pair / a.top_k];
     } else {
-      // the columns' maxima over the fragments of h, column c's in lane c
-      float top = 0.0f;
-      for (int c = 0; c < nc; ++c) {
-        const float* frag = w.h_top + (int64_t)__builtin_amdgcn_readlane(pair, c) * (K / 16);
-        float t = 0.0f;
-        for (int64_t i = lane; i < K / 16; i += 64) t = fmaxf(t, frag[i]);
-        t = wave_fold_max(t);
-        top = r == c ? t : top;
+      // the columns' maxima over the fragments of h, column c's in the lanes of row c
+      float top[kCols] = {};
+      for (int i = lane; i < (int)(K / 16); i += 64) {
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+          if (c < nc) top[c] = fmaxf(top[c], w.h_top[(int64_t)__builtin_amdgcn_readlane(pair, c) * (K / 16) + i]);
       }
-      scale = half_scale(top);
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        if (c < nc) {
+          const float s = half_scale(wave_fold_max(top[c]));
+          scale = r == c ? s : scale;
+        }
+      }
       inv = w.weights[pair] / scale;                          // a power of two: exact
     }
     float4v acc[R][1];
 #pragma unroll
     for (int i = 0; i < R; ++i) acc[i][0] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-    Pipe<R, 1, K32, TokensLds> pipe;
+    Pipe<R, 1, 4, K32, TokensLds> pipe;
     for (int64_t k0 = 0; k0 < K; k0 += kChunk) {
       const int64_t len = K - k0 < kChunk ? K - k0 : kChunk;
       const int first = (int)(k0 / kStep) + wave;
@@ -384,25 +419,36 @@ __global__ __launch_bounds__(64 * W) void k_expert(MoeArgs a, MoeWork w, int til
       pipe.start(weights, row, tok, first, kWaves);
       if (k0 > 0 || q0 > 0) __syncthreads();                  // the columns staged before have been read
       // the columns' elements, 8 at a time, zeros up to a whole step; column c's pair and scale
-      // are in lane c of every wave
+      // are in lane c of every wave, all columns' loads in flight together
       const int octets = (int)((len + kStep - 1) / kStep) * (kStep / 8);
-      for (int c = 0; c < nc; ++c) {
-        const int p = __builtin_amdgcn_readlane(pair, c);
-        const float s = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(scale), c));
-#pragma unroll 2
-        for (int o = threadIdx.x; o < octets; o += kThreads) {
-          half8 v{};
-          if (8 * o < len) {
+      for (int o = threadIdx.x; o < octets; o += kThreads) {
+        half8 v[kCols];
+        float s[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          v[c] = half8{};
+          s[c] = 1.0f;
+          if (c < nc && 8 * o < len) {
+            const int p = __builtin_amdgcn_readlane(pair, c);
             if constexpr (UP) {
-              v = *reinterpret_cast<const half8*>(w.x16 + (int64_t)(p / a.top_k) * K + k0 + 8 * o);
+              v[c] = *reinterpret_cast<const half8*>(w.x16 + (int64_t)(p / a.top_k) * K + k0 + 8 * o);
             } else {
-              const float* h = w.h + (int64_t)p * K + k0 + 8 * o;
-              const v4f32 x = ld_f32x4(h) * s, y = ld_f32x4(h + 4) * s;
-              v = half8{(_Float16)x[0], (_Float16)x[1], (_Float16)x[2], (_Float16)x[3],
-                        (_Float16)y[0], (_Float16)y[1], (_Float16)y[2], (_Float16)y[3]};
+              v[c] = *reinterpret_cast<const half8*>(w.h + (int64_t)p * K + k0 + 8 * o);
+              s[c] = w.h_top[(int64_t)p * (K / 16) + (k0 + 8 * o) / 16];
             }
           }
-          *reinterpret_cast<half8*>(tokens + c * pitch + 16 * o) = v;
+        }
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          if (c < nc) {
+            if constexpr (!UP) {                              // from the fragment's scale to the column's
+              const float f = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(scale), c)) /
+                              half_scale(s[c]);               // both powers of two: exact
+#pragma unroll
+              for (int q = 0; q < 8; ++q) v[c][q] = (_Float16)((float)v[c][q] * f);
+            }
+            *reinterpret_cast<half8*>(tokens + c * pitch + 16 * o) = v[c];
+          }
         }
       }
       __syncthreads();
@@ -430,8 +476,11 @@ __global__ __launch_bounds__(64 * W) void k_expert(MoeArgs a, MoeWork w, int til
         for (int q = 0; q < 4; ++q) top = fmaxf(top, fabsf(v[q]));
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const float s = half_scale(top);
         if (live && n < N) {
-          *reinterpret_cast<float4v*>(w.h + (int64_t)pair * N + n) = v;
+          typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+          *reinterpret_cast<half4*>(w.h + (int64_t)pair * N + n) =
+              half4{(_Float16)(v[0] * s), (_Float16)(v[1] * s), (_Float16)(v[2] * s), (_Float16)(v[3] * s)};
           if (g == 0) w.h_top[(int64_t)pair * (N / 16) + n / 16] = top;
         }
       } else if (live && n < N) {
@@ -444,20 +493,49 @@ __global__ __launch_bounds__(64 * W) void k_expert(MoeArgs a, MoeWork w, int til
   }
   if constexpr (!UP) {
     if (!last_to_finish(&w.counters[1 + kMoeMaxTokens / kGroupTokens + tile], *w.used)) return;
-    const int out_rows = (int)(N - n0 < 16 * R ? N - n0 : 16 * R);
-    for (int i = threadIdx.x; i < a.tokens * 16 * R; i += kThreads) {
-      const int t = i / (16 * R), n = i % (16 * R);
-      if (n >= out_rows) continue;
-      const float* part = w.part + (int64_t)t * a.top_k * N + n0 + n;
-      float s = 0.0f;
-#pragma unroll 4
-      for (int j = 0; j < a.top_k; ++j) s += get_shared(&part[(int64_t)j * N]);
-      a.y[(int64_t)t * a.ldy + n0 + n] = (uint16_t)bf16_rn_bits(s);
+    // y, two rows of a token a thread, the loads of two tokens' eight experts in flight together
+    constexpr int kPairs = 8 * R, kTokens = kThreads / kPairs;
+    const int n = threadIdx.x % kPairs * 2;
+    if (n0 + n >= N) return;
+    for (int t0 = threadIdx.x / kPairs; t0 < a.tokens; t0 += 2 * kTokens) {
+      const int t1 = t0 + kTokens < a.tokens ? t0 + kTokens : t0;
+      float lo[2] = {}, hi[2] = {};
+      for (int j0 = 0; j0 < a.top_k; j0 += 8) {
+        uint64_t v[2][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int jj = j0 + j < a.top_k ? j0 + j : j0;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            v[i][j] = get_shared(reinterpret_cast<const uint64_t*>(
+                w.part + ((int64_t)(i ? t1 : t0) * a.top_k + jj) * N + n0 + n));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j0 + j < a.top_k) {                             // uniform
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              lo[i] += __uint_as_float((uint32_t)v[i][j]);
+              hi[i] += __uint_as_float((uint32_t)(v[i][j] >> 32));
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = t0 + i * kTokens;
+        if (t < a.tokens) {
+          uint16_t* y = a.y + (int64_t)t * a.ldy + n0 + n;
+          const uint32_t b = bf16_rn_pair(lo[i], hi[i]);
+          y[0] = (uint16_t)b;
+          y[1] = (uint16_t)(b >> 16);
+        }
+      }
     }
   }
 }
 
-constexpr int kWideTokens = 4;
+constexpr int kWideTokens = 4;                                // up to here 8 waves split K, beyond 4
 constexpr int kRows = 2;                                      // fragments of 16 rows per workgroup
 constexpr int kMostLds = 8 * kRows * 64 * 16 + 64 + kCols * (2 * kChunk + 16);
 
@@ -514,7 +592,7 @@ size_t moe_layout(const MoeArgs& a, uint8_t* base, MoeWork* w) {
   x.x_inv = reinterpret_cast<float*>(part(4 * T));
   x.h_top = reinterpret_cast<float*>(part(4 * P * (size_t)a.ffn / 16));
   x.x16 = reinterpret_cast<_Float16*>(part(2 * T * (size_t)a.hidden));
-  x.h = reinterpret_cast<float*>(part(4 * P * (size_t)a.ffn));
+  x.h = reinterpret_cast<_Float16*>(part(2 * P * (size_t)a.ffn));
   x.part = reinterpret_cast<float*>(part(4 * P * (size_t)a.hidden));
   if (w) *w = x;
   return at;
@@ -529,17 +607,18 @@ hipError_t launch_moe(const MoeArgs& a, uint8_t* ws, hipStream_t stream) {
   if (a.tokens == 0) return hipSuccess;
   MoeWork w;
   moe_layout(a, ws, &w);
-  const bool vec_x = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx % 8 == 0;
-  const bool vec_r = reinterpret_cast<uintptr_t>(a.router) % 16 == 0;      // hidden % 16 == 0
+  const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx % 8 == 0 &&
+                   reinterpret_cast<uintptr_t>(a.router) % 16 == 0;        // hidden % 16 == 0
   const dim3 grid((unsigned)((a.experts + kRouteExperts - 1) / kRouteExperts + kGroupTokens),
                   (unsigned)((a.tokens + kGroupTokens - 1) / kGroupTokens));
-#define NVFP4_RT(F32, NT) \
-  hipLaunchKernelGGL((k_route<F32, NT>), grid, dim3(kRouteThreads), 0, stream, a, w, vec_x, vec_r)
-  if (a.tokens == 1) {
-    if (a.router_f32) NVFP4_RT(true, 1); else NVFP4_RT(false, 1);
-  } else {
-    if (a.router_f32) NVFP4_RT(true, 8); else NVFP4_RT(false, 8);
-  }
+#define NVFP4_RT(F32, NT, VEC) \
+  hipLaunchKernelGGL((k_route<F32, NT, VEC>), grid, dim3(kRouteThreads), 0, stream, a, w)
+#define NVFP4_RN(F32, VEC) do { if (a.tokens == 1) NVFP4_RT(F32, 1, VEC); else NVFP4_RT(F32, 8, VEC); } while (0)
+  if (vec && a.router_f32) NVFP4_RN(true, true);
+  else if (vec) NVFP4_RN(false, true);
+  else if (a.router_f32) NVFP4_RN(true, false);
+  else NVFP4_RN(false, false);
+#undef NVFP4_RN
 #undef NVFP4_RT
   hipError_t e = a.gated ? launch_expert<true, true>(a, w, stream) : launch_expert<true, false>(a, w, stream);
   if (e != hipSuccess || (e = launch_expert<false, false>(a, w, stream)) != hipSuccess) return e;

@@ -12,7 +12,7 @@
 //
 // A workgroup takes 16 R rows; its W waves share them and split K, every wave the next step in
 // turn (together they read whole runs of each row), and add up through LDS in a fixed order.
-// Everything goes straight from memory to registers, kAhead steps of the weights in flight per
+// Everything goes straight from memory to registers, a few steps of the weights in flight per
 // wave: no element is used twice in a workgroup, and what such a product waits for is HBM's
 // latency (about 2 us under load, so 5 TB/s want 40 KB in flight on every CU).
 #pragma once
@@ -27,7 +27,6 @@ typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float float4v __attribute__((ext_vector_type(4)));
 
 constexpr int kStep = 128;
-constexpr int kAhead = 4;
 
 // FP16 pair (S * 2^-8 twice) of an E4M3 scale code, and 8 codes as e2m1 * S (the conversion's own
 // scale operand returns the 2^8).
@@ -113,10 +112,11 @@ __device__ __forceinline__ half8 octet_of(const Run<false>& r, int t) {
 // elements at k; octet(raw, k, t) -> half8, zeros past K or without a token.
 // Loads return in the order of issue and the wait counts the younger ones, so a step's loads stay
 // together and in step order (the scheduling barriers), the tokens as far ahead as the weights.
-template <int R, int C, bool K32, class Tok>
+// A: steps in flight (they cost 5 (R + C) registers each).
+template <int R, int C, int A, bool K32, class Tok>
 struct Pipe {
-  Run<K32> w[kAhead][R];
-  typename Tok::Raw x[kAhead][C];
+  Run<K32> w[A][R];
+  typename Tok::Raw x[A][C];
 
   __device__ __forceinline__ void load(const Matrix& m, const uint32_t (&row)[R], const Tok& tok, int d, int s) {
     const uint32_t k = (uint32_t)s * kStep + ((threadIdx.x & 63) >> 4) * 32;
@@ -129,15 +129,15 @@ struct Pipe {
 
   __device__ __forceinline__ void start(const Matrix& m, const uint32_t (&row)[R], const Tok& tok, int first, int stride) {
 #pragma unroll
-    for (int d = 0; d < kAhead; ++d) load(m, row, tok, d, first + d * stride);
+    for (int d = 0; d < A; ++d) load(m, row, tok, d, first + d * stride);
   }
 
   __device__ __forceinline__ void run(const Matrix& m, const uint32_t (&row)[R], const Tok& tok, int first, int stride,
                                       int steps, float4v (&acc)[R][C]) {
 #pragma unroll 1
-    for (int s0 = first; s0 < steps; s0 += kAhead * stride) {
+    for (int s0 = first; s0 < steps; s0 += A * stride) {
 #pragma unroll
-      for (int d = 0; d < kAhead; ++d) {
+      for (int d = 0; d < A; ++d) {
         const int s = s0 + d * stride;
         if (s >= steps) return;                               // uniform (a break would look like another turn)
         const uint32_t k = (uint32_t)s * kStep + ((threadIdx.x & 63) >> 4) * 32;
@@ -154,7 +154,7 @@ struct Pipe {
               acc[i][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b[c], acc[i][c], 0, 0, 0);
           }
         }
-        load(m, row, tok, d, s + kAhead * stride);
+        load(m, row, tok, d, s + A * stride);
       }
     }
   }
