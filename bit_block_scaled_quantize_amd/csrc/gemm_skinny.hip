@@ -10,23 +10,23 @@ namespace {
 
 using namespace skinny;
 
-constexpr int kWaves = 8;
+constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 
 // Columns from NVFP4 rows: decoded like the weights.
-template <int C, bool K32>
+template <int C, bool K64>
 struct TokensNvfp4 {
-  typedef Run<K32> Raw;
+  typedef Run<K64> Raw;
   Matrix a;
   uint32_t rows, r;                                           // r: the lane's column of a fragment
   __device__ __forceinline__ Raw load(int c, uint32_t k) const {
     const uint32_t m = 16u * (uint32_t)c + r;
-    return load_run<K32>(a, m, m < rows, k);
+    return load_run<K64>(a, m, m < rows, k);
   }
   __device__ __forceinline__ half8 octet(const Raw& x, uint32_t, int t) const { return octet_of(x, t); }
 };
 
-template <int R, int C, bool K32>
+template <int R, int C, bool K64>
 __global__ __launch_bounds__(kThreads) void k_gemm_skinny(GemmOperand A, GemmOperand B, int64_t M, int64_t N,
                                                           int64_t K, int act, ActOut out, uint16_t* __restrict__ D,
                                                           int64_t ldd, float* __restrict__ amax) {
@@ -39,15 +39,15 @@ __global__ __launch_bounds__(kThreads) void k_gemm_skinny(GemmOperand A, GemmOpe
   uint32_t row[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) row[i] = (uint32_t)(n0 + 16 * i + r < N ? n0 + 16 * i + r : n0);   // rows past N: not stored
-  const TokensNvfp4<C, K32> tok{Matrix(A.codes, A.scales, M, K), (uint32_t)M, (uint32_t)r};
+  const TokensNvfp4<C, K64> tok{Matrix(A.codes, A.scales, M, K), (uint32_t)M, (uint32_t)r};
   float4v acc[R][C];
 #pragma unroll
   for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[i][c] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-  Pipe<R, C, C == 1 ? 4 : C == 2 ? 3 : 2, K32, TokensNvfp4<C, K32>> pipe;
+  Pipe<R, C, 2, K64, TokensNvfp4<C, K64>> pipe;
   pipe.start(weights, row, tok, wave, kWaves);
-  pipe.run(weights, row, tok, wave, kWaves, (int)((K + kStep - 1) / kStep), acc);
+  pipe.run(weights, row, tok, wave, kWaves, (int)((K + kStep<K64> - 1) / kStep<K64>), acc);
   put<R, C>(red, wave, acc);
   __syncthreads();
   const float alpha = A.global_scale[0] * B.global_scale[0];
@@ -73,7 +73,7 @@ template <int R, int C>
 void launch_rc(const GemmOperand& a, const GemmOperand& b, int64_t M, int64_t N, int64_t K, int act, const ActOut& out,
                uint16_t* D, int64_t ldd, float* amax, hipStream_t stream) {
   const dim3 grid((unsigned)((N + 16 * R - 1) / (16 * R)));
-  if (K % 32 == 0)
+  if (K % 64 == 0)
     hipLaunchKernelGGL((k_gemm_skinny<R, C, true>), grid, dim3(kThreads), 0, stream, a, b, M, N, K, act, out, D, ldd, amax);
   else
     hipLaunchKernelGGL((k_gemm_skinny<R, C, false>), grid, dim3(kThreads), 0, stream, a, b, M, N, K, act, out, D, ldd, amax);

@@ -128,14 +128,19 @@ __device__ __forceinline__ void pick_experts(const MoeArgs& a, const MoeWork& w,
   const int lane = threadIdx.x & 63;
   const float* logits = w.logits + (int64_t)t * a.experts;
   float key[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {                            // all in flight together
+    if (64 * j >= a.experts) break;                           // uniform
+    const int e = lane + 64 * j;
+    key[j] = get_shared(&logits[e < a.experts ? e : a.experts - 1]);
+  }
   float top = -INFINITY;
   bool bad = false;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    const int e = lane + 64 * j;
-    const float l = e < a.experts ? get_shared(&logits[e]) : -INFINITY;
-    bad |= l != l;
-    key[j] = l == l ? l : -INFINITY;
+    if (64 * j >= a.experts) break;
+    bad |= key[j] != key[j];
+    key[j] = lane + 64 * j < a.experts && key[j] == key[j] ? key[j] : -INFINITY;
     top = fmaxf(top, key[j]);
   }
   bad = __any(bad);
@@ -330,9 +335,9 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(MoeArgs a, MoeWork w) {
   }
 }
 
-// Columns staged in LDS as FP16: kCols rows of `pitch` bytes and one run of zeros for the lanes
+// Columns staged in LDS as FP16: rows of `pitch` bytes and one run of zeros for the lanes
 // without a token. Nothing of them is loaded in the loop over K, whose only loads are the weights'.
-constexpr int kCols = 8;                                      // tokens of an expert at a time
+constexpr int kZeroBytes = 2 * kRun<true>;
 constexpr int kChunk = 4096;                                  // elements of K staged at a time
 struct TokensLds {
   struct Raw {};
@@ -350,16 +355,17 @@ struct TokensLds {
 // leaves at once) x row tiles, tiles of one expert next to each other.
 // UP: rows of W1, K = hidden -> h[pair][f]. GATED: fragments 0 .. R/2 - 1 hold the gate's rows, the
 // others the same rows of U. DOWN: rows of W2, K = ffn -> part[pair][n], then y.
-template <bool UP, bool GATED, int R, int W, bool K32>
-__global__ __launch_bounds__(64 * W) void k_expert(MoeArgs a, MoeWork w, int tiles, int cols, uint32_t pitch) {
+// kCols: columns staged at a time (8, or 1 for one token). W: waves, which split K.
+template <bool UP, bool GATED, int R, int W, int kCols, bool K64>
+__global__ __launch_bounds__(64 * W) void k_expert(MoeArgs a, MoeWork w, int tiles, uint32_t pitch) {
   constexpr int kWaves = W, kThreads = 64 * W;
   static_assert(!GATED || R % 2 == 0, "a gated tile holds as many gate as up fragments");
   static_assert(R <= W, "a wave per fragment of output rows");
   constexpr int RO = GATED ? R / 2 : R;                       // fragments of output rows
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   float* red = reinterpret_cast<float*>(lds);                 // kWaves R fragments
-  uint8_t* const zeros = lds + kWaves * R * 64 * 16;          // 64 bytes
-  uint8_t* const tokens = zeros + 64;                         // cols rows of pitch bytes
+  uint8_t* const zeros = lds + kWaves * R * 64 * 16;          // a run's worth
+  uint8_t* const tokens = zeros + kZeroBytes;                 // kCols rows of pitch bytes
   const int u = blockIdx.x / tiles, tile = blockIdx.x % tiles;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -380,70 +386,87 @@ __global__ __launch_bounds__(64 * W) void k_expert(MoeArgs a, MoeWork w, int til
     const int64_t n = n0 + 16 * (i % RO) + r;
     row[i] = (uint32_t)((i >= RO ? N : 0) + (n < N ? n : n0));      // rows past N: not stored
   }
-  if (threadIdx.x < 16) reinterpret_cast<uint32_t*>(zeros)[threadIdx.x] = 0u;
+  if (threadIdx.x < kZeroBytes / 4) reinterpret_cast<uint32_t*>(zeros)[threadIdx.x] = 0u;
   const float gs = m.global_scale[e];
-  for (int q0 = 0; q0 < count; q0 += cols) {
-    const int nc = count - q0 < cols ? count - q0 : cols;     // columns of this round
+  for (int q0 = 0; q0 < count; q0 += kCols) {
+    const int nc = count - q0 < kCols ? count - q0 : kCols;   // columns of this round
     if (q0 > 0) mine = w.order[u * (int)kMoeMaxTokens + q0 + (r < nc ? r : 0)];
     const bool live = r < nc;
     const int pair = __shfl(mine, live ? r : 0);              // dead lanes: column 0's
-    float inv;                                                // undoes the column's power of two
-    float scale = 1.0f;
-    if constexpr (UP) {
-      inv = w.x_inv[pair / a.top_k];
-    } else {
-      // the columns' maxima over the fragments of h, column c's in the lanes of row c
-      float top[kCols] = {};
-      for (int i = lane; i < (int)(K / 16); i += 64) {
-#pragma unroll
-        for (int c = 0; c < kCols; ++c)
-          if (c < nc) top[c] = fmaxf(top[c], w.h_top[(int64_t)__builtin_amdgcn_readlane(pair, c) * (K / 16) + i]);
-      }
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        if (c < nc) {
-          const float s = half_scale(wave_fold_max(top[c]));
-          scale = r == c ? s : scale;
-        }
-      }
-      inv = w.weights[pair] / scale;                          // a power of two: exact
-    }
     float4v acc[R][1];
 #pragma unroll
     for (int i = 0; i < R; ++i) acc[i][0] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-    Pipe<R, 1, 4, K32, TokensLds> pipe;
+    float inv = 1.0f;                                         // undoes the column's power of two
+    float scale = 1.0f;                                       // DOWN: the column's, in the lanes of row c
+    Pipe<R, 1, 2, K64, TokensLds> pipe;
     for (int64_t k0 = 0; k0 < K; k0 += kChunk) {
       const int64_t len = K - k0 < kChunk ? K - k0 : kChunk;
-      const int first = (int)(k0 / kStep) + wave;
+      const int first = (int)(k0 / kStep<K64>) + wave;
       TokensLds tok{live ? tokens + r * pitch : zeros, (uint32_t)k0, (uint32_t)K, live ? 0xFFFFFFFFu : 0u};
-      pipe.start(weights, row, tok, first, kWaves);
-      if (k0 > 0 || q0 > 0) __syncthreads();                  // the columns staged before have been read
-      // the columns' elements, 8 at a time, zeros up to a whole step; column c's pair and scale
-      // are in lane c of every wave, all columns' loads in flight together
-      const int octets = (int)((len + kStep - 1) / kStep) * (kStep / 8);
-      for (int o = threadIdx.x; o < octets; o += kThreads) {
-        half8 v[kCols];
-        float s[kCols];
+      // The columns' elements, 8 at a time, zeros up to a whole step; column c's pair is in lane c of
+      // every wave. The first turn's loads (all of them, as a rule) are issued ahead of the weights', so
+      // that waiting for them does not wait for those.
+      const int octets = (int)((len + kStep<K64> - 1) / kStep<K64>) * (kStep<K64> / 8);
+      half8 v[kCols];
+      float vs[kCols];                                        // DOWN: maxima of the elements' fragments
+      auto fetch = [&](int o) {
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
           v[c] = half8{};
-          s[c] = 1.0f;
+          vs[c] = 0.0f;
           if (c < nc && 8 * o < len) {
             const int p = __builtin_amdgcn_readlane(pair, c);
             if constexpr (UP) {
               v[c] = *reinterpret_cast<const half8*>(w.x16 + (int64_t)(p / a.top_k) * K + k0 + 8 * o);
             } else {
               v[c] = *reinterpret_cast<const half8*>(w.h + (int64_t)p * K + k0 + 8 * o);
-              s[c] = w.h_top[(int64_t)p * (K / 16) + (k0 + 8 * o) / 16];
+              vs[c] = w.h_top[(int64_t)p * (K / 16) + (k0 + 8 * o) / 16];
             }
           }
         }
+      };
+      float top[kCols];
+      if (k0 == 0) {
+        if constexpr (UP) {
+          inv = w.x_inv[pair / a.top_k];
+        } else {
+          inv = w.weights[pair];
+          const int frags = (int)(K / 16);
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) {
+            top[c] = 0.0f;
+            if (c < nc) {
+              const float* t = w.h_top + (int64_t)__builtin_amdgcn_readlane(pair, c) * frags;
+              const float t0 = t[lane < frags ? lane : 0], t1 = t[lane + 64 < frags ? lane + 64 : 0];
+              top[c] = fmaxf(t0, t1);
+              for (int i = lane + 128; i < frags; i += 64) top[c] = fmaxf(top[c], t[i]);
+            }
+          }
+        }
+      }
+      fetch(threadIdx.x);
+      pipe.start(weights, row, tok, first, kWaves);
+      if constexpr (!UP) {
+        if (k0 == 0) {
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) {
+            if (c < nc) {
+              const float s = half_scale(wave_fold_max(top[c]));
+              scale = r == c ? s : scale;
+            }
+          }
+          inv /= scale;                                       // a power of two: exact
+        }
+      }
+      if (k0 > 0 || q0 > 0) __syncthreads();                  // the columns staged before have been read
+      for (int o = threadIdx.x; o < octets; o += kThreads) {
+        if (o >= kThreads) fetch(o);
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
           if (c < nc) {
             if constexpr (!UP) {                              // from the fragment's scale to the column's
               const float f = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(scale), c)) /
-                              half_scale(s[c]);               // both powers of two: exact
+                              half_scale(vs[c]);              // both powers of two: exact
 #pragma unroll
               for (int q = 0; q < 8; ++q) v[c][q] = (_Float16)((float)v[c][q] * f);
             }
@@ -452,7 +475,7 @@ __global__ __launch_bounds__(64 * W) void k_expert(MoeArgs a, MoeWork w, int til
         }
       }
       __syncthreads();
-      pipe.run(weights, row, tok, first, kWaves, (int)((k0 + len + kStep - 1) / kStep), acc);
+      pipe.run(weights, row, tok, first, kWaves, (int)((k0 + len + kStep<K64> - 1) / kStep<K64>), acc);
     }
     put<R, 1>(red, wave, acc);
     __syncthreads();
@@ -537,35 +560,40 @@ __global__ __launch_bounds__(64 * W) void k_expert(MoeArgs a, MoeWork w, int til
 
 constexpr int kWideTokens = 4;                                // up to here 8 waves split K, beyond 4
 constexpr int kRows = 2;                                      // fragments of 16 rows per workgroup
-constexpr int kMostLds = 8 * kRows * 64 * 16 + 64 + kCols * (2 * kChunk + 16);
+constexpr int kMostCols = 8;                                  // tokens of an expert at a time
+constexpr int kMostLds = 8 * kRows * 64 * 16 + kZeroBytes + kMostCols * (2 * kChunk + 16);
 
 int64_t tiles_of(int64_t rows, int frags) { return (rows + 16 * frags - 1) / (16 * frags); }
 
-template <bool UP, bool GATED, int W, bool K32>
+template <bool UP, bool GATED, int W, int COLS, bool K64>
 hipError_t launch_expert_as(const MoeArgs& a, const MoeWork& w, hipStream_t stream) {
   // the staged columns can take more LDS than a launch may by default
-  static const hipError_t ready = hipFuncSetAttribute((const void*)k_expert<UP, GATED, kRows, W, K32>,
+  static const hipError_t ready = hipFuncSetAttribute((const void*)k_expert<UP, GATED, kRows, W, COLS, K64>,
                                                       hipFuncAttributeMaxDynamicSharedMemorySize, kMostLds);
   if (ready != hipSuccess) return ready;
   const int64_t K = UP ? a.hidden : a.ffn, N = UP ? a.ffn : a.hidden;
   const int64_t pairs = (int64_t)a.tokens * a.top_k;
   const int64_t most = pairs < a.experts ? pairs : a.experts;
   const int tiles = (int)tiles_of(N, GATED ? kRows / 2 : kRows);
-  const int cols = a.tokens < kCols ? a.tokens : kCols;
-  const int64_t staged = K < kChunk ? (K + kStep - 1) / kStep * kStep : kChunk;
+  const int64_t staged = K < kChunk ? (K + kStep<K64> - 1) / kStep<K64> * kStep<K64> : kChunk;
   const uint32_t pitch = (uint32_t)(2 * staged + 16);         // rows start 4 banks apart
-  const size_t bytes = (size_t)W * kRows * 64 * 16 + 64 + (size_t)cols * pitch;
-  hipLaunchKernelGGL((k_expert<UP, GATED, kRows, W, K32>), dim3((unsigned)(most * tiles)), dim3(64 * W), bytes, stream,
-                     a, w, tiles, cols, pitch);
+  const size_t bytes = (size_t)W * kRows * 64 * 16 + kZeroBytes + (size_t)COLS * pitch;
+  hipLaunchKernelGGL((k_expert<UP, GATED, kRows, W, COLS, K64>), dim3((unsigned)(most * tiles)), dim3(64 * W), bytes,
+                     stream, a, w, tiles, pitch);
   return hipSuccess;
+}
+
+template <bool UP, bool GATED, bool K64>
+hipError_t launch_expert_k(const MoeArgs& a, const MoeWork& w, hipStream_t stream) {
+  if (a.tokens == 1) return launch_expert_as<UP, GATED, 8, 1, K64>(a, w, stream);
+  if (a.tokens <= kWideTokens) return launch_expert_as<UP, GATED, 8, kMostCols, K64>(a, w, stream);
+  return launch_expert_as<UP, GATED, 4, kMostCols, K64>(a, w, stream);
 }
 
 template <bool UP, bool GATED>
 hipError_t launch_expert(const MoeArgs& a, const MoeWork& w, hipStream_t stream) {
-  const bool k32 = (UP ? a.hidden : a.ffn) % 32 == 0;
-  const bool wide = a.tokens <= kWideTokens;
-  if (wide) return k32 ? launch_expert_as<UP, GATED, 8, true>(a, w, stream) : launch_expert_as<UP, GATED, 8, false>(a, w, stream);
-  return k32 ? launch_expert_as<UP, GATED, 4, true>(a, w, stream) : launch_expert_as<UP, GATED, 4, false>(a, w, stream);
+  return (UP ? a.hidden : a.ffn) % 64 == 0 ? launch_expert_k<UP, GATED, true>(a, w, stream)
+                                           : launch_expert_k<UP, GATED, false>(a, w, stream);
 }
 
 }  // namespace

@@ -4,9 +4,11 @@
 // with however few tokens there are, and decoding is shared by nothing but the lanes.
 //
 // v_mfma_f32_16x16x32_f16 with the weights as A (rows) and the tokens as B (columns): lane l holds
-// row / column l % 16 and 8 K-values picked by g = l / 16. Over a K step of 128 a lane owns the 32
-// consecutive elements [128 s + 32 g, + 32) of its row (16 bytes of codes, two scale bytes) and feeds
-// their four octets to four instructions; K order is free as long as rows and columns agree. The
+// row / column l % 16 and 8 K-values picked by g = l / 16. Over a K step a lane owns one run of
+// consecutive elements of its row and feeds their octets to consecutive instructions; K order is
+// free as long as rows and columns agree. With K a multiple of 64 a run is 64 elements, the step
+// 256: the four lanes of a row read a whole 128-byte line between them (two loads apart) and its 16
+// scale bytes as four words; otherwise 32 elements, step 128, the scales byte by byte. The
 // result holds column l % 16, rows 4 g .. 4 g + 3. Codes decode to FP16 exactly (e2m1 * e4m3 has at
 // most 6 significant bits in [2^-10, 2688]), products are exact, sums FP32.
 //
@@ -26,7 +28,10 @@ typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float float4v __attribute__((ext_vector_type(4)));
 
-constexpr int kStep = 128;
+// Elements of a lane's run, octets of it, elements of a step. K64: K is a multiple of 64.
+template <bool K64> constexpr int kRun = K64 ? 64 : 32;
+template <bool K64> constexpr int kOctets = kRun<K64> / 8;
+template <bool K64> constexpr int kStep = 4 * kRun<K64>;
 
 // FP16 pair (S * 2^-8 twice) of an E4M3 scale code, and 8 codes as e2m1 * S (the conversion's own
 // scale operand returns the 2^8).
@@ -66,14 +71,13 @@ struct Matrix {
       : codes(buffer(c, rows * (k >> 1))), scales(buffer(s, rows * (k >> 4))), K((uint32_t)k) {}
 };
 
-// The 32 codes of one row at element k (a multiple of 32) and their two scale bytes: zeros at and
-// past K and without a row.
-// K32: K is a multiple of 32 (rows of codes start on 16 bytes, of scales on 2). Values are kept as
-// they are loaded: arithmetic on one, even a widening, would wait for it where it is loaded.
-template <bool K32>
+// The codes of one row's run at element k (a multiple of the run) and their scale bytes: zeros at and
+// past K and without a row. Values are kept as they are loaded: arithmetic on one, even a widening,
+// would wait for it where it is loaded.
+template <bool K64>
 struct Run {
-  v4u32 codes;
-  uint16_t scales;                                            // both
+  v4u32 lo, hi;
+  uint32_t scales;
 };
 template <>
 struct Run<false> {
@@ -81,14 +85,16 @@ struct Run<false> {
   uint8_t s0, s1;
 };
 
-template <bool K32>
-__device__ __forceinline__ Run<K32> load_run(const Matrix& m, uint32_t row, bool live, uint32_t k) {
-  Run<K32> r;
+template <bool K64>
+__device__ __forceinline__ Run<K64> load_run(const Matrix& m, uint32_t row, bool live, uint32_t k) {
+  Run<K64> r;
   const uint32_t c = row * (m.K >> 1) + (k >> 1), s = row * (m.K >> 4) + (k >> 4);
   const bool a = live && k < m.K;
-  if constexpr (K32) {
-    r.codes = load16(m.codes, a ? c : kBeyond);
-    r.scales = __builtin_amdgcn_raw_buffer_load_b16(m.scales, a ? s : kBeyond, 0, 0);
+  if constexpr (K64) {
+    const uint32_t at = a ? c : kBeyond;
+    r.lo = load16(m.codes, at);
+    r.hi = load16(m.codes, at + 16);
+    r.scales = __builtin_amdgcn_raw_buffer_load_b32(m.scales, a ? s : kBeyond, 0, 0);
   } else {
     const bool b = live && k + 16 < m.K;
     r.lo = __builtin_bit_cast(v2u32, __builtin_amdgcn_raw_buffer_load_b64(m.codes, a ? c : kBeyond, 0, 0));
@@ -100,30 +106,30 @@ __device__ __forceinline__ Run<K32> load_run(const Matrix& m, uint32_t row, bool
 }
 
 __device__ __forceinline__ half8 octet_of(const Run<true>& r, int t) {
-  return decode8(r.codes[t], scale_pair((uint32_t)(r.scales >> (8 * (t >> 1))) & 0xFFu));
+  return decode8(t < 4 ? r.lo[t & 3] : r.hi[t & 3], scale_pair((r.scales >> (8 * (t >> 1))) & 0xFFu));
 }
 __device__ __forceinline__ half8 octet_of(const Run<false>& r, int t) {
   return decode8(t < 2 ? r.lo[t & 1] : r.hi[t & 1], scale_pair(t < 2 ? r.s0 : r.s1));
 }
 
 // acc[i][c] += rows 16 i .. + 15 of the tile times token columns 16 c .. + 15, over the steps
-// first, first + stride, ... below `steps` (of kStep elements from element 0). row: this lane's row
-// of each fragment. Tok: load(c, k) -> Raw, what the lane needs of column 16 c + l % 16 for its 32
-// elements at k; octet(raw, k, t) -> half8, zeros past K or without a token.
+// first, first + stride, ... below `steps` (from element 0 on). row: this lane's row
+// of each fragment. Tok: load(c, k) -> Raw, what the lane needs of column 16 c + l % 16 for its run
+// at k; octet(raw, k, t) -> half8, zeros past K or without a token.
 // Loads return in the order of issue and the wait counts the younger ones, so a step's loads stay
 // together and in step order (the scheduling barriers), the tokens as far ahead as the weights.
-// A: steps in flight (they cost 5 (R + C) registers each).
-template <int R, int C, int A, bool K32, class Tok>
+// A: steps in flight (they cost 9, or 5, registers for each fragment of rows or columns).
+template <int R, int C, int A, bool K64, class Tok>
 struct Pipe {
-  Run<K32> w[A][R];
+  Run<K64> w[A][R];
   typename Tok::Raw x[A][C];
 
   __device__ __forceinline__ void load(const Matrix& m, const uint32_t (&row)[R], const Tok& tok, int d, int s) {
-    const uint32_t k = (uint32_t)s * kStep + ((threadIdx.x & 63) >> 4) * 32;
+    const uint32_t k = (uint32_t)s * kStep<K64> + ((threadIdx.x & 63) >> 4) * kRun<K64>;
 #pragma unroll
     for (int c = 0; c < C; ++c) x[d][c] = tok.load(c, k);
 #pragma unroll
-    for (int i = 0; i < R; ++i) w[d][i] = load_run<K32>(m, row[i], true, k);
+    for (int i = 0; i < R; ++i) w[d][i] = load_run<K64>(m, row[i], true, k);
     __builtin_amdgcn_sched_barrier(0);
   }
 
@@ -140,9 +146,9 @@ struct Pipe {
       for (int d = 0; d < A; ++d) {
         const int s = s0 + d * stride;
         if (s >= steps) return;                               // uniform (a break would look like another turn)
-        const uint32_t k = (uint32_t)s * kStep + ((threadIdx.x & 63) >> 4) * 32;
+        const uint32_t k = (uint32_t)s * kStep<K64> + ((threadIdx.x & 63) >> 4) * kRun<K64>;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < kOctets<K64>; ++t) {
           half8 b[C];
 #pragma unroll
           for (int c = 0; c < C; ++c) b[c] = tok.octet(x[d][c], k, t);
