@@ -517,7 +517,7 @@ def gemm_act(a: NVFP4Tensor, b: NVFP4Tensor, bias: torch.Tensor | None = None, a
         _check_out(preact, m, n, torch.bfloat16, "preact")
     _check_vec(amax_out, 1, "amax_out")
     if workspace is None:
-        ws_n = workspace_size(OP_GEMM_ACT, m, n)
+        ws_n = workspace_size(OP_GEMM_ACT, m, n, a.cols)
         workspace = torch.empty((ws_n,), dtype=torch.uint8, device=a.codes.device) if ws_n else None
     else:
         ws_n = workspace.numel()

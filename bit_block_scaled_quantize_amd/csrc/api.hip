@@ -164,7 +164,7 @@ size_t nvfp4_workspace_size(int op, int64_t rows, int64_t cols, int64_t nseg) {
       return round_up(segs > partials ? segs : partials, kWsAlign);
     }
     case NVFP4_OP_AMAX_PAIR: return round_up(2 * partials, kWsAlign);
-    case NVFP4_OP_GEMM_ACT: return round_up(nvfp4::gemm_ex_workspace_bytes(rows, cols), kWsAlign);
+    case NVFP4_OP_GEMM_ACT: return round_up(nvfp4::gemm_act_workspace_bytes(rows, cols, nseg), kWsAlign);
     case NVFP4_OP_ACT_GRAD: return round_up(nvfp4::act_grad_workspace_bytes(rows, cols), kWsAlign);
     case NVFP4_OP_ADAMW: return round_up((size_t)nvfp4::kAdamWMaxParts * sizeof(double), kWsAlign);
     case NVFP4_OP_GEMM_EX: return round_up(nvfp4::gemm_ex_workspace_bytes(rows, cols), kWsAlign);
@@ -510,14 +510,17 @@ int nvfp4_gemm_act(const nvfp4_tensor* A, const nvfp4_tensor* B, uint16_t* D, in
       !aligned(bias, bias_dt == NVFP4_IN_FP32 ? 4 : 2) || !aligned(amax_out, 4))
     return fail(NVFP4_ERR_INVALID, "a buffer is not aligned to its element size");
   if (!aligned(A->scales, 4) || !aligned(B->scales, 4)) return fail(NVFP4_ERR_INVALID, "scales must be 4-byte aligned");
-  const size_t need = nvfp4_workspace_size(NVFP4_OP_GEMM_ACT, A->rows, N, 1);
+  const int64_t padded = nvfp4::gemm_act_padded_k(A->cols) / 2;
+  if (A->rows * padded > (int64_t)0x7FFFFFFF || N * padded > (int64_t)0x7FFFFFFF)
+    return fail(NVFP4_ERR_UNSUPPORTED, "codes exceed 2 GiB with K brought to a multiple of 64");
+  const size_t need = nvfp4_workspace_size(NVFP4_OP_GEMM_ACT, A->rows, N, A->cols);
   if (need && (!workspace || ws_bytes < need || !aligned(workspace, kWsAlign)))
     return fail(NVFP4_ERR_WORKSPACE, "workspace of %zu bytes (256-byte aligned) required, got %zu", need, workspace ? ws_bytes : (size_t)0);
   const nvfp4::GemmOperand a{A->codes, A->scales, A->global_scale};
   const nvfp4::GemmOperand b{B->codes, B->scales, B->global_scale};
   const nvfp4::ActOut out{bias, residual, preact, ldr, ldp, bias_dt == NVFP4_IN_FP32};
   return hip_status(nvfp4::launch_gemm_act(a, b, A->rows, N, A->cols, (int)act, out, D, ldd, amax_out,
-                                           static_cast<float*>(workspace), (hipStream_t)hip_stream), "gemm_act");
+                                           workspace, (hipStream_t)hip_stream), "gemm_act");
 }
 
 int nvfp4_act_grad(const void* dy, nvfp4_dtype dt, int64_t M, int64_t N, int64_t ldy, const uint16_t* z,

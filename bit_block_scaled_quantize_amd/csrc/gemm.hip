@@ -1267,9 +1267,7 @@ __device__ __forceinline__ void gemm_tile_small(Operand A, Operand B, int64_t m0
       for (int q = 0; q < 4; ++q) {
         const int64_t row = wm0 + 16 * i + 4 * g + q;
         if (row < m1) {
-          if constexpr (EXT && is_act(KIND))
-            mx = fmaxf(mx, put_act<KIND - kOutAct>(ext.act, static_cast<uint16_t*>(ext.d), ext.ldd, row, col, acc[i][j][q] * alpha));
-          else if constexpr (EXT) mx = fmaxf(mx, put_out<KIND>(ext.d, ext.ldd, row, col, acc[i][j][q] * alpha));
+          if constexpr (EXT) mx = fmaxf(mx, put_out<KIND>(ext.d, ext.ldd, row, col, acc[i][j][q] * alpha));
           else D[row * ldd + col] = acc[i][j][q] * alpha;
         }
       }
@@ -1297,7 +1295,7 @@ void k_gemm_small(Operand A, const float* __restrict__ ag, Operand B, const floa
 template <int KIND>
 __global__ __launch_bounds__(kThreads)
 void k_gemm_small_ext(Operand A, const float* __restrict__ ag, Operand B, const float* __restrict__ bg,
-                      int64_t K, void* D, int64_t ldd, float* amax, ActOut act) {
+                      int64_t K, void* D, int64_t ldd, float* amax) {
   using namespace small;
   const int64_t tiles_m = (A.rows + kBlockM - 1) / kBlockM;
   const int64_t tiles_n = (B.rows + kBlockN - 1) / kBlockN;
@@ -1307,7 +1305,7 @@ void k_gemm_small_ext(Operand A, const float* __restrict__ ag, Operand B, const 
   const int64_t m1 = m0 + kBlockM < A.rows ? m0 + kBlockM : A.rows;
   const int64_t n1 = n0 + kBlockN < B.rows ? n0 + kBlockN : B.rows;
   gemm_tile_small<KIND, true>(A, B, m0, m1, n0, n1, K, ag[0] * bg[0], nullptr, ldd,
-                              ExtOut{D, ldd, nullptr, amax, act});
+                              ExtOut{D, ldd, nullptr, amax, {}});
 }
 
 __global__ __launch_bounds__(kThreads)
@@ -1664,26 +1662,55 @@ size_t gemm_ex_workspace_bytes(int64_t M, int64_t N) {
   return (size_t)(tiles - tail_first) * (size_t)splits * big::kBlockM * big::kBlockN * sizeof(float);
 }
 
+namespace {
+
+template <int KIND>
+void launch_big_ext(const Operand& A, const float* ag, const Operand& B, const float* bg, int64_t K, void* D,
+                    int64_t ldd, float* amax, float* ws, const ActOut& act, hipStream_t stream) {
+  const int64_t M = A.rows, N = B.rows, tiles = big_tiles(M, N);
+  int64_t tail_first, splits;
+  split_plan(tiles, K, tail_first, splits);
+  const int64_t grid = tail_first + (tiles - tail_first) * (splits < 0 ? 4 : splits);
+  hipLaunchKernelGGL(k_gemm_big_ext<KIND>, dim3((unsigned)grid), dim3(kThreads), big::kLdsBytes, stream, A, ag, B, bg,
+                     K, D, ldd, amax, ws, tail_first, (int)splits, act);
+  if (tail_first < tiles && splits > 0)
+    hipLaunchKernelGGL(k_split_fixup<KIND>, dim3((unsigned)((tiles - tail_first) * kZeroParts)), dim3(kThreads), 0,
+                       stream, M, N, D, ldd, ws, tail_first, amax, act);
+}
+
 template <int KIND>
 void launch_ext(const Operand& A, const float* ag, const Operand& B, const float* bg, int64_t K, void* D,
-                int64_t ldd, float* amax, float* ws, const ActOut& act, hipStream_t stream) {
-  const int64_t M = A.rows, N = B.rows;
-  if (use_big(K)) {
-    const int64_t tiles = big_tiles(M, N);
-    int64_t tail_first, splits;
-    split_plan(tiles, K, tail_first, splits);
-    const int64_t grid = tail_first + (tiles - tail_first) * (splits < 0 ? 4 : splits);
-    hipLaunchKernelGGL(k_gemm_big_ext<KIND>, dim3((unsigned)grid), dim3(kThreads), big::kLdsBytes, stream, A, ag, B,
-                       bg, K, D, ldd, amax, ws, tail_first, (int)splits, act);
-    if (tail_first < tiles && splits > 0)
-      hipLaunchKernelGGL(k_split_fixup<KIND>, dim3((unsigned)((tiles - tail_first) * kZeroParts)), dim3(kThreads), 0,
-                         stream, M, N, D, ldd, ws, tail_first, amax, act);
-  } else {
-    const int64_t tiles = ((M + small::kBlockM - 1) / small::kBlockM) * ((N + small::kBlockN - 1) / small::kBlockN);
-    hipLaunchKernelGGL(k_gemm_small_ext<KIND>, dim3((unsigned)tiles), dim3(kThreads), 0, stream, A, ag, B, bg, K, D,
-                       ldd, amax, act);
+                int64_t ldd, float* amax, float* ws, hipStream_t stream) {
+  if (use_big(K)) return launch_big_ext<KIND>(A, ag, B, bg, K, D, ldd, amax, ws, ActOut{}, stream);
+  const int64_t tiles = ((A.rows + small::kBlockM - 1) / small::kBlockM) * ((B.rows + small::kBlockN - 1) / small::kBlockN);
+  hipLaunchKernelGGL(k_gemm_small_ext<KIND>, dim3((unsigned)tiles), dim3(kThreads), 0, stream, A, ag, B, bg, K, D, ldd,
+                     amax);
+}
+
+// Rows of K elements (codes and scales) copied to rows of Kp >= K, a multiple of 64, the rest zero
+// scales (and codes): 16 elements a thread. blockIdx.y: A or B.
+__global__ __launch_bounds__(kThreads) void k_pad_rows(Operand A, Operand B, int64_t K, int64_t Kp, uint8_t* codes_a,
+                                                       uint8_t* scales_a, uint8_t* codes_b, uint8_t* scales_b) {
+  const Operand& m = blockIdx.y ? B : A;
+  uint8_t* const codes = blockIdx.y ? codes_b : codes_a;
+  uint8_t* const scales = blockIdx.y ? scales_b : scales_a;
+  const int64_t from = K / 16, to = Kp / 16;                   // blocks of a row
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < m.rows * to; i += (int64_t)gridDim.x * kThreads) {
+    const int64_t row = i / to, j = i - row * to;
+    v2u32 c = {0, 0};
+    uint8_t s = 0;
+    if (j < from) {
+      c = *reinterpret_cast<const v2u32*>(m.codes + (row * from + j) * 8);
+      s = m.scales[row * from + j];
+    }
+    *reinterpret_cast<v2u32*>(codes + i * 8) = c;
+    scales[i] = s;
   }
 }
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
 
 hipError_t launch_gemm_ex(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int kind,
                           void* D, int64_t ldd, float* amax, float* ws, hipStream_t stream) {
@@ -1692,23 +1719,49 @@ hipError_t launch_gemm_ex(GemmOperand a, GemmOperand b, int64_t M, int64_t N, in
   if (M == 0 || N == 0) return hipGetLastError();
   if (use_big(K) && (e = enable_big_lds()) != hipSuccess) return e;
   const Operand A{a.codes, a.scales, M}, B{b.codes, b.scales, N};
-  const ActOut none{};
-  if (kind == kOutBF16) launch_ext<kOutBF16>(A, a.global_scale, B, b.global_scale, K, D, ldd, amax, ws, none, stream);
-  else if (kind == kOutF32Add) launch_ext<kOutF32Add>(A, a.global_scale, B, b.global_scale, K, D, ldd, amax, ws, none, stream);
-  else launch_ext<kOutF32>(A, a.global_scale, B, b.global_scale, K, D, ldd, amax, ws, none, stream);
+  if (kind == kOutBF16) launch_ext<kOutBF16>(A, a.global_scale, B, b.global_scale, K, D, ldd, amax, ws, stream);
+  else if (kind == kOutF32Add) launch_ext<kOutF32Add>(A, a.global_scale, B, b.global_scale, K, D, ldd, amax, ws, stream);
+  else launch_ext<kOutF32>(A, a.global_scale, B, b.global_scale, K, D, ldd, amax, ws, stream);
   return hipGetLastError();
 }
 
+// A K that is not a multiple of 64 is brought to one by copying both operands into the workspace
+// (9/16 byte an element, twice): the tile kernel's DMA moves scales by aligned words of four, and the
+// general kernel, which does without, reaches a tenth of its rate (1003 x 1857 x 2704: 80 us).
+int64_t gemm_act_padded_k(int64_t K) { return K > 0 ? (K + 63) / 64 * 64 : 64; }
+
+size_t gemm_act_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || gemm_act_few_rows(M, N, K)) return 0;
+  const size_t split = gemm_ex_workspace_bytes(M, N);
+  const int64_t Kp = gemm_act_padded_k(K);
+  if (Kp == K) return split;
+  return align256(split) + align256((size_t)(M * (Kp / 2))) + align256((size_t)(M * (Kp / 16))) +
+         align256((size_t)(N * (Kp / 2))) + align256((size_t)(N * (Kp / 16)));
+}
+
 hipError_t launch_gemm_act(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int act_kind, const ActOut& act,
-                           uint16_t* D, int64_t ldd, float* amax, float* ws, hipStream_t stream) {
+                           uint16_t* D, int64_t ldd, float* amax, void* ws, hipStream_t stream) {
   hipError_t e = amax ? launch_fill(amax, 1, 0.0f, stream) : hipSuccess;
   if (e != hipSuccess) return e;
   if (M == 0 || N == 0) return hipGetLastError();
-  if (M <= kSkinnyRows && K > 0) return launch_gemm_skinny(a, b, M, N, K, act_kind, act, D, ldd, amax, stream);
-  if (use_big(K) && (e = enable_big_lds()) != hipSuccess) return e;
-  const Operand A{a.codes, a.scales, M}, B{b.codes, b.scales, N};
+  if (gemm_act_few_rows(M, N, K)) return launch_gemm_skinny(a, b, M, N, K, act_kind, act, D, ldd, amax, stream);
+  if ((e = enable_big_lds()) != hipSuccess) return e;
+  Operand A{a.codes, a.scales, M}, B{b.codes, b.scales, N};
+  const int64_t Kp = gemm_act_padded_k(K);
+  if (Kp != K) {
+    uint8_t* at = static_cast<uint8_t*>(ws) + align256(gemm_ex_workspace_bytes(M, N));
+    uint8_t* const codes_a = at;
+    uint8_t* const scales_a = codes_a + align256((size_t)(M * (Kp / 2)));
+    uint8_t* const codes_b = scales_a + align256((size_t)(M * (Kp / 16)));
+    uint8_t* const scales_b = codes_b + align256((size_t)(N * (Kp / 2)));
+    const int64_t blocks = ((M > N ? M : N) * (Kp / 16) + kThreads - 1) / kThreads;
+    hipLaunchKernelGGL(k_pad_rows, dim3((unsigned)(blocks < 8192 ? blocks : 8192), 2), dim3(kThreads), 0, stream, A, B, K,
+                       Kp, codes_a, scales_a, codes_b, scales_b);
+    A = Operand{codes_a, scales_a, M};
+    B = Operand{codes_b, scales_b, N};
+  }
 #define NVFP4_GA(KD) \
-  launch_ext<kOutAct + KD>(A, a.global_scale, B, b.global_scale, K, D, ldd, amax, ws, act, stream)
+  launch_big_ext<kOutAct + KD>(A, a.global_scale, B, b.global_scale, Kp, D, ldd, amax, static_cast<float*>(ws), act, stream)
   switch (act_kind) {
     case kActRelu2: NVFP4_GA(kActRelu2); break;
     case kActGelu: NVFP4_GA(kActGelu); break;

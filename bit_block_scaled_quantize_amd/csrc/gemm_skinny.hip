@@ -1,6 +1,7 @@
-// nvfp4_gemm_act for at most 64 rows of A (the tokens of a generation step): D = act(A B^T + bias) +
+// nvfp4_gemm_act for few rows of A (the tokens of a generation step, a short prompt): D = act(A B^T + bias) +
 // residual with B's rows as the matrix instruction's rows and A's rows as its columns (skinny.h).
-// Bound by reading B: N K * 9/16 bytes.
+// Bound by reading B, N K * 9/16 bytes, up to 64 rows; beyond, workgroups on the same rows of B take 64
+// rows of A each and find B in the cache.
 #include "act_out.h"
 #include "launch.h"
 #include "skinny.h"
@@ -18,9 +19,9 @@ template <int C, bool K64>
 struct TokensNvfp4 {
   typedef Run<K64> Raw;
   Matrix a;
-  uint32_t rows, r;                                           // r: the lane's column of a fragment
+  uint32_t rows, first;                                       // first: the lane's row of A in the first fragment
   __device__ __forceinline__ Raw load(int c, uint32_t k) const {
-    const uint32_t m = 16u * (uint32_t)c + r;
+    const uint32_t m = 16u * (uint32_t)c + first;
     return load_run<K64>(a, m, m < rows, k);
   }
   __device__ __forceinline__ half8 octet(const Raw& x, uint32_t, int t) const { return octet_of(x, t); }
@@ -34,12 +35,12 @@ __global__ __launch_bounds__(kThreads) void k_gemm_skinny(GemmOperand A, GemmOpe
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * R);
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * R), m0 = (int64_t)blockIdx.y * (16 * C);
   const Matrix weights(B.codes, B.scales, N, K);
   uint32_t row[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) row[i] = (uint32_t)(n0 + 16 * i + r < N ? n0 + 16 * i + r : n0);   // rows past N: not stored
-  const TokensNvfp4<C, K64> tok{Matrix(A.codes, A.scales, M, K), (uint32_t)M, (uint32_t)r};
+  const TokensNvfp4<C, K64> tok{Matrix(A.codes, A.scales, M, K), (uint32_t)M, (uint32_t)(m0 + r)};
   float4v acc[R][C];
 #pragma unroll
   for (int i = 0; i < R; ++i)
@@ -56,7 +57,7 @@ __global__ __launch_bounds__(kThreads) void k_gemm_skinny(GemmOperand A, GemmOpe
   for (int f = wave; f < R * C; f += kWaves) {
     const int i = f / C, c = f % C;
     const float4v v = take<kWaves, R, C>(red, i, c);
-    const int64_t m = 16 * c + r, n = n0 + 16 * i + 4 * g;
+    const int64_t m = m0 + 16 * c + r, n = n0 + 16 * i + 4 * g;
     if (m < M) {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
@@ -72,7 +73,7 @@ __global__ __launch_bounds__(kThreads) void k_gemm_skinny(GemmOperand A, GemmOpe
 template <int R, int C>
 void launch_rc(const GemmOperand& a, const GemmOperand& b, int64_t M, int64_t N, int64_t K, int act, const ActOut& out,
                uint16_t* D, int64_t ldd, float* amax, hipStream_t stream) {
-  const dim3 grid((unsigned)((N + 16 * R - 1) / (16 * R)));
+  const dim3 grid((unsigned)((N + 16 * R - 1) / (16 * R)), (unsigned)((M + 16 * C - 1) / (16 * C)));
   if (K % 64 == 0)
     hipLaunchKernelGGL((k_gemm_skinny<R, C, true>), grid, dim3(kThreads), 0, stream, a, b, M, N, K, act, out, D, ldd, amax);
   else
@@ -80,6 +81,18 @@ void launch_rc(const GemmOperand& a, const GemmOperand& b, int64_t M, int64_t N,
 }
 
 }  // namespace
+
+// Up to 64 rows always; beyond by the number of workgroups, each worth 64 rows x 32 columns: the tile
+// kernel takes whole rounds of 256 x 256 tiles (or quarters of them), so its time hardly depends on
+// them below a round, and this kernel's is proportional to them. Measured, us (this kernel / tiles):
+// 5120 x 5120: 384 rows (960 workgroups) 52 / 54, 512 (1280) 66 / 54; 5120 x 20480: 384 (960) 170 / 190,
+// 512 (1280) 212 / 188; 2688 x 1856: 768 (1008) 23 / 26, 1024 (1344) 32 / 27. With a K that is not a
+// multiple of 64 (runs of 32 here, copied operands there), 5120 x 5136: 256 (640) 59 / 71, 512 (1280)
+// 96 / 71; 1857 x 2704: 512 (472) 25 / 40, 1003 (944) 42 / 42.
+bool gemm_act_few_rows(int64_t M, int64_t N, int64_t K) {
+  if (K == 0) return false;
+  return M <= 64 || (M + 63) / 64 * ((N + 31) / 32) <= (K % 64 == 0 ? 1024 : 768);
+}
 
 hipError_t launch_gemm_skinny(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int act, const ActOut& out,
                               uint16_t* D, int64_t ldd, float* amax, hipStream_t stream) {

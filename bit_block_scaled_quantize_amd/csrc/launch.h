@@ -123,7 +123,8 @@ hipError_t launch_gemm_ex(GemmOperand a, GemmOperand b, int64_t M, int64_t N, in
                           void* D, int64_t ldd, float* amax, float* ws, hipStream_t stream);
 
 // D = BF16(act(A B^T + bias) + residual), act_kind an ActKind; preact (optional) gets BF16(A B^T +
-// bias). ws as launch_gemm_ex.
+// bias). ws holds
+// gemm_act_workspace_bytes(M, N, K) bytes.
 struct ActOut {
   const void* bias;             // BF16 or FP32 [N], or null
   const uint16_t* residual;     // BF16 [M, N], row stride ldr, or null
@@ -131,11 +132,12 @@ struct ActOut {
   int64_t ldr, ldp;
   bool bias_f32;
 };
+int64_t gemm_act_padded_k(int64_t K);                   // the K that the tile kernel runs on
+size_t gemm_act_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_act(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int act_kind, const ActOut& act,
-                           uint16_t* D, int64_t ldd, float* amax, float* ws, hipStream_t stream);
-
-// The same for M <= kSkinnyRows rows of A, any K % 16 == 0, without a workspace.
-constexpr int64_t kSkinnyRows = 64;
+                           uint16_t* D, int64_t ldd, float* amax, void* ws, hipStream_t stream);
+// The kernel for few rows of A (csrc/gemm_skinny.hip): whether launch_gemm_act takes it, and it.
+bool gemm_act_few_rows(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_skinny(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int act_kind,
                               const ActOut& act, uint16_t* D, int64_t ldd, float* amax, hipStream_t stream);
 

@@ -314,8 +314,9 @@ typedef enum { NVFP4_ACT_NONE = 0, NVFP4_ACT_RELU2 = 1, NVFP4_ACT_GELU = 2, NVFP
  *              nvfp4_act_grad needs. Overlaps no other argument.
  *   amax_out   NULL, or device float[1] receiving max|D| over the values as stored (the amax_in of
  *              D's next quantization). The library clears it.
- *   workspace  nvfp4_workspace_size(NVFP4_OP_GEMM_ACT, M, N, 1) bytes, 256-byte aligned (NULL
- *              allowed for 0 bytes).
+ *   workspace  nvfp4_workspace_size(NVFP4_OP_GEMM_ACT, M, N, K) bytes, 256-byte aligned (NULL
+ *              allowed for 0 bytes): partial sums, and for a K that is not a multiple of 64 both
+ *              operands with zeros up to one.
  * The result is deterministic for a given device. Errors: NVFP4_ERR_INVALID (null pointers, K
  * mismatch, K % 16, a stride below N, bad enum, misaligned buffers), NVFP4_ERR_UNSUPPORTED
  * (operand size), NVFP4_ERR_WORKSPACE, NVFP4_ERR_HIP.
@@ -553,7 +554,8 @@ int nvfp4_adamw_table(const nvfp4_adamw_tensor* tensors, int64_t count, nvfp4_st
  * no memory itself (caller-owned buffers, see the conventions above), so the partial maxima of
  * the tensor amax (the FP32 tensor scale of "Nemotron NVFP4" explainer, "What NVFP4 actually
  * is") and the K-split partial sums of nvfp4_gemm_ex live in a workspace the caller sizes with
- * this call. ops: nvfp4_op; rows/cols/nseg as in the call the workspace is for. */
+ * this call. ops: nvfp4_op; rows/cols/nseg as in the call the workspace is for (for
+ * NVFP4_OP_GEMM_ACT: M, N, K; for NVFP4_OP_ACT_GRAD: M, N, 1). */
 size_t nvfp4_workspace_size(int op, int64_t rows, int64_t cols, int64_t nseg);
 
 /* Thread-local description of the last non-OK status returned on this thread: the error

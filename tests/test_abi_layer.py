@@ -99,7 +99,7 @@ def test_gemm_act_validation(lib):
     assert call(res=FAKE + 1, ldr=32) == INVALID
     assert call(pre=FAKE, ldp=31) == INVALID
     assert call(amax=FAKE + 2) == INVALID
-    need = lib.nvfp4_workspace_size(nv.OP_GEMM_ACT, 8192, 5120, 1)
+    need = lib.nvfp4_workspace_size(nv.OP_GEMM_ACT, 8192, 5120, 128)
     assert need > 0
     big = dict(A=_t(8192, 128), B=_t(5120, 128), ldd=5120)
     assert call(**big) == WORKSPACE

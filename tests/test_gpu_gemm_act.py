@@ -3,8 +3,9 @@
 gemm_act: the pre-activation is the FP32 GEMM's result (itself held to its bound by
 test_gpu_gemm.py) plus the bias, one FP32 addition, rounded once to BF16, bit for bit. D against
 act in 64 bits of that FP32 value: act's evaluation error (oracle.act_error), one FP32 addition of
-the residual (u) and one rounding to BF16 (2^-8 relative, 2^-134 below the normal range). Up to 64
-rows a kernel of its own sums in another order: its pre-activation is held to the GEMM's bound,
+the residual (u) and one rounding to BF16 (2^-8 relative, 2^-134 below the normal range). For few
+rows a kernel of its own sums in another order, and for a K that is not a multiple of 64 the GEMM
+itself has another kernel: there the pre-activation is held to the GEMM's bound,
 ez = 1e-5 sum |a||b| + u |z| around the 64-bit product, and D to act over that range.
 act_grad: dZ likewise with oracle.act_slope_error and one product (u); dbias sums M terms, each
 addition within u of the running sum: (M + 2) u of the sum of magnitudes."""
@@ -59,11 +60,13 @@ def _check_d(d, z32, act, res, what, ez=0.0):
     assert np.all(err <= tol), f"{what}: {(err > tol).sum()} elements, first {np.argwhere(err > tol)[0]}"
 
 
-# one row; few rows on both sides of 16, 32 and 64; a K that ends inside a step of 64 and of 128;
-# odd N (no whole vectors); 90 tiles of 256 x 256 (split along K); a last round in column quarters
+# one row; few rows on both sides of 16, 32 and 64; a K that ends inside a step of 64, 128 and 256;
+# odd N (rows on any boundary); then the tile kernel: odd sizes, operands brought to a K of 128, 2752
+# and 64, 90 tiles of 256 x 256 (split along K), a last round in column quarters
 SHAPES = [(1, 272, 256), (1, 48, 16), (2, 33, 80), (7, 1857, 272), (16, 512, 1344), (17, 520, 2688), (33, 256, 2704),
           (63, 100, 640), (64, 1000, 512), (65, 264, 512), (300, 520, 512), (130, 257, 272), (257, 33, 128),
-          (1000, 700, 1344), (2304, 2560, 256), (520, 16640, 128)]
+          (1000, 700, 1344), (1100, 2001, 576), (2050, 1030, 80), (1003, 1857, 2704), (1500, 1400, 48),
+          (2304, 2560, 256), (520, 16640, 128)]
 
 
 @pytest.mark.parametrize("mnk", SHAPES)
@@ -72,7 +75,8 @@ def test_gemm_act(mnk):
     log(f"gemm_act {mnk}")
     qa, qb = _operands(m, n, k, 900 + m + n + k)
     d32 = _host(nv.gemm(qa, qb))
-    if m <= 64:
+    same_order = -(-m // 64) * -(-n // 32) > 1024 and k % 64 == 0
+    if not same_order:
         ah, bh = (oracle.dequantize(*host(q)).astype(np.float64) for q in (qa, qb))
         d64, s64 = ah @ bh.T, np.abs(ah) @ np.abs(bh).T
     variants = [("none", None, False, 0), ("relu2", "bf16", False, 0), ("gelu", "fp32", True, 0),
@@ -88,7 +92,7 @@ def test_gemm_act(mnk):
         d = nv.gemm_act(qa, qb, bias=bias, activation=act, residual=res, out=out, preact=pre, amax_out=amax)
         torch.cuda.synchronize()
         what = f"gemm_act {mnk} {act}"
-        if m > 64:
+        if same_order:
             z32 = d32 if bias is None else (d32 + _host(bias)[None, :]).astype(np.float32)
             assert_bytes_equal(_host(pre).view(np.uint32), oracle.round_bf16(z32).view(np.uint32), what + " preact")
             ez = np.zeros(z32.shape)
@@ -107,12 +111,12 @@ def test_gemm_act(mnk):
 
 def test_gemm_act_is_the_bf16_gemm_without_extras():
     log("gemm_act plain")
-    for m, n, k in ((300, 520, 512), (130, 257, 272), (2304, 2560, 256)):
+    for m, n, k in ((2000, 1300, 512), (2304, 2560, 256)):
         qa, qb = _operands(m, n, k, 40)
         assert torch.equal(nv.gemm_act(qa, qb), nv.gemm_ex(qa, qb, out_dtype=torch.bfloat16))
 
 
-@pytest.mark.parametrize("m", [3, 300])
+@pytest.mark.parametrize("m", [3, 300, 8000])
 def test_residual_in_place(m):
     log(f"gemm_act residual in place {m}")
     qa, qb = _operands(m, 264, 512, 50)
@@ -122,11 +126,10 @@ def test_residual_in_place(m):
     assert torch.equal(got, want)
 
 
-@pytest.mark.parametrize("m", [5, 260])
-def test_signs_and_special_values(m):
+@pytest.mark.parametrize("m,n", [(5, 64), (260, 64), (1100, 2048)])
+def test_signs_and_special_values(m, n):
     """Large and tiny pre-activations, an infinite bias, NaN in the residual: each stays in its place."""
-    log(f"gemm_act special {m}")
-    n = 64
+    log(f"gemm_act special {m} {n}")
     qa, qb = _operands(m, n, 128, 60)
     bias = torch.zeros((n,), device="cuda")
     bias[:8] = torch.tensor([float("inf"), float("-inf"), 3e38, -3e38, 200.0, -200.0, 40.0, -40.0])
@@ -143,7 +146,7 @@ def test_signs_and_special_values(m):
 def test_gemm_act_streams_and_graph():
     """On another stream, and in a captured graph replayed with other work between."""
     log("gemm_act graph")
-    for m in (4, 300):
+    for m in (4, 300, 4100):
         qa, qb = _operands(m, 520, 512, 70)
         bias = to_device_bf16(workloads.normal_bf16((1, 520), 71)).reshape(520)
         amax, amax2 = torch.zeros((1,), device="cuda"), torch.zeros((1,), device="cuda")
@@ -154,7 +157,7 @@ def test_gemm_act_streams_and_graph():
         s.synchronize()
         assert torch.equal(got, want)
         out = torch.zeros_like(want)
-        ws = torch.empty((nv.workspace_size(nv.OP_GEMM_ACT, m, 520) + 256,), dtype=torch.uint8, device="cuda")
+        ws = torch.empty((nv.workspace_size(nv.OP_GEMM_ACT, m, 520, 512) + 256,), dtype=torch.uint8, device="cuda")
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             nv.gemm_act(qa, qb, bias=bias, activation="gelu", out=out, amax_out=amax2, workspace=ws)
