@@ -1,0 +1,114 @@
+"""AdamW for the layers of this package: one kernel launch a step for all of their tensors.
+
+artiverse.ca "NVIDIA's 4-bit floating point pushes AI training limits" (paragraph on which parts
+run in 4-bit): optimizer states and master weights stay in higher precision. The class only holds the
+buffers and orders the calls; the arithmetic is nvfp4_adamw's.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import AdamWPlan, AdamWTensor, NVFP4Error, adamw
+from .linear import NVFP4Linear
+
+
+class AdamW:
+    """entries: (parameter, gradient, weight_decay) triples, or (parameter, gradient) with the default
+    decay. A BF16 parameter gets an FP32 master copy; an FP32 one is updated itself. The gradient (FP32
+    or BF16, the parameter's shape) is read where it is at every step.
+
+    states: "fp32", or "8bit" (two bytes and a sixteenth per element instead of eight).
+    max_norm: clip the gradients' norm over all tensors; step() then returns the norm (a device
+    float [1]), and a step whose norm is not finite changes nothing but the step count.
+    amax: device float, one per tensor: max|weight| after the latest step.
+    """
+
+    def __init__(self, entries, lr: float = 3e-4, betas=(0.9, 0.95), eps: float = 1e-8, weight_decay: float = 0.1,
+                 states: str = "fp32", max_norm: float | None = None, seed: int = 0, layers=()):
+        if states not in ("fp32", "8bit"):
+            raise NVFP4Error(f"unknown states {states!r}: fp32 or 8bit")
+        self.lr, self.betas, self.eps, self.max_norm, self.seed = lr, betas, eps, max_norm, seed
+        self.states, self.steps = states, 0
+        self.params, self.grads, self.masters, tensors = [], [], [], []
+        for entry in entries:
+            param, grad, *decay = entry
+            p = param.detach()
+            if p.dtype not in (torch.bfloat16, torch.float32) or not p.is_contiguous():
+                raise NVFP4Error("parameters must be contiguous bfloat16 or float32 tensors")
+            if grad is None or grad.shape != p.shape:
+                raise NVFP4Error("every parameter needs a gradient of its shape that stays where it is")
+            master = p.float() if p.dtype == torch.bfloat16 else p
+            tensors.append(AdamWTensor(p=master, grad=grad, weight_decay=decay[0] if decay else weight_decay,
+                                       w_out=p if p.dtype == torch.bfloat16 else None, **self._state(p)))
+            self.params.append(p)
+            self.grads.append(grad)
+            self.masters.append(master)
+        self.plan = AdamWPlan(tensors)
+        self.amax = torch.zeros((len(tensors),), dtype=torch.float32, device=self.plan.device)
+        self._layers = list(layers)                          # (index of the weight, layer)
+
+    def _state(self, p):
+        n, dev = p.numel(), p.device
+        if self.states == "fp32":
+            return {k: torch.zeros((n,), dtype=torch.float32, device=dev) for k in ("m", "v")}
+        return {k: torch.zeros((n if len(k) == 1 else (n + 31) // 32,), dtype=torch.uint8, device=dev)
+                for k in ("m", "v", "m_scale", "v_scale")}
+
+    @classmethod
+    def of(cls, module: torch.nn.Module, weight_decay: float = 0.1, **kw):
+        """Of every parameter of a module: NVFP4Linear weights with their main_grad and decay, their
+        biases and every other parameter of one dimension without decay. A parameter without a main
+        gradient gets a .grad that has to stay in place (zero_grad of this class, not
+        set_to_none)."""
+        entries, layers, seen = [], [], set()
+        for m in module.modules():
+            if isinstance(m, NVFP4Linear):
+                if m.main_grad is not None and id(m.weight) not in seen:
+                    layers.append((len(entries), m))
+                    entries.append((m.weight, m.main_grad, weight_decay))
+                    seen.add(id(m.weight))
+                if m.bias is not None and m.bias_main_grad is not None and id(m.bias) not in seen:
+                    entries.append((m.bias, m.bias_main_grad, 0.0))
+                    seen.add(id(m.bias))
+        for p in module.parameters():
+            if id(p) in seen or not p.requires_grad:
+                continue
+            if p.grad is None:
+                p.grad = torch.zeros_like(p)
+            entries.append((p, p.grad, weight_decay if p.dim() > 1 else 0.0))
+            seen.add(id(p))
+        return cls(entries, weight_decay=weight_decay, layers=layers, **kw)
+
+    def step(self, lr: float | None = None):
+        """One step; returns the gradients' norm with max_norm, else None."""
+        self.steps += 1
+        norm = adamw(self.plan, lr=self.lr if lr is None else lr, betas=self.betas, eps=self.eps, step=self.steps,
+                     max_norm=self.max_norm, seed=self.seed, amax_out=self.amax)
+        for i, layer in self._layers:
+            layer.weight_amax = self.amax[i:i + 1]
+        return norm
+
+    def zero_grad(self):
+        torch._foreach_zero_(self.grads)
+
+    def state_dict(self) -> dict:
+        keys = ("m", "v") if self.states == "fp32" else ("m", "v", "m_scale", "v_scale")
+        return {"states": self.states, "steps": self.steps, "seed": self.seed,
+                "masters": [m.clone() for m in self.masters],
+                **{k: [getattr(t, k).clone() for t in self.plan.tensors] for k in keys}}
+
+    def load_state_dict(self, state: dict):
+        """Restores masters, states and step count, and the BF16 weights from the masters."""
+        if state["states"] != self.states or len(state["masters"]) != len(self.masters):
+            raise NVFP4Error("the state is of another optimizer")
+        keys = ("m", "v") if self.states == "fp32" else ("m", "v", "m_scale", "v_scale")
+        for mine, theirs in [(self.masters, state["masters"])] + [
+                ([getattr(t, k) for t in self.plan.tensors], state[k]) for k in keys]:
+            for a, b in zip(mine, theirs):
+                a.copy_(b)
+        for p, m in zip(self.params, self.masters):
+            if p is not m:
+                p.copy_(m)
+        for _, layer in self._layers:
+            layer.weight_amax = None                         # of the weights before
+        self.steps, self.seed = state["steps"], state["seed"]
