@@ -74,7 +74,7 @@ constexpr int kMaxAmaxPartials = 1024;
 
 // AdamW over many tensors. The device table is `count` entries followed by one int32 per chunk
 // (the entry that the chunk belongs to); a chunk is kAdamWChunk consecutive elements of one tensor.
-constexpr int64_t kAdamWChunk = 8192;
+constexpr int64_t kAdamWChunk = 2048;
 constexpr int kAdamWMaxParts = 1024;                     // partial sums of the gradient norm
 enum AdamWFlags : int32_t { kAdamWGradBf16 = 1 };
 struct AdamWEntry {

@@ -32,7 +32,7 @@ namespace {
 using namespace skinny;
 
 
-constexpr int kRouteThreads = 256, kRouteWaves = 4;
+constexpr int kRouteThreads = 512, kRouteWaves = 8;
 constexpr int kRouteExperts = 4;                              // per workgroup of k_route
 constexpr int kGroupTokens = 8;                               // tokens per workgroup of k_route
 
@@ -168,7 +168,13 @@ __device__ __forceinline__ void pick_experts(const MoeArgs& a, const MoeWork& w,
     }
     const float l = wave_fold_max(best);                      // the pick's logit
     // among the lanes that hold it the lowest expert; top_k <= experts: one is left
-    const int e = (int)wave_fold_min(at >= 0 && best == l ? (uint32_t)(lane + 64 * at) : 0xFFFFFFFFu);
+    int e = 0;
+#pragma unroll
+    for (int q = kPer - 1; q >= 0; --q) {
+      if (64 * q >= a.experts) continue;
+      const uint64_t have = __ballot(at == q && best == l);
+      e = have != 0 ? 64 * q + __builtin_ctzll(have) : e;
+    }
     if ((e & 63) == lane) taken |= 1u << (e >> 6);
     const float s = a.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top) / denom;
     total += s;
@@ -242,8 +248,8 @@ __device__ __forceinline__ void sort_pairs(const MoeArgs& a, const MoeWork& w, c
 }
 
 // Grid: x = blocks of 4 experts, then 8 blocks that bring one token each to FP16; y = groups of 8
-// tokens. A logit block's waves split the hidden dimension, two places a turn, so that a row's loads
-// are in flight together. NT: tokens of a group computed (1, or 8 with the surplus repeating the first).
+// tokens. A logit block's waves split the hidden dimension, so that a row's loads are in flight
+// together. NT: tokens of a group computed (1, or 8 with the surplus repeating the first).
 // VEC: x's rows and the router's start on 16 bytes.
 template <bool F32, int NT, bool VEC>
 __global__ __launch_bounds__(kRouteThreads) void k_route(MoeArgs a, MoeWork w) {
@@ -262,19 +268,19 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(MoeArgs a, MoeWork w) {
     const int t = t0 + q;
     const Row row = row_of<false, VEC>(a.x + (int64_t)t * a.ldx, H);
     float top = 0.0f;
-    for (int i = threadIdx.x * 8; i < H; i += 2 * kTurn) {
-      Eight<false, VEC> v[2];
+    for (int i = threadIdx.x * 8; i < H; i += kTurn) {
+      Eight<false, VEC> v;
+      v.load(row, i, H);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) v[j].load(row, i + j * kTurn, H);
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[j][k]));
+      for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]));
     }
     top = wave_fold_max(top);
     if (lane == 0) red[wave][0] = top;
     __syncthreads();
-    const float s = half_scale(fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0])));
+    top = red[0][0];
+#pragma unroll
+    for (int v = 1; v < kRouteWaves; ++v) top = fmaxf(top, red[v][0]);
+    const float s = half_scale(top);
     for (int i = threadIdx.x * 8; i < H; i += kTurn) {         // H is a multiple of 16
       Eight<false, VEC> v;
       v.load(row, i, H);
@@ -288,28 +294,22 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(MoeArgs a, MoeWork w) {
   }
   const int e0 = blockIdx.x * kRouteExperts;
   float acc[kRouteExperts][NT] = {};
-  for (int i = threadIdx.x * 8; i < H; i += 2 * kTurn) {
-    Eight<F32, VEC> r[kRouteExperts][2];
+  for (int i = threadIdx.x * 8; i < H; i += kTurn) {
+    Eight<F32, VEC> r[kRouteExperts];
+    Eight<false, VEC> v[NT];
 #pragma unroll
-    for (int e = 0; e < kRouteExperts; ++e) {
-      const Row row = row_of<F32, VEC>(static_cast<const uint8_t*>(a.router) +
-                                           (int64_t)(e0 + e < a.experts ? e0 + e : e0) * H * (F32 ? 4 : 2), H);
+    for (int e = 0; e < kRouteExperts; ++e)
+      r[e].load(row_of<F32, VEC>(static_cast<const uint8_t*>(a.router) +
+                                     (int64_t)(e0 + e < a.experts ? e0 + e : e0) * H * (F32 ? 4 : 2), H), i, H);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) r[e][j].load(row, i + j * kTurn, H);
-    }
+    for (int q = 0; q < NT; ++q)
+      v[q].load(row_of<false, VEC>(a.x + (int64_t)(t0 + (q < nt ? q : 0)) * a.ldx, H), i, H);
 #pragma unroll
-    for (int q = 0; q < NT; ++q) {
-      const Row row = row_of<false, VEC>(a.x + (int64_t)(t0 + (q < nt ? q : 0)) * a.ldx, H);
-      Eight<false, VEC> v[2];
+    for (int q = 0; q < NT; ++q)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) v[j].load(row, i + j * kTurn, H);
+      for (int e = 0; e < kRouteExperts; ++e)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < kRouteExperts; ++e)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) acc[e][q] = __builtin_fmaf(r[e][j][k], v[j][k], acc[e][q]);
-    }
+        for (int k = 0; k < 8; ++k) acc[e][q] = __builtin_fmaf(r[e][k], v[q][k], acc[e][q]);
   }
 #pragma unroll
   for (int e = 0; e < kRouteExperts; ++e)
@@ -321,9 +321,10 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(MoeArgs a, MoeWork w) {
   __syncthreads();
   if (threadIdx.x < kRouteExperts * NT) {
     const int e = threadIdx.x / NT, q = threadIdx.x % NT;
-    if (e0 + e < a.experts && q < nt)
-      put_shared(&w.logits[(int64_t)(t0 + q) * a.experts + e0 + e],
-                 (red[0][threadIdx.x] + red[1][threadIdx.x]) + (red[2][threadIdx.x] + red[3][threadIdx.x]));
+    float l = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kRouteWaves; ++v) l += red[v][threadIdx.x];
+    if (e0 + e < a.experts && q < nt) put_shared(&w.logits[(int64_t)(t0 + q) * a.experts + e0 + e], l);
   }
   if (!last_to_finish(&w.counters[1 + blockIdx.y], blocks)) return;
   for (int q = wave; q < nt; q += kRouteWaves) pick_experts(a, w, t0 + q, own_ids + q * a.top_k);
@@ -350,13 +351,55 @@ struct TokensLds {
   }
 };
 
+// y[t][n], y[t][n + 1] of the tokens t = first, first + step, ...: the routed experts' parts added in order,
+// the loads of two tokens' eight experts in flight together.
+__device__ __forceinline__ void join_pairs(const MoeArgs& a, const MoeWork& w, int64_t n, int first, int step) {
+  const int64_t N = a.hidden;
+  if (n >= N) return;
+  for (int t0 = first; t0 < a.tokens; t0 += 2 * step) {
+    const int t1 = t0 + step < a.tokens ? t0 + step : t0;
+    float lo[2] = {}, hi[2] = {};
+    for (int j0 = 0; j0 < a.top_k; j0 += 8) {
+      uint64_t v[2][8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int jj = j0 + j < a.top_k ? j0 + j : j0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          v[i][j] = get_shared(reinterpret_cast<const uint64_t*>(w.part + ((int64_t)(i ? t1 : t0) * a.top_k + jj) * N + n));
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j0 + j < a.top_k) {                               // uniform
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            lo[i] += __uint_as_float((uint32_t)v[i][j]);
+            hi[i] += __uint_as_float((uint32_t)(v[i][j] >> 32));
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = t0 + i * step;
+      if (t < a.tokens) {
+        uint16_t* y = a.y + (int64_t)t * a.ldy + n;
+        const uint32_t b = bf16_rn_pair(lo[i], hi[i]);
+        y[0] = (uint16_t)b;
+        y[1] = (uint16_t)(b >> 16);
+      }
+    }
+  }
+}
+
 // 16 R weight rows of one used expert times its tokens, kCols at a time (the weights' second and
 // later readings come from the cache). Grid: used experts (as many as there can be; the surplus
 // leaves at once) x row tiles, tiles of one expert next to each other.
 // UP: rows of W1, K = hidden -> h[pair][f]. GATED: fragments 0 .. R/2 - 1 hold the gate's rows, the
 // others the same rows of U. DOWN: rows of W2, K = ffn -> part[pair][n], then y.
-// kCols: columns staged at a time (8, or 1 for one token). W: waves, which split K.
-template <bool UP, bool GATED, int R, int W, int kCols, bool K64>
+// kCols: columns staged at a time (8, or 1 for one token). W: waves, which split K. A: steps in flight.
+// JOIN: the last workgroup of a row tile writes y.
+template <bool UP, bool GATED, int R, int W, int A, int kCols, bool JOIN, bool K64>
 __global__ __launch_bounds__(64 * W) void k_expert(MoeArgs a, MoeWork w, int tiles, uint32_t pitch) {
   constexpr int kWaves = W, kThreads = 64 * W;
   static_assert(!GATED || R % 2 == 0, "a gated tile holds as many gate as up fragments");
@@ -398,7 +441,7 @@ __global__ __launch_bounds__(64 * W) void k_expert(MoeArgs a, MoeWork w, int til
     for (int i = 0; i < R; ++i) acc[i][0] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
     float inv = 1.0f;                                         // undoes the column's power of two
     float scale = 1.0f;                                       // DOWN: the column's, in the lanes of row c
-    Pipe<R, 1, 2, K64, TokensLds> pipe;
+    Pipe<R, 1, A, K64, TokensLds> pipe;
     for (int64_t k0 = 0; k0 < K; k0 += kChunk) {
       const int64_t len = K - k0 < kChunk ? K - k0 : kChunk;
       const int first = (int)(k0 / kStep<K64>) + wave;
@@ -508,86 +551,57 @@ __global__ __launch_bounds__(64 * W) void k_expert(MoeArgs a, MoeWork w, int til
         }
       } else if (live && n < N) {
         uint64_t* out = reinterpret_cast<uint64_t*>(w.part + (int64_t)pair * N + n);
-        put_shared(out, (uint64_t)__float_as_uint(v[0]) | (uint64_t)__float_as_uint(v[1]) << 32);
-        put_shared(out + 1, (uint64_t)__float_as_uint(v[2]) | (uint64_t)__float_as_uint(v[3]) << 32);
+        if constexpr (!JOIN) *reinterpret_cast<float4v*>(out) = v;
+        else put_shared(out, (uint64_t)__float_as_uint(v[0]) | (uint64_t)__float_as_uint(v[1]) << 32);
+        if constexpr (JOIN) put_shared(out + 1, (uint64_t)__float_as_uint(v[2]) | (uint64_t)__float_as_uint(v[3]) << 32);
       }
     }
     // (the next round's first barrier, after its pipe.start, keeps put from overtaking take)
   }
-  if constexpr (!UP) {
+  if constexpr (JOIN) {
     if (!last_to_finish(&w.counters[1 + kMoeMaxTokens / kGroupTokens + tile], *w.used)) return;
-    // y, two rows of a token a thread, the loads of two tokens' eight experts in flight together
-    constexpr int kPairs = 8 * R, kTokens = kThreads / kPairs;
-    const int n = threadIdx.x % kPairs * 2;
-    if (n0 + n >= N) return;
-    for (int t0 = threadIdx.x / kPairs; t0 < a.tokens; t0 += 2 * kTokens) {
-      const int t1 = t0 + kTokens < a.tokens ? t0 + kTokens : t0;
-      float lo[2] = {}, hi[2] = {};
-      for (int j0 = 0; j0 < a.top_k; j0 += 8) {
-        uint64_t v[2][8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int jj = j0 + j < a.top_k ? j0 + j : j0;
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            v[i][j] = get_shared(reinterpret_cast<const uint64_t*>(
-                w.part + ((int64_t)(i ? t1 : t0) * a.top_k + jj) * N + n0 + n));
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (j0 + j < a.top_k) {                             // uniform
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              lo[i] += __uint_as_float((uint32_t)v[i][j]);
-              hi[i] += __uint_as_float((uint32_t)(v[i][j] >> 32));
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = t0 + i * kTokens;
-        if (t < a.tokens) {
-          uint16_t* y = a.y + (int64_t)t * a.ldy + n0 + n;
-          const uint32_t b = bf16_rn_pair(lo[i], hi[i]);
-          y[0] = (uint16_t)b;
-          y[1] = (uint16_t)(b >> 16);
-        }
-      }
-    }
+    constexpr int kPairs = 8 * R;
+    join_pairs(a, w, n0 + threadIdx.x % kPairs * 2, threadIdx.x / kPairs, kThreads / kPairs);
   }
 }
 
+// y after a k_expert<DOWN> that left the joining to a launch of its own: 64 rows x 8 tokens a workgroup.
+__global__ __launch_bounds__(256) void k_join(MoeArgs a, MoeWork w) {
+  join_pairs(a, w, (int64_t)blockIdx.x * 64 + threadIdx.x % 32 * 2, (int)blockIdx.y * 8 + (int)threadIdx.x / 32, 64);
+}
+
 constexpr int kWideTokens = 4;                                // up to here 8 waves split K, beyond 4
-constexpr int kRows = 2;                                      // fragments of 16 rows per workgroup
 constexpr int kMostCols = 8;                                  // tokens of an expert at a time
-constexpr int kMostLds = 8 * kRows * 64 * 16 + kZeroBytes + kMostCols * (2 * kChunk + 16);
+constexpr int kMostLds = 8 * 4 * 64 * 16 + kZeroBytes + kMostCols * (2 * kChunk + 16);
 
 int64_t tiles_of(int64_t rows, int frags) { return (rows + 16 * frags - 1) / (16 * frags); }
 
-template <bool UP, bool GATED, int W, int COLS, bool K64>
+template <bool UP, bool GATED, int R, int W, int A, int COLS, bool JOIN, bool K64>
 hipError_t launch_expert_as(const MoeArgs& a, const MoeWork& w, hipStream_t stream) {
   // the staged columns can take more LDS than a launch may by default
-  static const hipError_t ready = hipFuncSetAttribute((const void*)k_expert<UP, GATED, kRows, W, COLS, K64>,
+  static const hipError_t ready = hipFuncSetAttribute((const void*)k_expert<UP, GATED, R, W, A, COLS, JOIN, K64>,
                                                       hipFuncAttributeMaxDynamicSharedMemorySize, kMostLds);
   if (ready != hipSuccess) return ready;
   const int64_t K = UP ? a.hidden : a.ffn, N = UP ? a.ffn : a.hidden;
   const int64_t pairs = (int64_t)a.tokens * a.top_k;
   const int64_t most = pairs < a.experts ? pairs : a.experts;
-  const int tiles = (int)tiles_of(N, GATED ? kRows / 2 : kRows);
+  const int tiles = (int)tiles_of(N, GATED ? R / 2 : R);
   const int64_t staged = K < kChunk ? (K + kStep<K64> - 1) / kStep<K64> * kStep<K64> : kChunk;
   const uint32_t pitch = (uint32_t)(2 * staged + 16);         // rows start 4 banks apart
-  const size_t bytes = (size_t)W * kRows * 64 * 16 + kZeroBytes + (size_t)COLS * pitch;
-  hipLaunchKernelGGL((k_expert<UP, GATED, kRows, W, COLS, K64>), dim3((unsigned)(most * tiles)), dim3(64 * W), bytes,
+  const size_t bytes = (size_t)W * R * 64 * 16 + kZeroBytes + (size_t)COLS * pitch;
+  hipLaunchKernelGGL((k_expert<UP, GATED, R, W, A, COLS, JOIN, K64>), dim3((unsigned)(most * tiles)), dim3(64 * W), bytes,
                      stream, a, w, tiles, pitch);
   return hipSuccess;
 }
 
 template <bool UP, bool GATED, bool K64>
 hipError_t launch_expert_k(const MoeArgs& a, const MoeWork& w, hipStream_t stream) {
-  if (a.tokens == 1) return launch_expert_as<UP, GATED, 8, 1, K64>(a, w, stream);
-  if (a.tokens <= kWideTokens) return launch_expert_as<UP, GATED, 8, kMostCols, K64>(a, w, stream);
-  return launch_expert_as<UP, GATED, 4, kMostCols, K64>(a, w, stream);
+  // (us on 122 experts of 2688 x 1856, 64 tokens: up R = 2 with A = 1, 2, 3: 95, 95, 93, R = 4: 98; down
+  // R = 2: 108 with A = 1, 110 with 2; R = 4: 96 with A = 1, 115 with 2. 8 waves: down 129 to 140)
+  constexpr int R = UP ? 2 : 4, A = UP ? 3 : 1;
+  if (a.tokens == 1) return launch_expert_as<UP, GATED, 2, 8, 2, 1, !UP, K64>(a, w, stream);
+  if (a.tokens <= kWideTokens) return launch_expert_as<UP, GATED, 2, 8, 2, kMostCols, !UP, K64>(a, w, stream);
+  return launch_expert_as<UP, GATED, R, 4, A, kMostCols, false, K64>(a, w, stream);
 }
 
 template <bool UP, bool GATED>
@@ -650,6 +664,9 @@ hipError_t launch_moe(const MoeArgs& a, uint8_t* ws, hipStream_t stream) {
 #undef NVFP4_RT
   hipError_t e = a.gated ? launch_expert<true, true>(a, w, stream) : launch_expert<true, false>(a, w, stream);
   if (e != hipSuccess || (e = launch_expert<false, false>(a, w, stream)) != hipSuccess) return e;
+  if (a.tokens > kWideTokens)
+    hipLaunchKernelGGL(k_join, dim3((unsigned)((a.hidden + 63) / 64), (unsigned)((a.tokens + 7) / 8)), dim3(256), 0,
+                       stream, a, w);
   return hipGetLastError();
 }
 
