@@ -140,12 +140,11 @@ def _check(status: int):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
 def _on_stream(fn):
@@ -215,7 +214,7 @@ class MXFP4Tensor:
 def _input(x: torch.Tensor):
     if x.dtype not in _DTYPE:
         raise NVFP4Error(f"unsupported input dtype {x.dtype}")
-    if x.dim() != 2 or x.stride(1) != 1 or x.device.type != "cuda":
+    if x.dim() != 2 or x.stride(1) != 1 or not x.is_cuda:
         raise NVFP4Error("input must be a 2-D GPU tensor with unit column stride")
     return _DTYPE[x.dtype], x.shape[0], x.shape[1], x.stride(0)
 
@@ -229,13 +228,13 @@ def _check_q(q, nseg: int = 1, what: str = "tensor"):
     if not mx:
         need += ((q.global_scale, nseg),)
     for t, n in need:
-        if t.numel() < n or not t.is_contiguous() or t.device.type != "cuda":
+        if t.numel() < n or not t.is_contiguous() or not t.is_cuda:
             raise NVFP4Error(f"{what}: buffer of {t.numel()} elements (contiguous, on the GPU) needed {n}")
 
 
 def _check_out(out: torch.Tensor, rows: int, cols: int, dtype, what: str = "out"):
     """A 2-D output with at least rows x cols elements, unit column stride, the given dtype."""
-    if out.dtype != dtype or out.dim() != 2 or out.stride(1) != 1 or out.device.type != "cuda":
+    if out.dtype != dtype or out.dim() != 2 or out.stride(1) != 1 or not out.is_cuda:
         raise NVFP4Error(f"{what} must be a 2-D {dtype} GPU tensor with unit column stride")
     if out.shape[0] < rows or out.shape[1] < cols:
         raise NVFP4Error(f"{what} shape {tuple(out.shape)} smaller than ({rows}, {cols})")
@@ -254,7 +253,7 @@ def _check_table(t, what: str):
 
 
 def _check_vec(t, n: int, what: str):
-    if t is not None and (t.dtype != torch.float32 or t.numel() < n or t.device.type != "cuda"
+    if t is not None and (t.dtype != torch.float32 or t.numel() < n or not t.is_cuda
                           or not t.is_contiguous()):
         raise NVFP4Error(f"{what} must be a contiguous float32 GPU tensor of at least {n} elements")
 
@@ -696,22 +695,26 @@ def moe_tokens(x: torch.Tensor, weights: MoEWeights, out: torch.Tensor | None = 
     """nvfp4_moe_tokens: the whole expert layer for x [tokens <= 64, hidden] (bfloat16). ids_out
     (int32) and weights_out (float32), both [tokens, top_k], receive the routing. workspace: one of
     moe_workspace's, kept between calls (calls that share one have to be ordered)."""
+    if workspace is None and x.dim() == 2 and x.shape[0] > 0:
+        workspace = moe_workspace(weights, x.shape[0])
+    return _moe_call(x, weights.c(), out, ids_out, weights_out, workspace, stream)
+
+
+def _moe_call(x, layer: _CMoE, out, ids_out, weights_out, workspace, stream):
     lib = _load()
     if x.dtype != torch.bfloat16:
         raise NVFP4Error("x must be bfloat16")
     _, tokens, hidden, _ = _input(x)
-    layer = weights.c()
     if hidden != layer.hidden:
         raise NVFP4Error(f"x has {hidden} columns, the layer's hidden size is {layer.hidden}")
     if out is None:
         out = torch.empty((tokens, hidden), dtype=torch.bfloat16, device=x.device)
-    _check_out(out, tokens, hidden, torch.bfloat16)
+    else:
+        _check_out(out, tokens, hidden, torch.bfloat16)
+    n = tokens * layer.top_k
     for t, dtype, what in ((ids_out, torch.int32, "ids_out"), (weights_out, torch.float32, "weights_out")):
-        if t is not None and (t.dtype != dtype or t.numel() < tokens * weights.top_k or not t.is_contiguous()
-                              or t.device.type != "cuda"):
-            raise NVFP4Error(f"{what} must be a contiguous {dtype} GPU tensor of at least {tokens * weights.top_k} elements")
-    if workspace is None and 0 < tokens:
-        workspace = moe_workspace(weights, tokens)
+        if t is not None and (t.dtype != dtype or t.numel() < n or not t.is_contiguous() or not t.is_cuda):
+            raise NVFP4Error(f"{what} must be a contiguous {dtype} GPU tensor of at least {n} elements")
     _check(lib.nvfp4_moe_tokens(ctypes.byref(layer), _ptr(x), tokens, _row_stride(x), _ptr(out), _row_stride(out),
                                 _ptr(ids_out), _ptr(weights_out), _ptr(workspace),
                                 0 if workspace is None else workspace.numel(), _stream(stream)))

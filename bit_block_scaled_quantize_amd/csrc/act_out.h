@@ -35,6 +35,35 @@ __device__ __forceinline__ float put_act_of(int act, const ActOut& o, uint16_t* 
   }
 }
 
+// Four consecutive elements of a row with their bias and residual (two BF16 a word) at hand.
+template <int ACT, class V>
+__device__ __forceinline__ float put_act4(const ActOut& o, uint16_t* d, int64_t ldd, int64_t row, int64_t col,
+                                          const V& v, const float (&bias)[4], v2u32 res) {
+  float z[4], y[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    z[q] = v[q] + bias[q];
+    y[q] = act<ACT>(z[q]);
+    if (o.residual != nullptr) y[q] += (q & 1) ? bf16_hi(res[q >> 1]) : bf16_lo(res[q >> 1]);
+  }
+  if (o.preact != nullptr)
+    *reinterpret_cast<v2u32_any*>(o.preact + row * o.ldp + col) = v2u32{bf16_rn_pair(z[0], z[1]), bf16_rn_pair(z[2], z[3])};
+  const v2u32 w = {bf16_rn_pair(y[0], y[1]), bf16_rn_pair(y[2], y[3])};
+  *reinterpret_cast<v2u32_any*>(d + row * ldd + col) = w;
+  return fmaxf(fmaxf(fabsf(bf16_lo(w.x)), fabsf(bf16_hi(w.x))), fmaxf(fabsf(bf16_lo(w.y)), fabsf(bf16_hi(w.y))));
+}
+
+template <class V>
+__device__ __forceinline__ float put_act4_of(int act, const ActOut& o, uint16_t* d, int64_t ldd, int64_t row, int64_t col,
+                                             const V& v, const float (&bias)[4], v2u32 res) {
+  switch (act) {
+    case kActRelu2: return put_act4<kActRelu2>(o, d, ldd, row, col, v, bias, res);
+    case kActGelu: return put_act4<kActGelu>(o, d, ldd, row, col, v, bias, res);
+    case kActSilu: return put_act4<kActSilu>(o, d, ldd, row, col, v, bias, res);
+    default: return put_act4<kActNone>(o, d, ldd, row, col, v, bias, res);
+  }
+}
+
 // Eight consecutive elements of a row, every array moved as one 16-byte vector from wherever it starts.
 template <int ACT>
 __device__ __forceinline__ float put_act8(const ActOut& o, uint16_t* d, int64_t ldd, int64_t row, int64_t col,

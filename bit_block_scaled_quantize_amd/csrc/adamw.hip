@@ -19,7 +19,7 @@
 // Memory bound: 4 + 8 + 2 bytes (grad, p in and out, w) plus 16 (FP32 m, v in and out) or 4.125
 // (8 bits) per element against about 40 and 110 vector operations. Each thread takes 8
 // consecutive elements (one Philox call gives their 8 times 16 bits, 4 neighbouring lanes a
-// block of 32). A workgroup takes one chunk of 8192 elements of one tensor (the table holds the chunk's
+// block of 32). A workgroup takes one chunk of 2048 elements of one tensor (the table holds the chunk's
 // tensor, so finding it is one load and not a search).
 #include "device_common.h"
 #include "launch.h"

@@ -46,25 +46,48 @@ __global__ __launch_bounds__(kThreads) void k_gemm_skinny(GemmOperand A, GemmOpe
   for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[i][c] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-  Pipe<R, C, 2, K64, TokensNvfp4<C, K64>> pipe;
+  // (one step ahead is enough, and better, where four column fragments' arithmetic covers it)
+  Pipe<R, C, C == 4 ? 1 : 2, K64, TokensNvfp4<C, K64>> pipe;
   pipe.start(weights, row, tok, wave, kWaves);
   pipe.run(weights, row, tok, wave, kWaves, (int)((K + kStep<K64> - 1) / kStep<K64>), acc);
   put<R, C>(red, wave, acc);
+  // Fragment f = kPer wave + j of the R C, rows first, so that a wave's fragments are neighbours in a
+  // row of D: a lane has four consecutive columns of one row of each, moved as one vector wherever the
+  // row starts. Bias and residual are asked for ahead of the barrier.
+  constexpr int kPer = (R * C + kWaves - 1) / kWaves;
+  float bias[kPer][4];
+  v2u32 res[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int f = wave * kPer + j;
+    const int64_t m = m0 + 16 * (f / R) + r, n = n0 + 16 * (f % R) + 4 * g;
+    const bool in = f < R * C && m < M && n + 4 <= N;
+    res[j] = v2u32{0, 0};
+    if (in && out.residual != nullptr) res[j] = *reinterpret_cast<const v2u32_any*>(out.residual + m * out.ldr + n);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) bias[j][q] = in ? bias_at(out, n + q) : 0.0f;
+  }
   __syncthreads();
   const float alpha = A.global_scale[0] * B.global_scale[0];
   float mx = 0.0f;
-#pragma unroll 1
-  for (int f = wave; f < R * C; f += kWaves) {
-    const int i = f / C, c = f % C;
-    const float4v v = take<kWaves, R, C>(red, i, c);
-    const int64_t m = m0 + 16 * c + r, n = n0 + 16 * i + 4 * g;
-    if (m < M) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (n + q < N) mx = fmaxf(mx, put_act_of(act, out, D, ldd, m, n + q, v[q] * alpha));
+  for (int j = 0; j < kPer; ++j) {
+    const int f = wave * kPer + j;
+    if (f < R * C) {                                          // uniform
+      float4v v = take<kWaves, R, C>(red, f % R, f / R);
+      const int64_t m = m0 + 16 * (f / R) + r, n = n0 + 16 * (f % R) + 4 * g;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] *= alpha;
+      if (m < M && n + 4 <= N) {
+        mx = fmaxf(mx, put_act4_of(act, out, D, ldd, m, n, v, bias[j], res[j]));
+      } else if (m < M) {                                     // the last columns of an N that is not a multiple of 4
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (n + q < N) mx = fmaxf(mx, put_act_of(act, out, D, ldd, m, n + q, v[q]));
+      }
     }
   }
-  if (amax != nullptr && wave < R * C) {                      // uniform
+  if (amax != nullptr && wave * kPer < R * C) {                      // uniform
     mx = wave_fold_max(mx);
     if (lane == 0) atomic_raise_nonneg(amax, mx);
   }
@@ -82,16 +105,18 @@ void launch_rc(const GemmOperand& a, const GemmOperand& b, int64_t M, int64_t N,
 
 }  // namespace
 
-// Up to 64 rows always; beyond by the number of workgroups, each worth 64 rows x 32 columns: the tile
-// kernel takes whole rounds of 256 x 256 tiles (or quarters of them), so its time hardly depends on
-// them below a round, and this kernel's is proportional to them. Measured, us (this kernel / tiles):
-// 5120 x 5120: 384 rows (960 workgroups) 52 / 54, 512 (1280) 66 / 54; 5120 x 20480: 384 (960) 170 / 190,
-// 512 (1280) 212 / 188; 2688 x 1856: 768 (1008) 23 / 26, 1024 (1344) 32 / 27. With a K that is not a
-// multiple of 64 (runs of 32 here, copied operands there), 5120 x 5136: 256 (640) 59 / 71, 512 (1280)
-// 96 / 71; 1857 x 2704: 512 (472) 25 / 40, 1003 (944) 42 / 42.
+// Workgroups of 32 columns and 64 rows that the product makes.
+int64_t few_row_blocks(int64_t M, int64_t N) { return (M + 63) / 64 * ((N + 31) / 32); }
+
+// Up to 64 rows always; beyond by the number of workgroups: the tile kernel takes whole rounds of
+// 256 x 256 tiles (or quarters of them), so its time hardly depends on them below a round, and this
+// kernel's is proportional to them. Measured, us (this kernel / tiles): 5120 x 5120: 256 rows (640
+// workgroups) 40 / 51, 512 (1280) 56 / 54, 1024 (2560) 88 / 83; 20480 x 5120: 128 (1280) 56 / 78, 256
+// (2560) 89 / 82; 1856 x 2688: 1024 (928) 23 / 32. A K that is not a multiple of 64 (runs of 32 here,
+// copied operands there): 1857 x 2704: 1003 (944) 33 / 42; 5120 x 5136: 512 (1280) 85 / 71.
 bool gemm_act_few_rows(int64_t M, int64_t N, int64_t K) {
   if (K == 0) return false;
-  return M <= 64 || (M + 63) / 64 * ((N + 31) / 32) <= (K % 64 == 0 ? 1024 : 768);
+  return M <= 64 || few_row_blocks(M, N) <= (K % 64 == 0 ? 1280 : 960);
 }
 
 hipError_t launch_gemm_skinny(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int act, const ActOut& out,
@@ -99,7 +124,8 @@ hipError_t launch_gemm_skinny(GemmOperand a, GemmOperand b, int64_t M, int64_t N
 #define NVFP4_SK(R, C) launch_rc<R, C>(a, b, M, N, K, act, out, D, ldd, amax, stream)
   if (M <= 16) NVFP4_SK(2, 1);
   else if (M <= 32) NVFP4_SK(2, 2);
-  else NVFP4_SK(2, 4);
+  else if (few_row_blocks(M, N) <= 640) NVFP4_SK(2, 4);       // 64 columns halve the decoding of A, and the workgroups:
+  else NVFP4_SK(4, 4);                                        // 5120 x 5120, 256 rows 40 / 40 us, 512 63 / 56
 #undef NVFP4_SK
   return hipGetLastError();
 }

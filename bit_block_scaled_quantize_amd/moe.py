@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import torch
 
-from . import MoEWeights, NVFP4Error, NVFP4Tensor, moe_tokens, moe_workspace, quantize
+from . import MoEWeights, NVFP4Error, NVFP4Tensor, _moe_call, _on_stream, moe_workspace, quantize
 
 
 class MoETokens:
@@ -17,7 +17,8 @@ class MoETokens:
 
     router [experts, hidden] (bfloat16 or float32); w1 [experts*ffn, hidden] (gated: [experts*2*ffn,
     hidden], each expert's gate rows before its up rows) and w2 [experts*hidden, ffn] as NVFP4 tensors
-    with one global scale per expert. Calls share one workspace: on different streams, order them.
+    with one global scale per expert. The layer keeps the tensors it is made with. Calls share one
+    workspace: on different streams, order them.
     """
 
     def __init__(self, router: torch.Tensor, w1: NVFP4Tensor, w2: NVFP4Tensor, top_k: int, activation: str = "relu2",
@@ -26,6 +27,7 @@ class MoETokens:
         self.weights = MoEWeights(router, w1, w2, top_k, activation, gated, score, renormalize, routed_scale)
         self.max_tokens = max_tokens
         self.workspace = moe_workspace(self.weights, max_tokens)
+        self._layer = self.weights.c()                       # checked once; its tensors are self.weights'
 
     @classmethod
     def from_bf16(cls, router: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, top_k: int, **kw):
@@ -33,11 +35,12 @@ class MoETokens:
         16x16 blocks with one tensor scale per expert, as the training layers quantize them."""
         return cls(router, *(_expert_stack(w) for w in (w1, w2)), top_k, **kw)
 
+    @_on_stream
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, ids_out: torch.Tensor | None = None,
                  weights_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         if x.dim() != 2 or x.shape[0] > self.max_tokens:
             raise NVFP4Error(f"x must be [tokens, hidden] with at most {self.max_tokens} tokens")
-        return moe_tokens(x, self.weights, out, ids_out, weights_out, self.workspace, stream)
+        return _moe_call(x, self._layer, out, ids_out, weights_out, self.workspace, stream)
 
 
 def _expert_stack(w: torch.Tensor) -> NVFP4Tensor:

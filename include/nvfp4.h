@@ -545,7 +545,7 @@ size_t nvfp4_adamw_table_size(const nvfp4_adamw_tensor* tensors, int64_t count);
  *   table      host memory of at least nvfp4_adamw_table_size bytes.
  *   chunks     receives the value to pass to nvfp4_adamw.
  * Errors: NVFP4_ERR_INVALID (NULL or misaligned pointers with n > 0, n < 0, bad dtype or state,
- * table_bytes too small), NVFP4_ERR_UNSUPPORTED (more than 2^31 - 1 chunks of 8192 elements).
+ * table_bytes too small), NVFP4_ERR_UNSUPPORTED (more than 2^31 - 1 chunks of 2048 elements).
  */
 int nvfp4_adamw_table(const nvfp4_adamw_tensor* tensors, int64_t count, nvfp4_state state, void* table,
                       size_t table_bytes, int64_t* chunks);
