@@ -15,19 +15,24 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 
 // Columns from NVFP4 rows: decoded like the weights.
-template <int C, bool K64>
+template <Shape S>
 struct TokensNvfp4 {
-  typedef Run<K64> Raw;
+  typedef Loaded<S> Raw;
+  typedef Run<S> Cur;
   Matrix a;
   uint32_t rows, first;                                       // first: the lane's row of A in the first fragment
   __device__ __forceinline__ Raw load(int c, uint32_t k) const {
     const uint32_t m = 16u * (uint32_t)c + first;
-    return load_run<K64>(a, m, m < rows, k);
+    return load_run<S>(a, m, m < rows, k);
   }
-  __device__ __forceinline__ half8 octet(const Raw& x, uint32_t, int t) const { return octet_of(x, t); }
+  __device__ __forceinline__ Cur cook(int c, const Raw& x, uint32_t k) const {
+    const uint32_t m = 16u * (uint32_t)c + first;
+    return run_of(x, a, m, m < rows, k);
+  }
+  __device__ __forceinline__ half8 octet(const Cur& x, uint32_t, int t) const { return octet_of(x, t); }
 };
 
-template <int R, int C, bool K64>
+template <int R, int C, Shape S>
 __global__ __launch_bounds__(kThreads) void k_gemm_skinny(GemmOperand A, GemmOperand B, int64_t M, int64_t N,
                                                           int64_t K, int act, ActOut out, uint16_t* __restrict__ D,
                                                           int64_t ldd, float* __restrict__ amax) {
@@ -40,16 +45,16 @@ __global__ __launch_bounds__(kThreads) void k_gemm_skinny(GemmOperand A, GemmOpe
   uint32_t row[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) row[i] = (uint32_t)(n0 + 16 * i + r < N ? n0 + 16 * i + r : n0);   // rows past N: not stored
-  const TokensNvfp4<C, K64> tok{Matrix(A.codes, A.scales, M, K), (uint32_t)M, (uint32_t)(m0 + r)};
+  const TokensNvfp4<S> tok{Matrix(A.codes, A.scales, M, K), (uint32_t)M, (uint32_t)(m0 + r)};
   float4v acc[R][C];
 #pragma unroll
   for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[i][c] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
   // (one step ahead is enough, and better, where four column fragments' arithmetic covers it)
-  Pipe<R, C, C == 4 ? 1 : 2, K64, TokensNvfp4<C, K64>> pipe;
+  Pipe<R, C, C == 4 ? 1 : 2, S, TokensNvfp4<S>> pipe;
   pipe.start(weights, row, tok, wave, kWaves);
-  pipe.run(weights, row, tok, wave, kWaves, (int)((K + kStep<K64> - 1) / kStep<K64>), acc);
+  pipe.run(weights, row, tok, wave, kWaves, (int)((K + kStep<S> - 1) / kStep<S>), acc);
   put<R, C>(red, wave, acc);
   // Fragment f = kPer wave + j of the R C, rows first, so that a wave's fragments are neighbours in a
   // row of D: a lane has four consecutive columns of one row of each, moved as one vector wherever the
@@ -93,14 +98,11 @@ __global__ __launch_bounds__(kThreads) void k_gemm_skinny(GemmOperand A, GemmOpe
   }
 }
 
-template <int R, int C>
-void launch_rc(const GemmOperand& a, const GemmOperand& b, int64_t M, int64_t N, int64_t K, int act, const ActOut& out,
+template <int R, int C, Shape S>
+void launch_as(const GemmOperand& a, const GemmOperand& b, int64_t M, int64_t N, int64_t K, int act, const ActOut& out,
                uint16_t* D, int64_t ldd, float* amax, hipStream_t stream) {
   const dim3 grid((unsigned)((N + 16 * R - 1) / (16 * R)), (unsigned)((M + 16 * C - 1) / (16 * C)));
-  if (K % 64 == 0)
-    hipLaunchKernelGGL((k_gemm_skinny<R, C, true>), grid, dim3(kThreads), 0, stream, a, b, M, N, K, act, out, D, ldd, amax);
-  else
-    hipLaunchKernelGGL((k_gemm_skinny<R, C, false>), grid, dim3(kThreads), 0, stream, a, b, M, N, K, act, out, D, ldd, amax);
+  hipLaunchKernelGGL((k_gemm_skinny<R, C, S>), grid, dim3(kThreads), 0, stream, a, b, M, N, K, act, out, D, ldd, amax);
 }
 
 }  // namespace
@@ -108,20 +110,27 @@ void launch_rc(const GemmOperand& a, const GemmOperand& b, int64_t M, int64_t N,
 // Workgroups of 32 columns and 64 rows that the product makes.
 int64_t few_row_blocks(int64_t M, int64_t N) { return (M + 63) / 64 * ((N + 31) / 32); }
 
-// Up to 64 rows always; beyond by the number of workgroups: the tile kernel takes whole rounds of
-// 256 x 256 tiles (or quarters of them), so its time hardly depends on them below a round, and this
-// kernel's is proportional to them. Measured, us (this kernel / tiles): 5120 x 5120: 256 rows (640
-// workgroups) 40 / 51, 512 (1280) 56 / 54, 1024 (2560) 88 / 83; 20480 x 5120: 128 (1280) 56 / 78, 256
-// (2560) 89 / 82; 1856 x 2688: 1024 (928) 23 / 32. A K that is not a multiple of 64 (runs of 32 here,
-// copied operands there): 1857 x 2704: 1003 (944) 33 / 42; 5120 x 5136: 512 (1280) 85 / 71.
+// Up to 64 rows always; beyond by the number of workgroups, to which this kernel's time is
+// proportional. The tile kernel takes 256 x 256 tiles one to a CU: its time hardly depends on their
+// number up to a round; up to a quarter of the CUs it cuts them into column quarters, beyond it splits K, whose
+// joining costs some 25 us. Measured, us (this kernel / tiles), 64 tiles or fewer: 512 x 5120 (1280
+// workgroups): K 1088 20 / 20, 5120 52 / 54; 1500 x 1857 x 2688 (1416) 29 / 32; 1536 x 2048 (1536): K 1088 20 / 20, 5120
+// 54 / 57; 768 x 5120 (1920): K 1088 24 / 21, 5120 68 / 60. More tiles: 1024 x 5120 (2560): K 320 23 / 40, 2688
+// 42 / 60, 5120 83 / 82, 20480 281 / 229; 1536 x 5120 (3840): K 1088 42 / 54, 5120 124 / 96. For a K that is not a
+// multiple of 64 that kernel has its operands copied first: 1003 x 5136 of 5120 columns 83 / 95.
 bool gemm_act_few_rows(int64_t M, int64_t N, int64_t K) {
   if (K == 0) return false;
-  return M <= 64 || few_row_blocks(M, N) <= (K % 64 == 0 ? 1280 : 960);
+  if (M <= 64) return true;
+  const int64_t tiles = (M + 255) / 256 * ((N + 255) / 256);
+  return few_row_blocks(M, N) <= (tiles <= 64 ? 1536 : K <= 5120 ? 2560 : 1280);
 }
 
 hipError_t launch_gemm_skinny(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int act, const ActOut& out,
                               uint16_t* D, int64_t ldd, float* amax, hipStream_t stream) {
-#define NVFP4_SK(R, C) launch_rc<R, C>(a, b, M, N, K, act, out, D, ldd, amax, stream)
+#define NVFP4_SK(R, C)                                                                   \
+  (K % 64 == 0 ? launch_as<R, C, kAligned>(a, b, M, N, K, act, out, D, ldd, amax, stream) \
+   : K > 64    ? launch_as<R, C, kWord>(a, b, M, N, K, act, out, D, ldd, amax, stream)    \
+               : launch_as<R, C, kHalf>(a, b, M, N, K, act, out, D, ldd, amax, stream))
   if (M <= 16) NVFP4_SK(2, 1);
   else if (M <= 32) NVFP4_SK(2, 2);
   else if (few_row_blocks(M, N) <= 640) NVFP4_SK(2, 4);       // 64 columns halve the decoding of A, and the workgroups:

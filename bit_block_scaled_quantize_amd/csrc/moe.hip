@@ -31,7 +31,6 @@ namespace {
 
 using namespace skinny;
 
-
 constexpr int kRouteThreads = 512, kRouteWaves = 8;
 constexpr int kRouteExperts = 4;                              // per workgroup of k_route
 constexpr int kGroupTokens = 8;                               // tokens per workgroup of k_route
@@ -338,14 +337,16 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(MoeArgs a, MoeWork w) {
 
 // Columns staged in LDS as FP16: rows of `pitch` bytes and one run of zeros for the lanes
 // without a token. Nothing of them is loaded in the loop over K, whose only loads are the weights'.
-constexpr int kZeroBytes = 2 * kRun<true>;
+constexpr int kZeroBytes = 2 * kRun<kAligned>;
 constexpr int kChunk = 4096;                                  // elements of K staged at a time
 struct TokensLds {
   struct Raw {};
+  typedef Raw Cur;
   const uint8_t* at;                                          // of the lane's row
   uint32_t k0, K, mask;                                       // first element staged; 0 for the zeros
   __device__ __forceinline__ Raw load(int, uint32_t) const { return Raw{}; }
-  __device__ __forceinline__ half8 octet(const Raw&, uint32_t k, int t) const {
+  __device__ __forceinline__ Cur cook(int, const Raw& r, uint32_t) const { return r; }
+  __device__ __forceinline__ half8 octet(const Cur&, uint32_t k, int t) const {
     // past K the weights' scales are zero, and what LDS holds there is finite
     return *reinterpret_cast<const half8*>(at + ((2 * (k - k0)) & mask) + 16 * t);
   }
@@ -399,7 +400,7 @@ __device__ __forceinline__ void join_pairs(const MoeArgs& a, const MoeWork& w, i
 // others the same rows of U. DOWN: rows of W2, K = ffn -> part[pair][n], then y.
 // kCols: columns staged at a time (8, or 1 for one token). W: waves, which split K. A: steps in flight.
 // JOIN: the last workgroup of a row tile writes y.
-template <bool UP, bool GATED, int R, int W, int A, int kCols, bool JOIN, bool K64>
+template <bool UP, bool GATED, int R, int W, int A, int kCols, bool JOIN, Shape S>
 __global__ __launch_bounds__(64 * W) void k_expert(MoeArgs a, MoeWork w, int tiles, uint32_t pitch) {
   constexpr int kWaves = W, kThreads = 64 * W;
   static_assert(!GATED || R % 2 == 0, "a gated tile holds as many gate as up fragments");
@@ -441,15 +442,15 @@ __global__ __launch_bounds__(64 * W) void k_expert(MoeArgs a, MoeWork w, int til
     for (int i = 0; i < R; ++i) acc[i][0] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
     float inv = 1.0f;                                         // undoes the column's power of two
     float scale = 1.0f;                                       // DOWN: the column's, in the lanes of row c
-    Pipe<R, 1, A, K64, TokensLds> pipe;
+    Pipe<R, 1, A, S, TokensLds> pipe;
     for (int64_t k0 = 0; k0 < K; k0 += kChunk) {
       const int64_t len = K - k0 < kChunk ? K - k0 : kChunk;
-      const int first = (int)(k0 / kStep<K64>) + wave;
+      const int first = (int)(k0 / kStep<S>) + wave;
       TokensLds tok{live ? tokens + r * pitch : zeros, (uint32_t)k0, (uint32_t)K, live ? 0xFFFFFFFFu : 0u};
       // The columns' elements, 8 at a time, zeros up to a whole step; column c's pair is in lane c of
       // every wave. The first turn's loads (all of them, as a rule) are issued ahead of the weights', so
       // that waiting for them does not wait for those.
-      const int octets = (int)((len + kStep<K64> - 1) / kStep<K64>) * (kStep<K64> / 8);
+      const int octets = (int)((len + kStep<S> - 1) / kStep<S>) * (kStep<S> / 8);
       half8 v[kCols];
       float vs[kCols];                                        // DOWN: maxima of the elements' fragments
       auto fetch = [&](int o) {
@@ -518,7 +519,7 @@ __global__ __launch_bounds__(64 * W) void k_expert(MoeArgs a, MoeWork w, int til
         }
       }
       __syncthreads();
-      pipe.run(weights, row, tok, first, kWaves, (int)((k0 + len + kStep<K64> - 1) / kStep<K64>), acc);
+      pipe.run(weights, row, tok, first, kWaves, (int)((k0 + len + kStep<S> - 1) / kStep<S>), acc);
     }
     put<R, 1>(red, wave, acc);
     __syncthreads();
@@ -576,38 +577,38 @@ constexpr int kMostLds = 8 * 4 * 64 * 16 + kZeroBytes + kMostCols * (2 * kChunk 
 
 int64_t tiles_of(int64_t rows, int frags) { return (rows + 16 * frags - 1) / (16 * frags); }
 
-template <bool UP, bool GATED, int R, int W, int A, int COLS, bool JOIN, bool K64>
+template <bool UP, bool GATED, int R, int W, int A, int COLS, bool JOIN, Shape S>
 hipError_t launch_expert_as(const MoeArgs& a, const MoeWork& w, hipStream_t stream) {
   // the staged columns can take more LDS than a launch may by default
-  static const hipError_t ready = hipFuncSetAttribute((const void*)k_expert<UP, GATED, R, W, A, COLS, JOIN, K64>,
+  static const hipError_t ready = hipFuncSetAttribute((const void*)k_expert<UP, GATED, R, W, A, COLS, JOIN, S>,
                                                       hipFuncAttributeMaxDynamicSharedMemorySize, kMostLds);
   if (ready != hipSuccess) return ready;
   const int64_t K = UP ? a.hidden : a.ffn, N = UP ? a.ffn : a.hidden;
   const int64_t pairs = (int64_t)a.tokens * a.top_k;
   const int64_t most = pairs < a.experts ? pairs : a.experts;
   const int tiles = (int)tiles_of(N, GATED ? R / 2 : R);
-  const int64_t staged = K < kChunk ? (K + kStep<K64> - 1) / kStep<K64> * kStep<K64> : kChunk;
+  const int64_t staged = K < kChunk ? (K + kStep<S> - 1) / kStep<S> * kStep<S> : kChunk;
   const uint32_t pitch = (uint32_t)(2 * staged + 16);         // rows start 4 banks apart
   const size_t bytes = (size_t)W * R * 64 * 16 + kZeroBytes + (size_t)COLS * pitch;
-  hipLaunchKernelGGL((k_expert<UP, GATED, R, W, A, COLS, JOIN, K64>), dim3((unsigned)(most * tiles)), dim3(64 * W), bytes,
+  hipLaunchKernelGGL((k_expert<UP, GATED, R, W, A, COLS, JOIN, S>), dim3((unsigned)(most * tiles)), dim3(64 * W), bytes,
                      stream, a, w, tiles, pitch);
   return hipSuccess;
 }
 
-template <bool UP, bool GATED, bool K64>
+template <bool UP, bool GATED, Shape S>
 hipError_t launch_expert_k(const MoeArgs& a, const MoeWork& w, hipStream_t stream) {
   // (us on 122 experts of 2688 x 1856, 64 tokens: up R = 2 with A = 1, 2, 3: 95, 95, 93, R = 4: 98; down
   // R = 2: 108 with A = 1, 110 with 2; R = 4: 96 with A = 1, 115 with 2. 8 waves: down 129 to 140)
   constexpr int R = UP ? 2 : 4, A = UP ? 3 : 1;
-  if (a.tokens == 1) return launch_expert_as<UP, GATED, 2, 8, 2, 1, !UP, K64>(a, w, stream);
-  if (a.tokens <= kWideTokens) return launch_expert_as<UP, GATED, 2, 8, 2, kMostCols, !UP, K64>(a, w, stream);
-  return launch_expert_as<UP, GATED, R, 4, A, kMostCols, false, K64>(a, w, stream);
+  if (a.tokens == 1) return launch_expert_as<UP, GATED, 2, 8, 2, 1, !UP, S>(a, w, stream);
+  if (a.tokens <= kWideTokens) return launch_expert_as<UP, GATED, 2, 8, 2, kMostCols, !UP, S>(a, w, stream);
+  return launch_expert_as<UP, GATED, R, 4, A, kMostCols, false, S>(a, w, stream);
 }
 
 template <bool UP, bool GATED>
 hipError_t launch_expert(const MoeArgs& a, const MoeWork& w, hipStream_t stream) {
-  return (UP ? a.hidden : a.ffn) % 64 == 0 ? launch_expert_k<UP, GATED, true>(a, w, stream)
-                                           : launch_expert_k<UP, GATED, false>(a, w, stream);
+  return (UP ? a.hidden : a.ffn) % 64 == 0 ? launch_expert_k<UP, GATED, kAligned>(a, w, stream)
+                                           : launch_expert_k<UP, GATED, kHalf>(a, w, stream);
 }
 
 }  // namespace

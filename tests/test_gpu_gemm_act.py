@@ -63,7 +63,7 @@ def _check_d(d, z32, act, res, what, ez=0.0):
 # one row; few rows on both sides of 16, 32 and 64; a K that ends inside a step of 64, 128 and 256;
 # odd N (rows on any boundary); then the tile kernel: odd sizes, operands brought to a K of 128, 2752
 # and 64, 90 tiles of 256 x 256 (split along K), a last round in column quarters
-SHAPES = [(1, 272, 256), (1, 48, 16), (2, 33, 80), (7, 1857, 272), (16, 512, 1344), (17, 520, 2688), (33, 256, 2704),
+SHAPES = [(1, 272, 256), (1, 48, 16), (1, 1, 16), (3, 2, 16), (2, 1, 48), (1, 3, 80), (4, 70, 32), (2, 33, 80), (7, 1857, 272), (16, 512, 1344), (17, 520, 2688), (33, 256, 2704),
           (63, 100, 640), (64, 1000, 512), (65, 264, 512), (300, 520, 512), (130, 257, 272), (257, 33, 128),
           (1000, 700, 1344), (1100, 2001, 576), (2050, 1030, 80), (1003, 1857, 2704), (1500, 1400, 48),
           (2304, 2560, 256), (520, 16640, 128)]
