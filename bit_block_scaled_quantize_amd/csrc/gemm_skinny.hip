@@ -117,12 +117,13 @@ int64_t few_row_blocks(int64_t M, int64_t N) { return (M + 63) / 64 * ((N + 31) 
 // workgroups): K 1088 20 / 20, 5120 52 / 54; 1500 x 1857 x 2688 (1416) 29 / 32; 1536 x 2048 (1536): K 1088 20 / 20, 5120
 // 54 / 57; 768 x 5120 (1920): K 1088 24 / 21, 5120 68 / 60. More tiles: 1024 x 5120 (2560): K 320 23 / 40, 2688
 // 42 / 60, 5120 83 / 82, 20480 281 / 229; 1536 x 5120 (3840): K 1088 42 / 54, 5120 124 / 96. For a K that is not a
-// multiple of 64 that kernel has its operands copied first: 1003 x 5136 of 5120 columns 83 / 95.
+// multiple of 64 that kernel has its operands copied first: 1003 x 5120, K 5136 84 / 98, 8208 118 / 128 (6144
+// 107 / 101, 8192 127 / 116).
 bool gemm_act_few_rows(int64_t M, int64_t N, int64_t K) {
   if (K == 0) return false;
   if (M <= 64) return true;
   const int64_t tiles = (M + 255) / 256 * ((N + 255) / 256);
-  return few_row_blocks(M, N) <= (tiles <= 64 ? 1536 : K <= 5120 ? 2560 : 1280);
+  return few_row_blocks(M, N) <= (tiles <= 64 ? 1536 : K <= (K % 64 == 0 ? 5120 : 10240) ? 2560 : 1280);
 }
 
 hipError_t launch_gemm_skinny(GemmOperand a, GemmOperand b, int64_t M, int64_t N, int64_t K, int act, const ActOut& out,

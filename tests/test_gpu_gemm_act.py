@@ -169,7 +169,7 @@ def test_gemm_act_streams_and_graph():
             assert torch.equal(out, want) and torch.equal(amax, amax2)
 
 
-GRADS = [(1, 1), (1, 8), (3, 33), (8, 512), (9, 520), (123, 1857), (300, 1024), (2000, 72), (4100, 520)]
+GRADS = [(1, 1), (1, 8), (3, 33), (8, 512), (9, 520), (123, 1857), (128, 131), (129, 131), (260, 7), (300, 1024), (2000, 72), (4100, 520)]
 
 
 @pytest.mark.parametrize("mn", GRADS)
