@@ -64,21 +64,21 @@ __device__ __forceinline__ float put_act4_of(int act, const ActOut& o, uint16_t*
   }
 }
 
-// Eight consecutive elements of a row, every array moved as one 16-byte vector from wherever it starts.
+// Eight consecutive elements of a row with their bias and residual at hand, every array moved as one 16-byte
+// vector from wherever it starts. Non-temporal: the outputs go out to HBM and leave the caches to the operands.
 template <int ACT>
 __device__ __forceinline__ float put_act8(const ActOut& o, uint16_t* d, int64_t ldd, int64_t row, int64_t col,
-                                          const float (&v)[8], const float (&bias)[8]) {
+                                          const float (&v)[8], const float (&bias)[8], v4u32 res) {
   float z[8], y[8];
-  v4u32 res = {0, 0, 0, 0};
-  if (o.residual != nullptr) res = *reinterpret_cast<const v4u32_any*>(o.residual + row * o.ldr + col);
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     z[q] = v[q] + bias[q];
     y[q] = act<ACT>(z[q]);
   }
   if (o.preact != nullptr)
-    *reinterpret_cast<v4u32_any*>(o.preact + row * o.ldp + col) =
-        v4u32{bf16_rn_pair(z[0], z[1]), bf16_rn_pair(z[2], z[3]), bf16_rn_pair(z[4], z[5]), bf16_rn_pair(z[6], z[7])};
+    __builtin_nontemporal_store(
+        v4u32{bf16_rn_pair(z[0], z[1]), bf16_rn_pair(z[2], z[3]), bf16_rn_pair(z[4], z[5]), bf16_rn_pair(z[6], z[7])},
+        reinterpret_cast<v4u32_any*>(o.preact + row * o.ldp + col));
   v4u32 w;
   float mx = 0.0f;
 #pragma unroll
@@ -90,7 +90,7 @@ __device__ __forceinline__ float put_act8(const ActOut& o, uint16_t* d, int64_t 
     w[q] = bf16_rn_pair(y[2 * q], y[2 * q + 1]);
     mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[q])), fabsf(bf16_hi(w[q]))));
   }
-  *reinterpret_cast<v4u32_any*>(d + row * ldd + col) = w;
+  __builtin_nontemporal_store(w, reinterpret_cast<v4u32_any*>(d + row * ldd + col));
   return mx;
 }
 

@@ -243,9 +243,6 @@ __device__ __forceinline__ float wave_fold_sum(float v) {
     return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
   }));
 }
-__device__ __forceinline__ uint32_t wave_fold_min(uint32_t v) {
-  return wave_fold(v, 0xFFFFFFFFu, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
-}
 
 // atomic max of a non-negative float through its bit pattern (monotone for v >= 0)
 __device__ __forceinline__ void atomic_max_nonneg(float* p, float v) {

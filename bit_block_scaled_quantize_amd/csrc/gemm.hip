@@ -656,26 +656,39 @@ __device__ __forceinline__ void gemm_tile_big(Operand A, Operand B, int64_t m0, 
       for (int q = 0; q < 8; ++q) bias[q] = col0 + cl + q < n1 ? bias_at(ext.act, col0 + cl + q) : 0.0f;
 #pragma unroll
       for (int i = 0; i < kFragsM; ++i) {
+        const int64_t row0 = m0 + wm * kWaveM + 32 * i;
+        constexpr int kRowsAt = 64 / kLanes;                   // rows at a time
+        // the residual of all these rows, asked for ahead of the pass through LDS (two rows at a time behind it,
+        // and stores that stay in the caches: 8192 x 20480 x 5120 1652 us, now 1516 to 1548, without a
+        // residual 1522 to 1549, nvfp4_gemm_ex 1501 to 1511 on the same card)
+        v4u32 res[32 / kRowsAt];
+#pragma unroll
+        for (int t = 0; t < 32 / kRowsAt; ++t) {
+          const int64_t row = row0 + rl + t * kRowsAt;
+          res[t] = v4u32{0, 0, 0, 0};
+          if (ext.act.residual != nullptr && col0 + cl + 8 <= n1 && row < m1)
+            res[t] = __builtin_nontemporal_load(reinterpret_cast<const v4u32_any*>(ext.act.residual + row * ext.act.ldr + col0 + cl));
+        }
 #pragma unroll
         for (int j = 0; j < kFragsN; ++j)
 #pragma unroll
           for (int q = 0; q < 16; ++q)
             own[(8 * (q >> 2) + 4 * h + (q & 3)) * kPitch + 32 * j + r] = acc[i][j][q] * alpha;
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the wave's LDS writes before its reads
-        const int64_t row0 = m0 + wm * kWaveM + 32 * i;
         if (col0 + cl + 8 <= n1) {
-#pragma unroll 2
-          for (int rr = rl; rr < 32; rr += 64 / kLanes) {
+#pragma unroll
+          for (int t = 0; t < 32 / kRowsAt; ++t) {
+            const int rr = rl + t * kRowsAt;
             if (row0 + rr < m1) {
               float v[8];
 #pragma unroll
               for (int q = 0; q < 8; ++q) v[q] = own[rr * kPitch + cl + q];
-              mx = fmaxf(mx, put_act8<KIND - kOutAct>(ext.act, d, ext.ldd, row0 + rr, col0 + cl, v, bias));
+              mx = fmaxf(mx, put_act8<KIND - kOutAct>(ext.act, d, ext.ldd, row0 + rr, col0 + cl, v, bias, res[t]));
             }
           }
         } else {                                               // the last columns of an N that is not a multiple of 8
 #pragma unroll 1
-          for (int rr = rl; rr < 32; rr += 64 / kLanes)
+          for (int rr = rl; rr < 32; rr += kRowsAt)
 #pragma unroll 1
             for (int q = 0; q < 8; ++q)
               if (row0 + rr < m1 && col0 + cl + q < n1)

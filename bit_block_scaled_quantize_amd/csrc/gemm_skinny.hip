@@ -2,6 +2,9 @@
 // residual with B's rows as the matrix instruction's rows and A's rows as its columns (skinny.h).
 // Bound by reading B, N K * 9/16 bytes, up to 64 rows; beyond, workgroups on the same rows of B take 64
 // rows of A each and find B in the cache.
+// Measured: 1 x 20480 x 5120 18.3 us (59 MB, 3.2 TB/s), 1 x 5120 x 5120 7.9; 64 x 5120 x 5120 15.7, where decoding
+// is what it does; 1003 x 1857 x 2704 with residual, bias and Z 28 (0.36 PFLOP/s): the decoding again, every
+// workgroup's own.
 #include "act_out.h"
 #include "launch.h"
 #include "skinny.h"

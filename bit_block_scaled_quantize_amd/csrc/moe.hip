@@ -5,14 +5,19 @@
 //   y = sum_j w_j W2_j h_j,  h_j = act(W1_j x), or act(G_j x) * (U_j x) with W1_j = [G_j; U_j]
 //
 // Bound by reading each chosen expert's weights once (9/16 byte per element): 1 token with 6 of
-// 128 experts of 2688 x 1856 reads 34 MB, 64 tokens read most of the 718 MB. Three launches, each
-// the next one's dependence on all of the one before:
+// 128 experts of 2688 x 1856 reads 34 MB, 64 tokens read most of the 718 MB. Three launches, or four, each
+// depending on all of the one before:
 //  1. k_route: logits (a wave per expert, 8 tokens at a time), x in FP16; the last workgroup of a
 //     token group to finish picks its tokens' experts, the last group to finish sorts the
 //     (token, expert) pairs by expert.
-//  2. k_expert<UP>: 32 rows of one used expert times its tokens (skinny.h), the activation, h.
-//  3. k_expert<DOWN>: the same over W2, the routing weight, one partial result per pair; the last
-//     workgroup of a row tile to finish adds the k partials of each token in order.
+//  2. k_expert<UP>: 32 rows (gated: 16 of each half) of one used expert times its tokens (skinny.h), the
+//     activation, h.
+//  3. k_expert<DOWN>: 32 or 64 rows of W2 likewise, the routing weight, one partial result per pair.
+//  4. y, the k partials of each token added in order: up to 4 tokens by the last workgroup of a row tile
+//     to finish, beyond by k_join (there is so much to add that those workgroups would be the launch's tail).
+// Measured (that layer, us): 1 token 7.9 + 8.9 + 9.4 (the weights at 1.9 TB/s in the products: 17 MB each is
+// 4 us of reading behind a launch's 3 us and the round trips to the routing, x and the weights); 64 tokens 17 +
+// 95 + 96 + 5 (3.6 TB/s). Routing one token is latency: the logits, the counter, the picks one after the other.
 // "The last to finish" is found with a counter that the last one resets: nothing waits for
 // anything, and no sum depends on an order of arrival.
 //
@@ -20,8 +25,9 @@
 // pair) that brings their largest magnitude into [2^14, 2^15). A BF16 x is then exact down to
 // 2^-28 of that maximum, and what is lost below is under 2^-40 of it; an FP32 h keeps 11 bits,
 // three more than the BF16 result. A pair's maximum is known only when all of its h is, so h is
-// stored with a scale for each 16 rows (its maximum beside it) and brought to the pair's in k_expert<DOWN>. Non-finite tokens take scale 1 and come out non-finite; other
-// tokens' columns do not see them.
+// stored with a scale for each 16 rows (its maximum beside it) and brought to the pair's in
+// k_expert<DOWN>. Non-finite tokens take scale 1 and come out non-finite; other tokens' columns do not
+// see them.
 #include "activation.h"
 #include "launch.h"
 #include "skinny.h"
