@@ -125,10 +125,12 @@ def test_act_grad_validation(lib):
     assert call(dy=FAKE + 2, dt=1) == INVALID
     assert call(dz=FAKE + 1) == INVALID
     assert call(dbias=FAKE + 2) == INVALID
-    assert call(ws=None, ws_n=0) == WORKSPACE
-    assert call(ws=FAKE + 64) == WORKSPACE
-    assert lib.nvfp4_workspace_size(nv.OP_ACT_GRAD, 8, 32, 1) == 0          # one run of rows: no partial sums
-    assert lib.nvfp4_workspace_size(nv.OP_ACT_GRAD, 100, 32, 1) > 0
+    assert lib.nvfp4_workspace_size(nv.OP_ACT_GRAD, 128, 32, 1) == 0        # one run of rows: no partial sums
+    need = lib.nvfp4_workspace_size(nv.OP_ACT_GRAD, 129, 32, 1)
+    assert need > 0
+    assert call(M=129, ws=None, ws_n=0) == WORKSPACE
+    assert call(M=129, ws_n=need - 1) == WORKSPACE
+    assert call(M=129, ws=FAKE + 64) == WORKSPACE
 
 
 def _moe(**kw):
