@@ -75,12 +75,14 @@ class _LinearFn(torch.autograd.Function):
 
 
 def _gradient_gemms(ctx, t, g):
-    """dX and dW (None when it went into main_grad) of one call from its input t and the gradient g
-    of its product."""
+    """dX and dW (None when it went into main_grad, or the weight is frozen) of one call from its input
+    t and the gradient g of its product."""
     layer = ctx.layer
     pair = amax_pair(g, layer.sign_mask)                     # max|dY|, max|H dY| from one read
     qdy, _ = quantize(g, "1x16", "sr", seed=layer.seed, offset=2 * ctx.call, amax=pair[0:1])
     dx = gemm_ex(qdy, ctx.qwt, out_dtype=torch.bfloat16)
+    if not ctx.needs_input_grad[1]:
+        return dx, None
     hx_amax = ctx.hx_amax
     if hx_amax is None:
         hx_amax = amax(t, rht=True, sign_mask=layer.sign_mask)
@@ -145,7 +147,7 @@ class _LinearActFn(torch.autograd.Function):
             g = g.float()
         g = g.contiguous()
         db = None
-        if layer.bias is not None:
+        if ctx.needs_input_grad[2]:
             db = layer.bias_main_grad
             if db is None:
                 db = torch.empty((g.shape[1],), dtype=torch.float32, device=g.device)
@@ -155,9 +157,9 @@ class _LinearActFn(torch.autograd.Function):
                            accumulate=layer.bias_main_grad is not None, bias_only=z is None)
             dz = g if z is None else out
         dx, dw = _gradient_gemms(ctx, t, dz)
-        if layer.bias is None or layer.bias_main_grad is not None:
+        if layer.bias_main_grad is not None:
             db = None
-        else:
+        elif db is not None:
             db = db.to(layer.bias.dtype)
         dr = dy if ctx.needs_input_grad[3] else None
         return dx.view(ctx.x_shape), dw, db, dr, None, None, None
@@ -171,7 +173,7 @@ class NVFP4Linear(torch.nn.Module):
     main_grad: with ``fp32_main_grad`` (default) the weight gradient is accumulated into the
     FP32 tensor ``self.main_grad`` (zero it between optimizer steps) and ``weight.grad`` stays
     None; otherwise ``weight.grad`` receives it in BF16. ``bias_main_grad`` and ``bias.grad``
-    (FP32) likewise.
+    (FP32) likewise. A weight or bias with requires_grad False gets no gradient.
     last_output_amax: max|y| of the latest forward (a device float [1]), the ``x_amax`` of a
     following NVFP4Linear.
     weight_amax: None, or a device float [1] holding max|W| (optim.AdamW keeps it up to date), which

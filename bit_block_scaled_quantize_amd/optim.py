@@ -56,18 +56,18 @@ class AdamW:
 
     @classmethod
     def of(cls, module: torch.nn.Module, weight_decay: float = 0.1, **kw):
-        """Of every parameter of a module: NVFP4Linear weights with their main_grad and decay, their
-        biases and every other parameter of one dimension without decay. A parameter without a main
-        gradient gets a .grad that has to stay in place (zero_grad of this class, not
-        set_to_none)."""
+        """Of every parameter of a module that requires a gradient now: NVFP4Linear weights with their
+        main_grad and decay, their biases and every other parameter of one dimension without decay. A
+        parameter without a main gradient gets a .grad that has to stay in place (zero_grad of this
+        class, not set_to_none)."""
         entries, layers, seen = [], [], set()
         for m in module.modules():
             if isinstance(m, NVFP4Linear):
-                if m.main_grad is not None and id(m.weight) not in seen:
+                if m.main_grad is not None and m.weight.requires_grad and id(m.weight) not in seen:
                     layers.append((len(entries), m))
                     entries.append((m.weight, m.main_grad, weight_decay))
                     seen.add(id(m.weight))
-                if m.bias is not None and m.bias_main_grad is not None and id(m.bias) not in seen:
+                if m.bias_main_grad is not None and m.bias.requires_grad and id(m.bias) not in seen:
                     entries.append((m.bias, m.bias_main_grad, 0.0))
                     seen.add(id(m.bias))
         for p in module.parameters():

@@ -1,0 +1,131 @@
+"""What NVFP4Linear and optim.AdamW do with their buffers, on the CPU: the library calls are stood in for
+by plain products (no quantization) and the optimizer's step by the 64-bit oracle, so that only the
+wrappers' own decisions are tested: which gradients are computed, where they go, what is stepped."""
+import numpy as np
+import pytest
+import torch
+
+import bit_block_scaled_quantize_amd as nv
+import oracle
+from bit_block_scaled_quantize_amd import linear, optim
+from bit_block_scaled_quantize_amd.linear import NVFP4Linear
+from bit_block_scaled_quantize_amd.optim import AdamW
+
+
+class Plan:
+    """AdamWPlan without a device table."""
+
+    def __init__(self, tensors):
+        self.tensors, self.device = list(tensors), torch.device("cpu")
+
+
+def _adamw(plan, lr, betas, eps, step, max_norm=None, seed=0, amax_out=None, **_):
+    norm = np.sqrt(sum(float(t.grad.double().square().sum()) for t in plan.tensors))
+    clip = 1.0 if max_norm is None else min(1.0, max_norm / (norm + 1e-6))
+    for i, t in enumerate(plan.tensors):
+        out = oracle.adamw64(t.p.reshape(-1).numpy(), t.grad.reshape(-1).float().numpy(), t.m.numpy(), t.v.numpy(), lr,
+                             *betas, eps, step, t.weight_decay, clip)
+        for dst, src in zip((t.p, t.m, t.v), out):
+            dst.numpy().reshape(-1)[:] = src                 # as the kernel writes: no version counter moves
+        w = t.p if t.w_out is None else t.w_out
+        if t.w_out is not None:
+            t.w_out.view(torch.int16).numpy().reshape(-1)[:] = t.p.bfloat16().view(torch.int16).numpy().reshape(-1)
+        if amax_out is not None:
+            amax_out[i] = w.abs().max().float()
+    return None if max_norm is None else torch.tensor([norm])
+
+
+@pytest.fixture(autouse=True)
+def library(monkeypatch):
+    """The calls made, by name, in order."""
+    calls = []
+
+    def quantize(x, block="1x16", rnd="rn", amax=None, emit_transposed=False, **kw):
+        calls.append(("quantize", amax))
+        return x.detach().float().clone(), x.detach().t().float().clone() if emit_transposed else None
+
+    def gemm_ex(a, b, out=None, accumulate=False, out_dtype=torch.float32, amax_out=None):
+        d = a @ b.t()
+        if accumulate:
+            return out.add_(d)
+        if amax_out is not None:
+            amax_out.copy_(d.abs().max())
+        return d.to(out_dtype)
+
+    def gemm_act(a, b, bias=None, activation="none", residual=None, preact=None, amax_out=None):
+        z = a @ b.t() + (0 if bias is None else bias)
+        if preact is not None:
+            preact.copy_(z)
+        d = {"none": z, "relu2": z.clamp_min(0).square()}[activation] + (0 if residual is None else residual)
+        amax_out.copy_(d.abs().max())
+        return d.bfloat16()
+
+    def act_grad(dy, preact=None, activation="none", dbias=None, accumulate=False, bias_only=False):
+        g = dy.float() * (2 * preact.float().clamp_min(0) if activation == "relu2" else 1)
+        if dbias is not None:
+            dbias.copy_(g.sum(0) + (dbias if accumulate else 0))
+        return None if bias_only else g.bfloat16()
+
+    def rht_quantize(x, *_, **__):
+        calls.append(("rht_quantize", None))
+        return x.detach().t().float()
+
+    for name, fn in dict(quantize=quantize, gemm_ex=gemm_ex, gemm_act=gemm_act, act_grad=act_grad, rht_quantize=rht_quantize,
+                         amax=lambda x, **_: x.abs().max().float().reshape(1),
+                         amax_pair=lambda x, _: x.abs().max().float().expand(2).clone()).items():
+        monkeypatch.setattr(linear, name, fn)
+    monkeypatch.setattr(optim, "AdamWPlan", Plan)
+    monkeypatch.setattr(optim, "adamw", _adamw)
+    return calls
+
+
+def _layer(d_in, d_out, seed, **kw):
+    torch.manual_seed(seed)
+    layer = NVFP4Linear(d_in, d_out, **kw)
+    with torch.no_grad():
+        layer.weight.copy_(torch.randn(d_out, d_in) * 0.2)
+        if layer.bias is not None:
+            layer.bias.copy_(torch.randn(d_out))
+    return layer
+
+
+def _x(rows, cols, seed=0):
+    torch.manual_seed(100 + seed)
+    return torch.randn(rows, cols).bfloat16()
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(bias=True, activation="relu2")], ids=["plain", "act"])
+def test_a_frozen_layer_is_left_alone(kw):
+    """requires_grad_(False) between trainable layers: no gradient is added to the layer's buffers, the
+    optimizer does not step or decay it, and its gradient is no part of the norm."""
+    net = torch.nn.Sequential(_layer(32, 48, 1, **kw), _layer(48, 64, 2, **kw), _layer(64, 32, 3, **kw))
+    net[1].requires_grad_(False)
+    net[1].main_grad.fill_(0.5)                                       # of an earlier step: not to be read either
+    keep = [t.clone() for t in net[1].parameters()]
+    opt = AdamW.of(net, lr=1e-2, weight_decay=0.1, max_norm=1.0)
+    addresses = {p.data_ptr() for p in opt.params}
+    assert not addresses & {p.data_ptr() for p in net[1].parameters()}
+    assert addresses == {p.data_ptr() for p in net.parameters() if p.requires_grad}
+    for _ in range(2):
+        net(_x(32, 32)).float().square().mean().backward()
+        norm = opt.step()
+        assert norm.item() == pytest.approx(np.sqrt(sum(float(g.double().square().sum()) for g in opt.grads)))
+        assert all(torch.count_nonzero(g) for g in opt.grads)
+        opt.zero_grad()
+    assert torch.all(net[1].main_grad == 0.5)
+    if net[1].bias is not None:
+        assert torch.count_nonzero(net[1].bias_main_grad).item() == 0
+    assert all(torch.equal(a, b) for a, b in zip(net[1].parameters(), keep))
+
+
+@pytest.mark.parametrize("frozen", ["weight", "bias"])
+def test_one_of_weight_and_bias_frozen(frozen):
+    layer = _layer(32, 48, 4, bias=True, activation="relu2")
+    getattr(layer, frozen).requires_grad_(False)
+    x = _x(16, 32, 4).requires_grad_(True)
+    layer(x).float().sum().backward()
+    assert torch.count_nonzero(x.grad) > 0
+    got = {"weight": layer.main_grad, "bias": layer.bias_main_grad}
+    for name, g in got.items():
+        assert (torch.count_nonzero(g).item() == 0) == (name == frozen)
+    assert len(AdamW.of(layer).params) == 1
