@@ -46,6 +46,7 @@ class AdamW:
         self.plan = AdamWPlan(tensors)
         self.amax = torch.zeros((len(tensors),), dtype=torch.float32, device=self.plan.device)
         self._layers = list(layers)                          # (index of the weight, layer)
+        self._mains = []                                     # (parameter, its main gradient)
 
     def _state(self, p):
         n, dev = p.numel(), p.device
@@ -59,28 +60,42 @@ class AdamW:
         """Of every parameter of a module that requires a gradient now: NVFP4Linear weights with their
         main_grad and decay, their biases and every other parameter of one dimension without decay. A
         parameter without a main gradient gets a .grad that has to stay in place (zero_grad of this
-        class, not set_to_none)."""
-        entries, layers, seen = [], [], set()
+        class, not set_to_none). A parameter that several layers share is stepped once, with all of
+        their gradients: the layers share one main gradient from here on, and what other uses of the
+        parameter leave in its .grad is added there by step()."""
+        entries, layers, at = [], [], {}
         for m in module.modules():
-            if isinstance(m, NVFP4Linear):
-                if m.main_grad is not None and m.weight.requires_grad and id(m.weight) not in seen:
-                    layers.append((len(entries), m))
-                    entries.append((m.weight, m.main_grad, weight_decay))
-                    seen.add(id(m.weight))
-                if m.bias_main_grad is not None and m.bias.requires_grad and id(m.bias) not in seen:
-                    entries.append((m.bias, m.bias_main_grad, 0.0))
-                    seen.add(id(m.bias))
+            if not isinstance(m, NVFP4Linear):
+                continue
+            for name, main, decay in (("weight", "main_grad", weight_decay), ("bias", "bias_main_grad", 0.0)):
+                p, grad = getattr(m, name), getattr(m, main)
+                if grad is None or not p.requires_grad:
+                    continue
+                if id(p) not in at:
+                    at[id(p)] = len(entries)
+                    entries.append((p, grad, decay))
+                elif grad is not entries[at[id(p)]][1]:
+                    entries[at[id(p)]][1].add_(grad)
+                    setattr(m, main, entries[at[id(p)]][1])
+                if name == "weight":
+                    layers.append((at[id(p)], m))
+        mains = [(p, grad) for p, grad, _ in entries]
         for p in module.parameters():
-            if id(p) in seen or not p.requires_grad:
+            if id(p) in at or not p.requires_grad:
                 continue
             if p.grad is None:
                 p.grad = torch.zeros_like(p)
             entries.append((p, p.grad, weight_decay if p.dim() > 1 else 0.0))
-            seen.add(id(p))
-        return cls(entries, weight_decay=weight_decay, layers=layers, **kw)
+        opt = cls(entries, weight_decay=weight_decay, layers=layers, **kw)
+        opt._mains = mains
+        return opt
 
     def step(self, lr: float | None = None):
         """One step; returns the gradients' norm with max_norm, else None."""
+        for p, main in self._mains:
+            if p.grad is not None:                           # of a use without the main gradient
+                main.add_(p.grad)
+                p.grad = None
         self.steps += 1
         norm = adamw(self.plan, lr=self.lr if lr is None else lr, betas=self.betas, eps=self.eps, step=self.steps,
                      max_norm=self.max_norm, seed=self.seed, amax_out=self.amax)
@@ -90,6 +105,8 @@ class AdamW:
 
     def zero_grad(self):
         torch._foreach_zero_(self.grads)
+        for p, _ in self._mains:
+            p.grad = None
 
     def state_dict(self) -> dict:
         keys = ("m", "v") if self.states == "fp32" else ("m", "v", "m_scale", "v_scale")

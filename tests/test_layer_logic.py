@@ -129,3 +129,64 @@ def test_one_of_weight_and_bias_frozen(frozen):
     for name, g in got.items():
         assert (torch.count_nonzero(g).item() == 0) == (name == frozen)
     assert len(AdamW.of(layer).params) == 1
+
+
+class Tied(torch.nn.Module):
+    """Two layers with one weight, and (table) the weight as an ordinary parameter too."""
+
+    def __init__(self, second_main_grad=True, table=False, bias=False):
+        super().__init__()
+        self.a = _layer(32, 32, 5, bias=bias)
+        self.b = _layer(32, 32, 6, bias=bias, fp32_main_grad=second_main_grad)
+        self.b.weight = self.a.weight
+        if bias:
+            self.b.bias = self.a.bias
+        self.table = table
+
+    def forward(self, x):
+        y = self.b(self.a(x))
+        return y + x @ self.a.weight.t() if self.table else y
+
+
+def _weight_gradient(net, x):
+    """The gradient of the tied weight and bias summed over all of their uses, in FP32."""
+    w = net.a.weight.detach().float().requires_grad_(True)
+    b = (torch.zeros(32) if net.a.bias is None else net.a.bias.detach().clone()).requires_grad_(True)
+    h = (x.float() @ w.t() + b).bfloat16().float()
+    y = (h @ w.t() + b).bfloat16().float()
+    y = y + (x.float() @ w.t() if net.table else 0)
+    y.sum().backward()
+    return w.grad, b.grad
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(bias=True), dict(second_main_grad=False), dict(table=True),
+                                dict(second_main_grad=False, table=True)],
+                         ids=lambda k: "-".join(k) or "plain")
+@pytest.mark.parametrize("backward_before", [False, True], ids=["", "gradients-before"])
+def test_tied_weights_get_every_gradient(kw, backward_before):
+    """Each use of a shared weight adds to the gradient that is stepped, whichever buffer it goes to,
+    also where a backward pass came before the optimizer; nothing of it is left for the next step.
+    BF16 gradients: 2^-8 of the sum of magnitudes over 16 rows, three uses."""
+    net = Tied(**kw)
+    x = _x(16, 32, 7)
+    want, want_bias = _weight_gradient(net, x)
+    if backward_before:
+        net(x).float().sum().backward()
+    opt = AdamW.of(net, lr=1e-2, max_norm=1e9, weight_decay=0.0)
+    assert len(opt.params) == (1 if net.a.bias is None else 2)
+    for step in range(2):
+        if step or not backward_before:
+            net(x).float().sum().backward()
+        want, want_bias = _weight_gradient(net, x)
+        norm = opt.step()
+        tol = 2.0 ** -7 * float(want.abs().max())
+        assert torch.allclose(opt.grads[0], want, rtol=0, atol=3 * tol)
+        if net.a.bias is not None:
+            assert torch.allclose(opt.grads[1], want_bias, rtol=0, atol=2.0 ** -7 * float(want_bias.abs().max()))
+        assert norm.item() == pytest.approx(np.sqrt(sum(float(g.double().square().sum()) for g in opt.grads)))
+        assert net.a.weight_amax.item() == net.a.weight.abs().max().item()
+        assert net.b.weight_amax is None or net.b.weight_amax.item() == net.a.weight_amax.item()
+        opt.zero_grad()
+        for layer in (net.a, net.b):
+            assert all(g is None or torch.count_nonzero(g).item() == 0
+                       for g in (layer.main_grad, layer.bias_main_grad, layer.weight.grad))
