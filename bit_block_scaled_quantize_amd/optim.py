@@ -30,6 +30,7 @@ class AdamW:
         self.lr, self.betas, self.eps, self.max_norm, self.seed = lr, betas, eps, max_norm, seed
         self.states, self.steps = states, 0
         self.params, self.grads, self.masters, tensors = [], [], [], []
+        self._held = []                                      # (owner, attribute, the tensor it has to stay)
         for entry in entries:
             param, grad, *decay = entry
             p = param.detach()
@@ -42,6 +43,9 @@ class AdamW:
                                        w_out=p if p.dtype == torch.bfloat16 else None, **self._state(p)))
             self.params.append(p)
             self.grads.append(grad)
+            self._held.append((param, "data", p))
+            if param.is_leaf and param.grad is grad:
+                self._held.append((param, "grad", grad))
             self.masters.append(master)
         self.plan = AdamWPlan(tensors)
         self.amax = torch.zeros((len(tensors),), dtype=torch.float32, device=self.plan.device)
@@ -63,7 +67,7 @@ class AdamW:
         class, not set_to_none). A parameter that several layers share is stepped once, with all of
         their gradients: the layers share one main gradient from here on, and what other uses of the
         parameter leave in its .grad is added there by step()."""
-        entries, layers, at = [], [], {}
+        entries, layers, held, at = [], [], [], {}
         for m in module.modules():
             if not isinstance(m, NVFP4Linear):
                 continue
@@ -77,6 +81,7 @@ class AdamW:
                 elif grad is not entries[at[id(p)]][1]:
                     entries[at[id(p)]][1].add_(grad)
                     setattr(m, main, entries[at[id(p)]][1])
+                held.append((m, main, entries[at[id(p)]][1]))
                 if name == "weight":
                     layers.append((at[id(p)], m))
         mains = [(p, grad) for p, grad, _ in entries]
@@ -88,10 +93,17 @@ class AdamW:
             entries.append((p, p.grad, weight_decay if p.dim() > 1 else 0.0))
         opt = cls(entries, weight_decay=weight_decay, layers=layers, **kw)
         opt._mains = mains
+        opt._held += held
         return opt
 
     def step(self, lr: float | None = None):
-        """One step; returns the gradients' norm with max_norm, else None."""
+        """One step; returns the gradients' norm with max_norm, else None. The kernel reads and writes
+        the buffers that the optimizer was made with: one that has been replaced since is an error."""
+        for owner, name, buffer in self._held:
+            now = getattr(owner, name)
+            if now is None or now.data_ptr() != buffer.data_ptr():
+                raise NVFP4Error(f"the {name} of {type(owner).__name__} {tuple(buffer.shape)} has moved since the optimizer "
+                                 f"was made: clear gradients with its zero_grad, make it anew after moving parameters")
         for p, main in self._mains:
             if p.grad is not None:                           # of a use without the main gradient
                 main.add_(p.grad)

@@ -190,3 +190,71 @@ def test_tied_weights_get_every_gradient(kw, backward_before):
         for layer in (net.a, net.b):
             assert all(g is None or torch.count_nonzero(g).item() == 0
                        for g in (layer.main_grad, layer.bias_main_grad, layer.weight.grad))
+
+
+class Scaled(torch.nn.Module):
+    def __init__(self):
+        super().__init__()
+        self.norm = torch.nn.Parameter(torch.ones(32))
+        self.lin = _layer(32, 32, 8, bias=True)
+
+    def forward(self, x):
+        return self.lin((x.float() * self.norm).bfloat16())
+
+
+def _moved_grad(net):
+    net.norm.grad = net.norm.grad.clone()
+
+
+def _no_grad(net):
+    net.zero_grad()                                                   # set_to_none is torch's default
+
+
+def _moved_main(net):
+    net.lin.main_grad = torch.zeros_like(net.lin.main_grad)
+
+
+def _moved_bias_main(net):
+    net.lin.bias_main_grad = torch.zeros_like(net.lin.bias_main_grad)
+
+
+def _moved_weight(net):
+    net.lin.weight.data = net.lin.weight.data.clone()
+
+
+def _moved_parameter(net):
+    net.norm.data = net.norm.data.clone()
+
+
+@pytest.mark.parametrize("move", [_moved_grad, _no_grad, _moved_main, _moved_bias_main, _moved_weight, _moved_parameter])
+def test_a_step_from_buffers_that_moved_is_refused(move):
+    """The plan holds addresses: a step from the old gradient, or of the old weight, is an error and
+    changes nothing."""
+    net = Scaled()
+    opt = AdamW.of(net, lr=1e-2)
+    net(_x(16, 32, 8)).float().sum().backward()
+    opt.step()
+    opt.zero_grad()
+    move(net)
+    net(_x(16, 32, 9)).float().sum().backward()
+    keep = [t.clone() for t in opt.masters]
+    with pytest.raises(nv.NVFP4Error, match="moved"):
+        opt.step()
+    assert opt.steps == 1 and all(torch.equal(a, b) for a, b in zip(keep, opt.masters))
+
+
+def test_gradients_given_one_by_one_are_the_callers():
+    """Entries name any gradient; one that is the parameter's .grad has to stay it."""
+    p, g = torch.nn.Parameter(torch.ones(8)), torch.full((8,), 0.5)
+    opt = AdamW([(p, g)], lr=1e-2)
+    opt.step()
+    assert p.grad is None and torch.all(p.detach() < 1)
+    p.grad = torch.zeros(8)
+    opt.step()
+    q = torch.nn.Parameter(torch.ones(8))
+    q.grad = torch.ones(8)
+    opt = AdamW([(q, q.grad)], lr=1e-2)
+    opt.step()
+    q.grad = None
+    with pytest.raises(nv.NVFP4Error, match="moved"):
+        opt.step()
