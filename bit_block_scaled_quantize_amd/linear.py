@@ -35,6 +35,11 @@ import torch
 from . import ACTIVATIONS, NVFP4Error, act_grad, amax, amax_pair, gemm_act, gemm_ex, quantize, rht_quantize
 
 
+def _state_of(weight):
+    """Differs after torch has changed or replaced the weight's values."""
+    return weight.data_ptr(), 0 if weight.is_inference() else weight._version
+
+
 class _LinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, layer, x_amax):
@@ -176,8 +181,11 @@ class NVFP4Linear(torch.nn.Module):
     (FP32) likewise. A weight or bias with requires_grad False gets no gradient.
     last_output_amax: max|y| of the latest forward (a device float [1]), the ``x_amax`` of a
     following NVFP4Linear.
-    weight_amax: None, or a device float [1] holding max|W| (optim.AdamW keeps it up to date), which
-    makes the weight's quantization a single pass; whoever changes the weight otherwise sets it to None.
+    weight_amax: None, or a device float [1] holding max|W| (optim.AdamW sets it at every step), which
+    makes the weight's quantization a single pass. It holds for the weight as it is when this is set:
+    once torch has changed or replaced the weight (load_state_dict, an in-place operation) it reads
+    None. torch counts no writes through ``weight.data`` and none by other libraries: after those set
+    it to None.
     """
 
     def __init__(self, in_features: int, out_features: int, device=None, sign_mask: int = 0x6E04,
@@ -202,6 +210,15 @@ class NVFP4Linear(torch.nn.Module):
         self.last_output_amax = None
         self.weight_amax = None
         self.frozen = None
+
+    @property
+    def weight_amax(self):
+        value, of = self._weight_amax
+        return value if of == _state_of(self.weight) else None
+
+    @weight_amax.setter
+    def weight_amax(self, value):
+        self._weight_amax = value, _state_of(self.weight)
 
     def forward(self, x: torch.Tensor, x_amax: torch.Tensor | None = None,
                 residual: torch.Tensor | None = None) -> torch.Tensor:

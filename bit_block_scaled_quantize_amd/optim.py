@@ -111,6 +111,8 @@ class AdamW:
         self.steps += 1
         norm = adamw(self.plan, lr=self.lr if lr is None else lr, betas=self.betas, eps=self.eps, step=self.steps,
                      max_norm=self.max_norm, seed=self.seed, amax_out=self.amax)
+        # the kernel wrote them: autograd and the layers are to see it
+        torch.autograd.graph.increment_version([p for p in self.params if not p.is_inference()])
         for i, layer in self._layers:
             layer.weight_amax = self.amax[i:i + 1]
         return norm

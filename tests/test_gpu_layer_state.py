@@ -1,0 +1,59 @@
+"""What NVFP4Linear, optim.AdamW and moe.MoETokens keep between calls, on the GPU: a layer gives the
+result of the weights it has at the call, however they came there."""
+import numpy as np
+import pytest
+import torch
+
+import bit_block_scaled_quantize_amd as nv
+import workloads
+from bit_block_scaled_quantize_amd.linear import NVFP4Linear
+from bit_block_scaled_quantize_amd.optim import AdamW
+from helpers import log, to_device_bf16
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def _layer(d_in, d_out, seed, **kw):
+    layer = NVFP4Linear(d_in, d_out, device="cuda", sign_mask=workloads.wgrad_sign_mask(), seed=seed, **kw)
+    with torch.no_grad():
+        layer.weight.copy_(_bf16((d_out, d_in), seed, 0.05))
+        if layer.bias is not None:
+            layer.bias.copy_(torch.randn(d_out, device="cuda"))
+    return layer
+
+
+def _bf16(shape, seed, std=1.0):
+    return to_device_bf16(workloads.normal_bf16(shape, seed, std=std))
+
+
+def _fresh(layer, x):
+    """The layer's result by the library's calls, nothing kept."""
+    qx, _ = nv.quantize(x)
+    qw, _ = nv.quantize(layer.weight.detach(), "16x16")
+    if layer.bias is None and layer.activation == "none":
+        return nv.gemm_ex(qx, qw, out_dtype=torch.bfloat16)
+    return nv.gemm_act(qx, qw, bias=None if layer.bias is None else layer.bias.detach(), activation=layer.activation)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(bias=True, activation="gelu")], ids=["plain", "act"])
+def test_weights_loaded_after_a_step(kw):
+    log(f"layer state {kw}")
+    layer = _layer(128, 96, 21, **kw)
+    opt = AdamW.of(layer, lr=1e-2)
+    x = _bf16((32, 128), 22)
+    layer(x).float().sum().backward()
+    opt.step()
+    assert torch.equal(layer(x).detach(), _fresh(layer, x))
+    layer.load_state_dict({k: v * 16 for k, v in layer.state_dict().items()})     # far above the step's maximum
+    assert torch.equal(layer(x).detach(), _fresh(layer, x))
+    opt.zero_grad()
+    layer(x).float().sum().backward()
+    opt.step()
+    assert layer.weight_amax.item() == layer.weight.abs().max().item()
+    assert torch.equal(layer(x).detach(), _fresh(layer, x))

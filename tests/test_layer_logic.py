@@ -258,3 +258,68 @@ def test_gradients_given_one_by_one_are_the_callers():
     q.grad = None
     with pytest.raises(nv.NVFP4Error, match="moved"):
         opt.step()
+
+
+def _copy(layer):
+    with torch.no_grad():
+        layer.weight.copy_(layer.weight * 8)
+
+
+def _load(layer):
+    layer.load_state_dict({k: v * 8 for k, v in layer.state_dict().items()})
+
+
+def _replace(layer):
+    layer.weight.data = layer.weight.data * 8
+
+
+def _reset(layer):
+    torch.nn.init.normal_(layer.weight, std=3.0)
+
+
+CHANGES = [_copy, _load, _replace, _reset]
+
+
+@pytest.mark.parametrize("change", CHANGES)
+@pytest.mark.parametrize("kw", [dict(), dict(bias=True)], ids=["plain", "act"])
+def test_a_changed_weight_is_not_scaled_by_its_old_maximum(library, change, kw):
+    layer = _layer(32, 32, 11, **kw)
+    opt = AdamW.of(layer, lr=1e-2)
+    x = _x(16, 32, 11)
+    layer(x).float().sum().backward()
+    opt.step()
+    after = layer.weight_amax
+    assert after.item() == layer.weight.abs().max().item()
+    del library[:]
+    layer(x)
+    assert [a for n, a in library if n == "quantize"][1] is after     # of X, then of W: one pass
+    change(layer)
+    assert layer.weight_amax is None
+    del library[:]
+    layer(x)
+    assert [a for n, a in library if n == "quantize"][1] is None
+    layer.weight_amax = layer.weight.detach().abs().max().float().reshape(1)
+    assert layer.weight_amax.item() == layer.weight.abs().max().item()
+    layer.weight_amax = None
+    assert layer.weight_amax is None
+
+
+def test_a_step_counts_as_a_change_of_what_it_writes():
+    """The kernel writes behind torch's back: the version counters of the parameters move all the same."""
+    net = Scaled()
+    opt = AdamW.of(net, lr=1e-2)
+    y = net(_x(16, 32, 12)).float().sum() + net.norm.square().sum()   # the square's backward needs norm as it was
+    y.backward(retain_graph=True)
+    before = [p._version for p in net.parameters()]
+    opt.step()
+    assert all(p._version > v for p, v in zip(net.parameters(), before))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+
+
+def test_a_layer_made_in_inference_mode():
+    with torch.inference_mode():
+        layer = _layer(32, 32, 13)
+        layer.weight_amax = layer.weight.abs().max().float().reshape(1)
+        assert layer(_x(16, 32, 13)).shape == (16, 32)
+        assert layer.weight_amax is not None
