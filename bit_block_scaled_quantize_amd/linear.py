@@ -123,6 +123,8 @@ class _LinearActFn(torch.autograd.Function):
                 x_amax = amax(t)
         qx, _ = quantize(t, "1x16", "rn", amax=x_amax)
         if layer.frozen is not None and not train:
+            if layer._frozen_of != _state_of(weight):
+                layer.freeze()
             qw, qwt = layer.frozen, None
         else:
             qw, qwt = quantize(weight, "16x16", "rn", amax=layer.weight_amax, emit_transposed=train)
@@ -184,8 +186,8 @@ class NVFP4Linear(torch.nn.Module):
     weight_amax: None, or a device float [1] holding max|W| (optim.AdamW sets it at every step), which
     makes the weight's quantization a single pass. It holds for the weight as it is when this is set:
     once torch has changed or replaced the weight (load_state_dict, an in-place operation) it reads
-    None. torch counts no writes through ``weight.data`` and none by other libraries: after those set
-    it to None.
+    None. torch counts no writes through ``weight.data``, to a weight made in inference mode, or by
+    other libraries: after those set it to None (and freeze() again).
     """
 
     def __init__(self, in_features: int, out_features: int, device=None, sign_mask: int = 0x6E04,
@@ -209,7 +211,7 @@ class NVFP4Linear(torch.nn.Module):
         self._calls = 0
         self.last_output_amax = None
         self.weight_amax = None
-        self.frozen = None
+        self.frozen = self._frozen_of = None
 
     @property
     def weight_amax(self):
@@ -231,9 +233,11 @@ class NVFP4Linear(torch.nn.Module):
 
     def freeze(self):
         """Quantizes the weight once for the calls without gradients that follow (generation: any
-        number of tokens, down to one). unfreeze() before the weight changes."""
+        number of tokens, down to one). A call that finds the weight changed (an optimizer's step,
+        load_state_dict: what weight_amax sees) quantizes it anew."""
         with torch.no_grad():
             self.frozen, _ = quantize(self.weight, "16x16", "rn", amax=self.weight_amax)
+        self._frozen_of = _state_of(self.weight)
         return self
 
     def unfreeze(self):

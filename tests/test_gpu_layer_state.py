@@ -57,3 +57,19 @@ def test_weights_loaded_after_a_step(kw):
     opt.step()
     assert layer.weight_amax.item() == layer.weight.abs().max().item()
     assert torch.equal(layer(x).detach(), _fresh(layer, x))
+
+
+def test_a_frozen_layer_after_a_step():
+    """An evaluation between two steps uses the weights of the last one, for one token too."""
+    log("frozen layer after a step")
+    layer = _layer(128, 96, 23, bias=True, activation="silu")
+    opt = AdamW.of(layer, lr=3e-1)
+    x = _bf16((32, 128), 24)
+    layer.freeze()
+    for _ in range(3):
+        with torch.no_grad():
+            for t in (1, 7, 32):
+                assert torch.equal(layer(x[:t]), _fresh(layer, x[:t]))
+        layer(x).float().sum().backward()
+        opt.step()
+        opt.zero_grad()

@@ -323,3 +323,32 @@ def test_a_layer_made_in_inference_mode():
         layer.weight_amax = layer.weight.abs().max().float().reshape(1)
         assert layer(_x(16, 32, 13)).shape == (16, 32)
         assert layer.weight_amax is not None
+
+
+@pytest.mark.parametrize("change", CHANGES + ["step"])
+@pytest.mark.parametrize("kw", [dict(), dict(bias=True, activation="relu2")], ids=["plain", "act"])
+def test_a_frozen_quantization_follows_the_weight(library, change, kw):
+    """freeze() saves the quantization of an unchanged weight and no more than that."""
+    layer = _layer(32, 32, 14, **kw)
+    opt = AdamW.of(layer, lr=1e-1)
+    x = _x(16, 32, 14)
+    layer.freeze()
+
+    def calls():
+        del library[:]
+        with torch.no_grad():
+            y = layer(x)
+        return y, [n for n, _ in library].count("quantize")
+
+    first, n = calls()
+    assert n == 1 and calls()[1] == 1                                 # of X alone
+    if change == "step":
+        layer(x).float().sum().backward()
+        opt.step()
+    else:
+        change(layer)
+    y, n = calls()
+    assert n == 2 and not torch.equal(y, first)
+    assert calls()[1] == 1 and torch.equal(calls()[0], y)
+    layer.unfreeze()
+    assert torch.equal(layer(x).detach(), y)
