@@ -12,10 +12,15 @@ from . import AdamWPlan, AdamWTensor, NVFP4Error, adamw
 from .linear import NVFP4Linear
 
 
+def _version(p):
+    return 0 if p.is_inference() else p._version
+
+
 class AdamW:
     """entries: (parameter, gradient, weight_decay) triples, or (parameter, gradient) with the default
-    decay. A BF16 parameter gets an FP32 master copy; an FP32 one is updated itself. The gradient (FP32
-    or BF16, the parameter's shape) is read where it is at every step.
+    decay. A BF16 parameter gets an FP32 master copy, which follows it where it is changed between steps
+    (as far as torch counts changes: not through .data); an FP32 one is updated itself. The gradient
+    (FP32 or BF16, the parameter's shape) is read where it is at every step.
 
     states: "fp32", or "8bit" (two bytes and a sixteenth per element instead of eight).
     max_norm: clip the gradients' norm over all tensors; step() then returns the norm (a device
@@ -51,6 +56,15 @@ class AdamW:
         self.amax = torch.zeros((len(tensors),), dtype=torch.float32, device=self.plan.device)
         self._layers = list(layers)                          # (index of the weight, layer)
         self._mains = []                                     # (parameter, its main gradient)
+        self._seen = [_version(p) for p in self.params]
+
+    def _follow_parameters(self):
+        """Masters of parameters that changed since the last step: where the BF16 value is no longer the
+        master's, the parameter's."""
+        for i, (p, m) in enumerate(zip(self.params, self.masters)):
+            if p is not m and _version(p) != self._seen[i]:
+                m.copy_(torch.where(p == m.bfloat16(), m, p.float()))
+                self._seen[i] = _version(p)
 
     def _state(self, p):
         n, dev = p.numel(), p.device
@@ -108,11 +122,13 @@ class AdamW:
             if p.grad is not None:                           # of a use without the main gradient
                 main.add_(p.grad)
                 p.grad = None
+        self._follow_parameters()
         self.steps += 1
         norm = adamw(self.plan, lr=self.lr if lr is None else lr, betas=self.betas, eps=self.eps, step=self.steps,
                      max_norm=self.max_norm, seed=self.seed, amax_out=self.amax)
         # the kernel wrote them: autograd and the layers are to see it
         torch.autograd.graph.increment_version([p for p in self.params if not p.is_inference()])
+        self._seen = [_version(p) for p in self.params]
         for i, layer in self._layers:
             layer.weight_amax = self.amax[i:i + 1]
         return norm
@@ -123,6 +139,7 @@ class AdamW:
             p.grad = None
 
     def state_dict(self) -> dict:
+        self._follow_parameters()
         keys = ("m", "v") if self.states == "fp32" else ("m", "v", "m_scale", "v_scale")
         return {"states": self.states, "steps": self.steps, "seed": self.seed,
                 "masters": [m.clone() for m in self.masters],
@@ -140,6 +157,7 @@ class AdamW:
         for p, m in zip(self.params, self.masters):
             if p is not m:
                 p.copy_(m)
+        self._seen = [_version(p) for p in self.params]
         for _, layer in self._layers:
             layer.weight_amax = None                         # of the weights before
         self.steps, self.seed = state["steps"], state["seed"]

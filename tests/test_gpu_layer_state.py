@@ -73,3 +73,21 @@ def test_a_frozen_layer_after_a_step():
         layer(x).float().sum().backward()
         opt.step()
         opt.zero_grad()
+
+
+@pytest.mark.parametrize("states", ["fp32", "8bit"])
+def test_a_step_after_loading_weights(states):
+    """The step moves the loaded weights by what it moves any weights with this gradient and history, not
+    back to those of the optimizer's master copies."""
+    log(f"step after loading {states}")
+    layer = _layer(64, 48, 25)
+    opt = AdamW.of(layer, lr=1e-2, weight_decay=0.0, states=states)
+    layer.main_grad.copy_(_bf16((48, 64), 26).float())
+    opt.step()
+    loaded = _bf16((48, 64), 27, 4.0)
+    layer.load_state_dict({"weight": loaded})
+    opt.step()
+    moved = (opt.masters[0] - loaded.float()).abs()
+    assert torch.equal(layer.weight.detach(), opt.masters[0].bfloat16())
+    # the same gradient twice: m/(1 - b1^t) = g and v/(1 - b2^t) = g^2, 8-bit states within two E4M3 gaps (2^-3 each)
+    assert moved.max().item() <= 1e-2 * 1.5 and moved.min().item() >= 1e-2 * 0.5

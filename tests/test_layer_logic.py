@@ -352,3 +352,32 @@ def test_a_frozen_quantization_follows_the_weight(library, change, kw):
     assert calls()[1] == 1 and torch.equal(calls()[0], y)
     layer.unfreeze()
     assert torch.equal(layer(x).detach(), y)
+
+
+@pytest.mark.parametrize("change", [_copy, _load, _reset])
+def test_a_step_starts_from_the_weights_that_are_there(change):
+    """Weights loaded after the optimizer was made are stepped, not overwritten by its master copies;
+    what was not changed keeps the master's FP32 value (an average swapped in and out again)."""
+    layer = _layer(32, 32, 15)
+    opt = AdamW.of(layer, lr=1e-3, weight_decay=0.0)
+    for seed in range(2):
+        layer(_x(16, 32, seed)).float().sum().backward()
+        opt.step()
+        opt.zero_grad()
+    master = opt.masters[0].clone()
+    assert not torch.equal(master, master.bfloat16().float())
+    keep = layer.weight.detach().clone()
+    change(layer)                                                     # swapped in, and out again
+    with torch.no_grad():
+        layer.weight.copy_(keep)
+    assert torch.equal(opt.state_dict()["masters"][0], master)
+    change(layer)
+    with torch.no_grad():
+        layer.weight[:3] = keep[:3]
+    here = layer.weight.detach().float()
+    here[:3] = master[:3]
+    assert torch.equal(opt.state_dict()["masters"][0], here)
+    layer(_x(16, 32, 3)).float().sum().backward()
+    opt.step()
+    assert (opt.masters[0] - here).abs().max() <= 1.5e-2             # a few times lr / (1 - beta1) at most
+    assert torch.equal(layer.weight.detach(), opt.masters[0].bfloat16())
