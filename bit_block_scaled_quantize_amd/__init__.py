@@ -262,6 +262,13 @@ def workspace_size(op: int, rows: int, cols: int, nseg: int = 1) -> int:
     return int(_load().nvfp4_workspace_size(op, rows, cols, nseg))
 
 
+def _given_workspace(workspace: torch.Tensor) -> int:
+    """Bytes of a caller's workspace."""
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise NVFP4Error("workspace must be a contiguous GPU tensor")
+    return workspace.numel() * workspace.element_size()
+
+
 def _workspace(op, rows, cols, nseg, device):
     n = workspace_size(op, rows, cols, nseg)
     return torch.empty((max(n, 1),), dtype=torch.uint8, device=device), n
@@ -287,7 +294,7 @@ def quantize(x: torch.Tensor, block: str = "1x16", rounding: str = "rn", seed: i
         if workspace is None:
             workspace, ws_n = _workspace(OP_QUANTIZE, rows, cols, nseg, x.device)
         else:
-            ws_n = workspace.numel()
+            ws_n = _given_workspace(workspace)
     _check_table(segments, "segments")
     _check_vec(amax, nseg, "amax")
     _check_q(out, nseg, "out")
@@ -350,7 +357,7 @@ def rht_rows_quantize(x: torch.Tensor, sign_mask: int, rounding: str = "rn", see
         if workspace is None:
             workspace, ws_n = _workspace(OP_QUANTIZE, rows, cols, 1, x.device)
         else:
-            ws_n = workspace.numel()
+            ws_n = _given_workspace(workspace)
     _check_vec(amax, 1, "amax")
     _check_q(out, 1, "out")
     oc = out.c()
@@ -422,7 +429,7 @@ def rht_quantize(x: torch.Tensor, sign_mask: int, rounding: str = "rn", seed: in
         if workspace is None:
             workspace, ws_n = _workspace(OP_RHT_QUANTIZE, tokens, cols, nseg, x.device)
         else:
-            ws_n = workspace.numel()
+            ws_n = _given_workspace(workspace)
     _check_table(segments, "segments")
     _check_vec(amax, nseg, "amax")
     _check_q(out, nseg, "out")
@@ -478,7 +485,7 @@ def gemm_ex(a: NVFP4Tensor, b: NVFP4Tensor, out: torch.Tensor | None = None,
     if workspace is None:
         workspace, ws_n = _workspace(OP_GEMM_EX, a.rows, b.rows, 1, a.codes.device)
     else:
-        ws_n = workspace.numel()
+        ws_n = _given_workspace(workspace)
     ac, bc = a.c(), b.c()
     _check(lib.nvfp4_gemm_ex(ctypes.byref(ac), ctypes.byref(bc), _ptr(out), out.stride(0), kind,
                              _ptr(amax_out), _ptr(workspace), ws_n, _stream(stream)))
@@ -519,7 +526,7 @@ def gemm_act(a: NVFP4Tensor, b: NVFP4Tensor, bias: torch.Tensor | None = None, a
         ws_n = workspace_size(OP_GEMM_ACT, m, n, a.cols)
         workspace = torch.empty((ws_n,), dtype=torch.uint8, device=a.codes.device) if ws_n else None
     else:
-        ws_n = workspace.numel()
+        ws_n = _given_workspace(workspace)
     ac, bc = a.c(), b.c()
     _check(lib.nvfp4_gemm_act(ctypes.byref(ac), ctypes.byref(bc), _ptr(out), _row_stride(out), _ptr(bias),
                               0 if bias is None else _DTYPE[bias.dtype], kind, _ptr(residual),
@@ -552,7 +559,7 @@ def act_grad(dy: torch.Tensor, preact: torch.Tensor | None = None, activation: s
             ws_n = workspace_size(OP_ACT_GRAD, m, n)
             workspace = torch.empty((ws_n,), dtype=torch.uint8, device=dy.device) if ws_n else None
         else:
-            ws_n = workspace.numel()
+            ws_n = _given_workspace(workspace)
     _check(lib.nvfp4_act_grad(_ptr(dy), dt, m, n, _row_stride(dy), _ptr(preact), 0 if preact is None else _row_stride(preact),
                               kind, _ptr(dz), 0 if dz is None else _row_stride(dz), _ptr(dbias), int(accumulate),
                               _ptr(workspace), ws_n, _stream(stream)))
@@ -613,7 +620,7 @@ def amax(x: torch.Tensor, segments: torch.Tensor | None = None, rht: bool | int 
     if workspace is None:
         workspace, ws_n = _workspace(OP_RHT_QUANTIZE if int(rht) == 1 else OP_QUANTIZE, rows, cols, nseg, x.device)
     else:
-        ws_n = workspace.numel()
+        ws_n = _given_workspace(workspace)
     _check_table(segments, "segments")
     _check_vec(out, nseg, "out")
     _check(lib.nvfp4_amax(_ptr(x), dt, rows, cols, ld, _ptr(segments), nseg, int(rht),
@@ -632,7 +639,7 @@ def amax_pair(x: torch.Tensor, sign_mask: int, out: torch.Tensor | None = None,
     if workspace is None:
         workspace, ws_n = _workspace(OP_AMAX_PAIR, tokens, cols, 1, x.device)
     else:
-        ws_n = workspace.numel()
+        ws_n = _given_workspace(workspace)
     _check_vec(out, 2, "out")
     _check(lib.nvfp4_amax_pair(_ptr(x), dt, tokens, cols, ld, sign_mask & 0xFFFF, _ptr(out),
                                _ptr(workspace), ws_n, _stream(stream)))
@@ -717,7 +724,7 @@ def _moe_call(x, layer: _CMoE, out, ids_out, weights_out, workspace, stream):
             raise NVFP4Error(f"{what} must be a contiguous {dtype} GPU tensor of at least {n} elements")
     _check(lib.nvfp4_moe_tokens(ctypes.byref(layer), _ptr(x), tokens, _row_stride(x), _ptr(out), _row_stride(out),
                                 _ptr(ids_out), _ptr(weights_out), _ptr(workspace),
-                                0 if workspace is None else workspace.numel(), _stream(stream)))
+                                0 if workspace is None else _given_workspace(workspace), _stream(stream)))
     return out
 
 
@@ -813,7 +820,7 @@ def adamw(plan: AdamWPlan, lr: float, betas=(0.9, 0.95), eps: float = 1e-8, step
         if workspace is None:
             workspace, ws_n = _workspace(OP_ADAMW, 0, 0, 1, plan.device)
         else:
-            ws_n = workspace.numel()
+            ws_n = _given_workspace(workspace)
     hyper = _CAdamWHyper(lr, betas[0], betas[1], eps, step, 0.0 if max_norm is None else max_norm, seed & (2 ** 64 - 1))
     _check(lib.nvfp4_adamw(_ptr(plan.table), len(plan.tensors), plan.chunks, int(plan.eight_bit), ctypes.byref(hyper),
                            _ptr(norm_out), _ptr(amax_out), _ptr(workspace) if max_norm is not None else None, ws_n,
