@@ -759,7 +759,8 @@ class AdamWPlan:
         if not tensors:
             raise NVFP4Error("an AdamW plan needs at least one tensor")
         lib = _load()
-        self.tensors = tensors
+        self.tensors, self.count = tensors, len(tensors)
+        self._kept = []                                      # every tensor whose address is in the table
         self.eight_bit = tensors[0].m.dtype == torch.uint8
         self.device = tensors[0].p.device
         array = (_CAdamWTensor * len(tensors))(*(self._entry(i, t) for i, t in enumerate(tensors)))
@@ -779,6 +780,7 @@ class AdamWPlan:
                     or x.device.type != "cuda" or x.device != self.device):
                 raise NVFP4Error(f"tensor {i}: {name} must be a contiguous {dtype} tensor of {count} elements on "
                                  f"the GPU of the first tensor")
+            self._kept.append(x)
             return x.data_ptr()
 
         if not isinstance(t.grad, torch.Tensor) or t.grad.dtype not in _DTYPE:
@@ -814,7 +816,7 @@ def adamw(plan: AdamWPlan, lr: float, betas=(0.9, 0.95), eps: float = 1e-8, step
     if max_norm is not None and norm_out is None:
         norm_out = torch.empty((1,), dtype=torch.float32, device=plan.device)
     _check_vec(norm_out, 1, "norm_out")
-    _check_vec(amax_out, len(plan.tensors), "amax_out")
+    _check_vec(amax_out, plan.count, "amax_out")
     ws_n = 0
     if max_norm is not None:
         if workspace is None:
@@ -822,7 +824,7 @@ def adamw(plan: AdamWPlan, lr: float, betas=(0.9, 0.95), eps: float = 1e-8, step
         else:
             ws_n = _given_workspace(workspace)
     hyper = _CAdamWHyper(lr, betas[0], betas[1], eps, step, 0.0 if max_norm is None else max_norm, seed & (2 ** 64 - 1))
-    _check(lib.nvfp4_adamw(_ptr(plan.table), len(plan.tensors), plan.chunks, int(plan.eight_bit), ctypes.byref(hyper),
+    _check(lib.nvfp4_adamw(_ptr(plan.table), plan.count, plan.chunks, int(plan.eight_bit), ctypes.byref(hyper),
                            _ptr(norm_out), _ptr(amax_out), _ptr(workspace) if max_norm is not None else None, ws_n,
                            _stream(stream)))
     return norm_out

@@ -27,7 +27,8 @@ class MoETokens:
         self.weights = MoEWeights(router, w1, w2, top_k, activation, gated, score, renormalize, routed_scale)
         self.max_tokens = max_tokens
         self.workspace = moe_workspace(self.weights, max_tokens)
-        self._layer = self.weights.c()                       # checked once; its tensors are self.weights'
+        self._layer = self.weights.c()                       # checked once; addresses of:
+        self._kept = (router, *(t for w in (w1, w2) for t in (w.codes, w.scales, w.global_scale)))
 
     @classmethod
     def from_bf16(cls, router: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, top_k: int, **kw):

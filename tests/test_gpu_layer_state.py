@@ -91,3 +91,45 @@ def test_a_step_after_loading_weights(states):
     assert torch.equal(layer.weight.detach(), opt.masters[0].bfloat16())
     # the same gradient twice: m/(1 - b1^t) = g and v/(1 - b2^t) = g^2, 8-bit states within two E4M3 gaps (2^-3 each)
     assert moved.max().item() <= 1e-2 * 1.5 and moved.min().item() >= 1e-2 * 0.5
+
+
+def _fill_freed_memory():
+    """Hands out, and writes, blocks of the sizes that a small layer's tensors have."""
+    kept = [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda") for n in (512, 1024, 4096, 8192, 16384, 32768) for _ in range(40)]
+    torch.cuda.synchronize()
+    return kept
+
+
+def test_an_expert_layer_keeps_the_tensors_it_was_made_with():
+    """Also where its weights are given other tensors later: the addresses it passes stay valid."""
+    from bit_block_scaled_quantize_amd.moe import MoETokens
+    log("expert layer's tensors")
+    make = lambda seed: MoETokens.from_bf16(_bf16((8, 128), seed), _bf16((8 * 64, 128), seed + 1, 0.1).view(8, 64, 128),  # noqa: E731
+                                            _bf16((8 * 128, 64), seed + 2, 0.1).view(8, 128, 64), 2)
+    layer, other = make(31), make(41)
+    x = _bf16((5, 128), 34)
+    want = layer(x).clone()
+    torch.cuda.synchronize()
+    layer.weights.router, layer.weights.w1, layer.weights.w2 = other.weights.router, other.weights.w1, other.weights.w2
+    del other
+    held = _fill_freed_memory()
+    assert torch.equal(layer(x), want)
+    del held
+
+
+def test_a_plan_keeps_the_tensors_it_was_made_with():
+    log("plan's tensors")
+    def tensors():
+        return [nv.AdamWTensor(p=_bf16((16, 64), 51).float().reshape(-1), grad=_bf16((16, 64), 52).float().reshape(-1),
+                               m=torch.zeros(1024, device="cuda"), v=torch.zeros(1024, device="cuda"))]
+    want = tensors()
+    nv.adamw(nv.AdamWPlan(want), lr=1e-2, step=1)
+    ts = tensors()
+    plan, p = nv.AdamWPlan(ts), ts[0].p
+    torch.cuda.synchronize()
+    ts[0].grad = ts[0].m = ts[0].v = None
+    plan.tensors[0].p = None
+    plan.tensors.clear()
+    held = _fill_freed_memory()
+    nv.adamw(plan, lr=1e-2, step=1)
+    assert torch.equal(p, want[0].p) and all(torch.all(h == 0x5A) for h in held)
