@@ -147,11 +147,12 @@ class AdamW:
 
     def load_state_dict(self, state: dict):
         """Restores masters, states and step count, and the BF16 weights from the masters."""
-        if state["states"] != self.states or len(state["masters"]) != len(self.masters):
-            raise NVFP4Error("the state is of another optimizer")
         keys = ("m", "v") if self.states == "fp32" else ("m", "v", "m_scale", "v_scale")
-        for mine, theirs in [(self.masters, state["masters"])] + [
-                ([getattr(t, k) for t in self.plan.tensors], state[k]) for k in keys]:
+        pairs = [(self.masters, state["masters"])] if state["states"] == self.states else []
+        pairs += [([getattr(t, k) for t in self.plan.tensors], state[k]) for k in keys if pairs]
+        if not pairs or any([a.shape for a in mine] != [b.shape for b in theirs] for mine, theirs in pairs):
+            raise NVFP4Error("the state is of another optimizer")
+        for mine, theirs in pairs:
             for a, b in zip(mine, theirs):
                 a.copy_(b)
         for p, m in zip(self.params, self.masters):

@@ -381,3 +381,19 @@ def test_a_step_starts_from_the_weights_that_are_there(change):
     opt.step()
     assert (opt.masters[0] - here).abs().max() <= 1.5e-2             # a few times lr / (1 - beta1) at most
     assert torch.equal(layer.weight.detach(), opt.masters[0].bfloat16())
+
+
+def test_a_state_of_other_shapes_is_refused():
+    """Before anything of it is copied: one element would spread over a whole tensor."""
+    def make(n):
+        p = torch.nn.Parameter(torch.full((n,), 2.0))
+        return AdamW([(p, torch.ones(n)), (torch.nn.Parameter(torch.full((4,), 3.0)), torch.ones(4))], lr=1e-2)
+
+    opt, other = make(8), make(1)
+    opt.step()
+    keep = opt.state_dict()
+    for key, value in (("masters", other.masters), ("m", other.state_dict()["m"]), ("v", keep["v"][:1])):
+        with pytest.raises(nv.NVFP4Error, match="another optimizer"):
+            opt.load_state_dict({**keep, "masters": [torch.zeros_like(m) for m in keep["masters"]], key: value})
+        assert all(torch.equal(a, b) for k in ("masters", "m", "v") for a, b in zip(opt.state_dict()[k], keep[k])), key
+    opt.load_state_dict(keep)
