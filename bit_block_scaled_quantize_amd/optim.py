@@ -123,9 +123,9 @@ class AdamW:
                 main.add_(p.grad)
                 p.grad = None
         self._follow_parameters()
-        self.steps += 1
-        norm = adamw(self.plan, lr=self.lr if lr is None else lr, betas=self.betas, eps=self.eps, step=self.steps,
+        norm = adamw(self.plan, lr=self.lr if lr is None else lr, betas=self.betas, eps=self.eps, step=self.steps + 1,
                      max_norm=self.max_norm, seed=self.seed, amax_out=self.amax)
+        self.steps += 1
         # the kernel wrote them: autograd and the layers are to see it
         torch.autograd.graph.increment_version([p for p in self.params if not p.is_inference()])
         self._seen = [_version(p) for p in self.params]

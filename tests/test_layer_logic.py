@@ -397,3 +397,17 @@ def test_a_state_of_other_shapes_is_refused():
             opt.load_state_dict({**keep, "masters": [torch.zeros_like(m) for m in keep["masters"]], key: value})
         assert all(torch.equal(a, b) for k in ("masters", "m", "v") for a, b in zip(opt.state_dict()[k], keep[k])), key
     opt.load_state_dict(keep)
+
+
+def test_a_refused_step_is_not_counted(monkeypatch):
+    p = torch.nn.Parameter(torch.ones(8))
+    opt = AdamW([(p, torch.ones(8))], lr=1e-2)
+    opt.step()
+
+    def refuse(*_, **__):
+        raise nv.NVFP4Error("out of range")
+
+    monkeypatch.setattr(optim, "adamw", refuse)
+    with pytest.raises(nv.NVFP4Error):
+        opt.step(lr=float("nan"))
+    assert opt.steps == 1
