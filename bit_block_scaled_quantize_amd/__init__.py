@@ -688,7 +688,7 @@ class MoEWeights:
 
 
 def moe_workspace(weights: MoEWeights, tokens: int) -> torch.Tensor:
-    """A workspace for moe_tokens with up to `tokens` tokens, its counters zero."""
+    """A workspace for moe_tokens with up to `tokens` tokens, its counters zeroed on the current stream."""
     n = _load().nvfp4_moe_workspace_size(ctypes.byref(weights.c()), tokens)
     if n == 0:
         raise NVFP4Error(f"no expert layer for {tokens} tokens: {_load().nvfp4_last_error().decode()}")

@@ -27,6 +27,8 @@ class MoETokens:
         self.weights = MoEWeights(router, w1, w2, top_k, activation, gated, score, renormalize, routed_scale)
         self.max_tokens = max_tokens
         self.workspace = moe_workspace(self.weights, max_tokens)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()        # the first call may be on any stream, and needs the zeros
         self._layer = self.weights.c()                       # checked once; addresses of:
         self._kept = (router, *(t for w in (w1, w2) for t in (w.codes, w.scales, w.global_scale)))
 

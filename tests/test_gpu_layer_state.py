@@ -133,3 +133,27 @@ def test_a_plan_keeps_the_tensors_it_was_made_with():
     held = _fill_freed_memory()
     nv.adamw(plan, lr=1e-2, step=1)
     assert torch.equal(p, want[0].p) and all(torch.all(h == 0x5A) for h in held)
+
+
+def test_the_first_call_of_an_expert_layer_on_another_stream():
+    """The workspace's counters are zero by then, however busy the stream is that the layer was made on."""
+    from bit_block_scaled_quantize_amd.moe import MoETokens
+    log("expert layer's first call")
+    w = MoETokens.from_bf16(_bf16((8, 128), 61), _bf16((8 * 64, 128), 62, 0.1).view(8, 64, 128),
+                            _bf16((8 * 128, 64), 63, 0.1).view(8, 128, 64), 2)
+    x, n = _bf16((20, 128), 64), w.workspace.numel()
+    want = w(x).clone()
+    a = torch.randn(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        dirty = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        del dirty                                                     # the block that the next layer's workspace gets
+        for _ in range(20):
+            a @ a
+        layer = MoETokens(w.weights.router, w.weights.w1, w.weights.w2, 2)
+        got = layer(x, stream=side)
+        side.synchronize()
+        assert torch.equal(got, want)
+        torch.cuda.synchronize()
