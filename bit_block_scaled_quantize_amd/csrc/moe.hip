@@ -404,13 +404,15 @@ __device__ __forceinline__ void join_pairs(const MoeArgs& a, const MoeWork& w, i
 // leaves at once) x row tiles, tiles of one expert next to each other.
 // UP: rows of W1, K = hidden -> h[pair][f]. GATED: fragments 0 .. R/2 - 1 hold the gate's rows, the
 // others the same rows of U. DOWN: rows of W2, K = ffn -> part[pair][n], then y.
-// kCols: columns staged at a time (8, or 1 for one token). W: waves, which split K. A: steps in flight.
+// kCols: columns staged at a time (8, or 1 for one token). A: steps in flight.
 // JOIN: the last workgroup of a row tile writes y.
-template <bool UP, bool GATED, int R, int W, int A, int kCols, bool JOIN, Shape S>
-__global__ __launch_bounds__(64 * W) void k_expert(MoeArgs a, MoeWork w, int tiles, uint32_t pitch) {
-  constexpr int kWaves = W, kThreads = 64 * W;
+// The waves split K, the same number of them whatever the batch: the order of a token's sums, and so its
+// result, does not depend on how many tokens there are.
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+template <bool UP, bool GATED, int R, int A, int kCols, bool JOIN, Shape S>
+__global__ __launch_bounds__(kThreads) void k_expert(MoeArgs a, MoeWork w, int tiles, uint32_t pitch) {
   static_assert(!GATED || R % 2 == 0, "a gated tile holds as many gate as up fragments");
-  static_assert(R <= W, "a wave per fragment of output rows");
+  static_assert(R <= kWaves, "a wave per fragment of output rows");
   constexpr int RO = GATED ? R / 2 : R;                       // fragments of output rows
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   float* red = reinterpret_cast<float*>(lds);                 // kWaves R fragments
@@ -577,16 +579,16 @@ __global__ __launch_bounds__(256) void k_join(MoeArgs a, MoeWork w) {
   join_pairs(a, w, (int64_t)blockIdx.x * 64 + threadIdx.x % 32 * 2, (int)blockIdx.y * 8 + (int)threadIdx.x / 32, 64);
 }
 
-constexpr int kWideTokens = 4;                                // up to here 8 waves split K, beyond 4
+constexpr int kJoinTokens = 4;                                // up to here k_expert<DOWN> writes y itself
 constexpr int kMostCols = 8;                                  // tokens of an expert at a time
-constexpr int kMostLds = 8 * 4 * 64 * 16 + kZeroBytes + kMostCols * (2 * kChunk + 16);
+constexpr int kMostLds = kWaves * 4 * 64 * 16 + kZeroBytes + kMostCols * (2 * kChunk + 16);
 
 int64_t tiles_of(int64_t rows, int frags) { return (rows + 16 * frags - 1) / (16 * frags); }
 
-template <bool UP, bool GATED, int R, int W, int A, int COLS, bool JOIN, Shape S>
+template <bool UP, bool GATED, int R, int A, int COLS, bool JOIN, Shape S>
 hipError_t launch_expert_as(const MoeArgs& a, const MoeWork& w, hipStream_t stream) {
   // the staged columns can take more LDS than a launch may by default
-  static const hipError_t ready = hipFuncSetAttribute((const void*)k_expert<UP, GATED, R, W, A, COLS, JOIN, S>,
+  static const hipError_t ready = hipFuncSetAttribute((const void*)k_expert<UP, GATED, R, A, COLS, JOIN, S>,
                                                       hipFuncAttributeMaxDynamicSharedMemorySize, kMostLds);
   if (ready != hipSuccess) return ready;
   const int64_t K = UP ? a.hidden : a.ffn, N = UP ? a.ffn : a.hidden;
@@ -595,8 +597,8 @@ hipError_t launch_expert_as(const MoeArgs& a, const MoeWork& w, hipStream_t stre
   const int tiles = (int)tiles_of(N, GATED ? R / 2 : R);
   const int64_t staged = K < kChunk ? (K + kStep<S> - 1) / kStep<S> * kStep<S> : kChunk;
   const uint32_t pitch = (uint32_t)(2 * staged + 16);         // rows start 4 banks apart
-  const size_t bytes = (size_t)W * R * 64 * 16 + kZeroBytes + (size_t)COLS * pitch;
-  hipLaunchKernelGGL((k_expert<UP, GATED, R, W, A, COLS, JOIN, S>), dim3((unsigned)(most * tiles)), dim3(64 * W), bytes,
+  const size_t bytes = (size_t)kWaves * R * 64 * 16 + kZeroBytes + (size_t)COLS * pitch;
+  hipLaunchKernelGGL((k_expert<UP, GATED, R, A, COLS, JOIN, S>), dim3((unsigned)(most * tiles)), dim3(kThreads), bytes,
                      stream, a, w, tiles, pitch);
   return hipSuccess;
 }
@@ -604,11 +606,13 @@ hipError_t launch_expert_as(const MoeArgs& a, const MoeWork& w, hipStream_t stre
 template <bool UP, bool GATED, Shape S>
 hipError_t launch_expert_k(const MoeArgs& a, const MoeWork& w, hipStream_t stream) {
   // (us on 122 experts of 2688 x 1856, 64 tokens: up R = 2 with A = 1, 2, 3: 95, 95, 93, R = 4: 98; down
-  // R = 2: 108 with A = 1, 110 with 2; R = 4: 96 with A = 1, 115 with 2. 8 waves: down 129 to 140)
+  // R = 2: 108 with A = 1, 110 with 2; R = 4: 96 with A = 1, 115 with 2. Few tokens, the whole layer of 128
+  // experts: R = 2 with A = 2, 3, 4, 5: 1 token 24.3, 24.9, 25.3, 25.5, 4 tokens 51, 58, 62, 64; 8 waves
+  // with A = 2 24.1 and 70, but at 64 tokens down 129 to 140)
   constexpr int R = UP ? 2 : 4, A = UP ? 3 : 1;
-  if (a.tokens == 1) return launch_expert_as<UP, GATED, 2, 8, 2, 1, !UP, S>(a, w, stream);
-  if (a.tokens <= kWideTokens) return launch_expert_as<UP, GATED, 2, 8, 2, kMostCols, !UP, S>(a, w, stream);
-  return launch_expert_as<UP, GATED, R, 4, A, kMostCols, false, S>(a, w, stream);
+  if (a.tokens == 1) return launch_expert_as<UP, GATED, 2, 2, 1, !UP, S>(a, w, stream);
+  if (a.tokens <= kJoinTokens) return launch_expert_as<UP, GATED, 2, 2, kMostCols, !UP, S>(a, w, stream);
+  return launch_expert_as<UP, GATED, R, A, kMostCols, false, S>(a, w, stream);
 }
 
 template <bool UP, bool GATED>
@@ -671,7 +675,7 @@ hipError_t launch_moe(const MoeArgs& a, uint8_t* ws, hipStream_t stream) {
 #undef NVFP4_RT
   hipError_t e = a.gated ? launch_expert<true, true>(a, w, stream) : launch_expert<true, false>(a, w, stream);
   if (e != hipSuccess || (e = launch_expert<false, false>(a, w, stream)) != hipSuccess) return e;
-  if (a.tokens > kWideTokens)
+  if (a.tokens > kJoinTokens)
     hipLaunchKernelGGL(k_join, dim3((unsigned)((a.hidden + 63) / 64), (unsigned)((a.tokens + 7) / 8)), dim3(256), 0,
                        stream, a, w);
   return hipGetLastError();
