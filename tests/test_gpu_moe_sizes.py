@@ -1,5 +1,7 @@
 """nvfp4_moe_tokens at layer sizes of real use, where K is split over several steps of every wave: a
-token's result is bit for bit the same in every batch."""
+token's result is bit for bit the same in every batch; and just past the sizes from which the kernels take
+another turn: 4096 elements of K staged at a time (and of a token brought to FP16, and of a router's row),
+128 maxima of h (ffn 2048), 8 tokens of an expert at a time. Bounds as in test_gpu_moe.py."""
 import numpy as np
 import pytest
 import torch
@@ -33,3 +35,29 @@ def test_a_token_does_not_know_the_others(case):
         part = layer.run(x[first:first + n].contiguous())
         assert np.array_equal(part[1], ids[first:first + n]) and np.array_equal(part[2], w[first:first + n])
         assert torch.equal(part[0], y[first:first + n]), f"{n} tokens from {first}"
+
+
+LARGE = [dict(h=4112, f=2064), dict(h=8208, f=64), dict(h=4096, f=4176, activation="silu", gated=True),
+         dict(h=272, f=8208, activation="gelu"), dict(h=4160, f=4112, activation="silu", gated=True, score="sigmoid")]
+
+
+@pytest.mark.parametrize("t", [1, 4, 5, 20])
+@pytest.mark.parametrize("case", LARGE, ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
+def test_past_one_turn(case, t):
+    """Two experts, one a token: more than 8 tokens on one of them at 20."""
+    log(f"moe large {case} t={t}")
+    c = dict(case)
+    layer = Layer(2, c.pop("h"), c.pop("f"), 1, 840, **c)
+    x = _bf16((t, layer.h), 841 + t, outliers=True)
+    layer.check(x, str(case))
+    assert t < 20 or np.bincount(layer.run(x)[1][:, 0]).max() > 8
+
+
+def test_past_one_turn_with_rows_anywhere():
+    """The same walks over x and the router where rows start on any element."""
+    log("moe large, strides")
+    layer = Layer(2, 4112, 64, 2, 860)
+    x = _bf16((3, 4112), 861)
+    wide = torch.zeros((3, 4112 + 3), dtype=torch.bfloat16, device="cuda")
+    wide[:, 1:4113] = x
+    layer.check(wide[:, 1:4113], "strides")
