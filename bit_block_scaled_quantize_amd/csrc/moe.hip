@@ -448,7 +448,8 @@ __global__ __launch_bounds__(kThreads) void k_expert(MoeArgs a, MoeWork w, int t
     float4v acc[R][1];
 #pragma unroll
     for (int i = 0; i < R; ++i) acc[i][0] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-    float inv = 1.0f;                                         // undoes the column's power of two
+    float inv = 1.0f;                                         // undoes the column's power of two (exact)
+    float weight = 1.0f;                                      // DOWN: the pair's
     float scale = 1.0f;                                       // DOWN: the column's, in the lanes of row c
     Pipe<R, 1, A, S, TokensLds> pipe;
     for (int64_t k0 = 0; k0 < K; k0 += kChunk) {
@@ -482,7 +483,7 @@ __global__ __launch_bounds__(kThreads) void k_expert(MoeArgs a, MoeWork w, int t
         if constexpr (UP) {
           inv = w.x_inv[pair / a.top_k];
         } else {
-          inv = w.weights[pair];
+          weight = w.weights[pair];
           const int frags = (int)(K / 16);
 #pragma unroll
           for (int c = 0; c < kCols; ++c) {
@@ -507,7 +508,7 @@ __global__ __launch_bounds__(kThreads) void k_expert(MoeArgs a, MoeWork w, int t
               scale = r == c ? s : scale;
             }
           }
-          inv /= scale;                                       // a power of two: exact
+          inv = 1.0f / scale;
         }
       }
       if (k0 > 0 || q0 > 0) __syncthreads();                  // the columns staged before have been read
@@ -533,17 +534,17 @@ __global__ __launch_bounds__(kThreads) void k_expert(MoeArgs a, MoeWork w, int t
     __syncthreads();
     if (wave < RO) {                                          // a wave per fragment of output rows
       const int64_t n = n0 + 16 * wave + 4 * g;               // N % 16 == 0: all four rows or none
-      const float f = gs * inv;
+      const float f = gs * weight;                            // (times inv it can be too small for FP32 where v f inv is not)
       float4v v = take<kWaves, R, 1>(red, wave, 0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] *= f;
+      for (int q = 0; q < 4; ++q) v[q] = v[q] * f * inv;
       if constexpr (UP) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] = act_of(a.act, v[q]);
         if constexpr (GATED) {
           const float4v up = take<kWaves, R, 1>(red, wave + RO, 0);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] *= up[q] * f;
+          for (int q = 0; q < 4; ++q) v[q] *= up[q] * f * inv;
         }
         // this fragment's maximum; NaN is dropped by it and stays in h, an infinite one gives scale 1
         float top = 0.0f;

@@ -61,3 +61,17 @@ def test_past_one_turn_with_rows_anywhere():
     wide = torch.zeros((3, 4112 + 3), dtype=torch.bfloat16, device="cuda")
     wide[:, 1:4113] = x
     layer.check(wide[:, 1:4113], "strides")
+
+
+@pytest.mark.parametrize("which", ["w1", "w2"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_small_scales(which, gated):
+    """Tokens and tensor scales whose product leaves FP32's normal range on the way to a result that does
+    not: 1e-32 and 2^-26 or so, results of 1e-36."""
+    log(f"moe small scales {which} gated={gated}")
+    layer = Layer(8, 128, 64, 2, 880, activation="none", gated=gated)
+    getattr(layer.gpu.weights, which).global_scale.mul_(2.0 ** -13)
+    x = _bf16((6, 128), 881)
+    size = 1e-32 ** (0.5 if gated else 1)                            # gated: h is of the order of x^2
+    x = (x.float() * (size * torch.tensor([0.7, 1.0, 1.3, 2.0, 3.0, 5.0], device="cuda")[:, None])).bfloat16()
+    layer.check(x, "small scales")
