@@ -14,7 +14,8 @@
 // random bits) keeps the running mean's expectation. 16 bits because the rule truncates: on
 // average it rounds down by 2^-17 of a gap, and at b2 = 0.999 the 2^-9 of 8 bits would be a third
 // of what a step takes from r. m and r of an element share their h: only the two errors' product
-// knows. A nonzero r never becomes 0 (m / eps would follow).
+// knows. Rounding never makes a nonzero r 0 (m / eps would follow); below 2^-75, where r^2 leaves
+// FP32, r falls to 0, and m, no larger than gradients of that size make it, is nothing against eps.
 //
 // Memory bound: 4 + 8 + 2 bytes (grad, p in and out, w) plus 16 (FP32 m, v in and out) or 4.125
 // (8 bits) per element against about 40 and 110 vector operations. Each thread takes 8
@@ -198,8 +199,8 @@ __device__ __forceinline__ double group_sum(double v) {
   return s;
 }
 
-// partial[b] = sum of g^2 over the chunks b, b + gridDim.x, ...: FP32 over the 32 elements that a
-// thread squares per chunk, binary64 beyond, a fixed order throughout.
+// partial[b] = sum of g^2 over the chunks b, b + gridDim.x, ...: FP32 over the 8 elements that a
+// thread squares per chunk, binary64 beyond, a fixed order throughout. (A |g| above 1.8e19 makes it infinite.)
 __global__ __launch_bounds__(kThreads) void k_grad_norm(const AdamWEntry* __restrict__ table,
                                                         const int32_t* __restrict__ chunk_of, int64_t chunks,
                                                         double* __restrict__ partial) {

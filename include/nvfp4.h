@@ -507,14 +507,17 @@ typedef struct nvfp4_adamw_hyper {
  *   g  = c * grad,  c = min(1, max_norm / (norm + 1e-6)) with max_norm > 0, else 1
  *   m' = beta1 m + (1 - beta1) g;   v' = beta2 v + (1 - beta2) g^2
  *   p' = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m' / (sqrt(v' / (1 - beta2^step)) + eps)
- * norm = sqrt(sum of grad^2 over all tensors), summed in a fixed order. With max_norm > 0 a norm
- * that is infinite or NaN makes the step write back what it read (w_out = BF16(p)); without it
- * non-finite gradients are outside the contract.
+ * norm = sqrt(sum of grad^2 over all tensors), summed in a fixed order: eight consecutive squares
+ * in FP32, those sums in binary64. A gradient above 1.8e19 (eight neighbours above 6.5e18) therefore
+ * makes it infinite, and one below 2.6e-23 adds nothing. With max_norm > 0 a norm that is infinite or
+ * NaN makes the step write back what it read (w_out = BF16(p)); without it gradients that are not
+ * finite, or whose square is not, are outside the contract.
  *
  * NVFP4_STATE_8BIT holds m and r = sqrt(v) as E4M3 codes with one scale 2^e per 32 consecutive
  * elements (E8M0 code e + 127; e is the smallest exponent with max|x| <= 448 * 2^e, at least
  * -117; code 0 and value 0 for an all-zero block). A value y = |x| 2^-e is rounded up to the next
- * E4M3 value iff its fraction of the gap + h/65536 >= 1; a nonzero r never becomes 0. Element
+ * E4M3 value iff its fraction of the gap + h/65536 >= 1; rounding never makes a nonzero r 0 (an r
+ * below 2^-75 has a square below FP32 and ends as sqrt((1 - beta2) g^2)). Element
  * 8b + j (j < 8) of tensor i takes for h the 16 bits of half j % 2 (low first) of word j / 2 of
  * Philox4x32-10 with key (lo32 seed, hi32 seed) and counter (lo32 b, hi32 b, lo32 step, i), the
  * same h for m and r.
