@@ -20,7 +20,8 @@ call into libnvfp4, the wrapper only orders the calls and holds the buffers:
 
 With a bias, an activation or a residual the forward's last step is one call (gemm_act): Y =
 act(Xq Wq^T + b) + R in BF16, with max|Y| and, for the backward, the pre-activation in BF16; the
-backward then begins with act_grad: dZ = dY act'(Z), the bias gradient (added into ``bias_main_grad``
+backward then begins with act_grad: dZ = dY act'(Z) in BF16 (also of an FP32 dY: it goes to 4 bits
+next, and Z, whose slope it is, has no more), the bias gradient (added into ``bias_main_grad``
 like the weight's) and, for the residual, dY itself.
 
 Stochastic rounding draws from Philox4x32-10 keyed by the layer's seed; call n of the layer's

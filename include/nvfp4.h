@@ -442,7 +442,8 @@ typedef struct nvfp4_moe {
 /*
  * nvfp4_moe_tokens - a whole mixture-of-experts layer for a few tokens, a generation step's batch
  * ("Nemotron NVFP4" explainer, "The model underneath": expert layers, and "The honest part: this is
- * not end-to-end FP4": the expert weights are what runs in NVFP4). Activations stay in BF16:
+ * not end-to-end FP4": the expert weights are what runs in NVFP4). x and y are BF16; h is held
+ * with the 11 significant bits of FP16 (its range by powers of two beside it), sums are FP32:
  *   l = x router^T (FP32);  the top_k largest of a token's l pick its experts, ties the lowest
  *   s = softmax(l) over all experts, or 1 / (1 + exp(-l));  w = s * routed_scale, or with
  *   renormalize s / (sum over the token's experts of s + 1e-20) * routed_scale
