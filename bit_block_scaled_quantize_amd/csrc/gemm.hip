@@ -1740,7 +1740,9 @@ hipError_t launch_gemm_ex(GemmOperand a, GemmOperand b, int64_t M, int64_t N, in
 
 // A K that is not a multiple of 64 is brought to one by copying both operands into the workspace
 // (9/16 byte an element, twice): the tile kernel's DMA moves scales by aligned words of four, and the
-// general kernel, which does without, reaches a tenth of its rate (1003 x 1857 x 2704: 80 us).
+// general kernel, which does without, has no output pass of this kind and a lower rate. Measured, us
+// (nvfp4_gemm_act / nvfp4_gemm_ex in the general kernel): 2050 x 5120 x 2704 84 / 115, 4096 x 5120 x 1040
+// 67 / 85; 2600 x 2000 x 528, where copying and joining are most of it, 44 / 26.
 int64_t gemm_act_padded_k(int64_t K) { return K > 0 ? (K + 63) / 64 * 64 : 64; }
 
 size_t gemm_act_workspace_bytes(int64_t M, int64_t N, int64_t K) {
