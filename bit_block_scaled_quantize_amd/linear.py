@@ -73,11 +73,18 @@ class _LinearFn(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         (t,) = ctx.saved_tensors
+        if t.shape[0] == 0:
+            return dy.new_zeros(ctx.x_shape), _nothing(ctx, 1, ctx.layer.weight, ctx.layer.main_grad), None, None
         g = dy.reshape(-1, dy.shape[-1])
         if g.dtype not in (torch.bfloat16, torch.float32):
             g = g.float()                                    # exact widening; FP32 goes in as is
         dx, dw = _gradient_gemms(ctx, t, g.contiguous())
         return dx.view(ctx.x_shape), dw, None, None
+
+
+def _nothing(ctx, i, param, main_grad):
+    """The gradient of input i, a parameter, from a call without tokens (an expert that got none)."""
+    return torch.zeros_like(param) if ctx.needs_input_grad[i] and main_grad is None else None
 
 
 def _gradient_gemms(ctx, t, g):
@@ -150,6 +157,10 @@ class _LinearActFn(torch.autograd.Function):
     def backward(ctx, dy):
         layer = ctx.layer
         t, z = ctx.saved_tensors
+        dr = dy if ctx.needs_input_grad[3] else None
+        if t.shape[0] == 0:
+            return (dy.new_zeros(ctx.x_shape), _nothing(ctx, 1, layer.weight, layer.main_grad),
+                    _nothing(ctx, 2, layer.bias, layer.bias_main_grad), dr, None, None, None)
         g = dy.reshape(-1, dy.shape[-1])
         if g.dtype not in (torch.bfloat16, torch.float32):
             g = g.float()
@@ -169,7 +180,6 @@ class _LinearActFn(torch.autograd.Function):
             db = None
         elif db is not None:
             db = db.to(layer.bias.dtype)
-        dr = dy if ctx.needs_input_grad[3] else None
         return dx.view(ctx.x_shape), dw, db, dr, None, None, None
 
 

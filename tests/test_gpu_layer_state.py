@@ -157,3 +157,25 @@ def test_the_first_call_of_an_expert_layer_on_another_stream():
         side.synchronize()
         assert torch.equal(got, want)
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("main_grad", [True, False])
+@pytest.mark.parametrize("kw", [dict(), dict(bias=True, activation="silu")], ids=["plain", "act"])
+def test_no_tokens(kw, main_grad):
+    """An expert that got no token in a step: empty results and gradients, nothing added to the weight's,
+    with an output gradient of any strides (sum() gives one of stride 0)."""
+    log(f"no tokens {kw} main_grad={main_grad}")
+    layer = _layer(64, 32, 71, fp32_main_grad=main_grad, **kw)
+    if main_grad:
+        layer.main_grad.fill_(2.0)
+    for loss in (lambda y: y.sum(), lambda y: y.float().square().sum()):
+        x = torch.zeros(0, 64, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+        y = layer(x)
+        loss(y).backward()
+        assert y.shape == (0, 32) and x.grad.shape == (0, 64) and layer.last_output_amax.item() == 0
+        if main_grad:
+            assert torch.all(layer.main_grad == 2.0)
+        else:
+            assert torch.count_nonzero(layer.weight.grad).item() == 0
+        if layer.bias is not None:
+            assert torch.count_nonzero(layer.bias_main_grad if main_grad else layer.bias.grad).item() == 0
