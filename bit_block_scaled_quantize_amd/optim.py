@@ -9,11 +9,7 @@ from __future__ import annotations
 import torch
 
 from . import AdamWPlan, AdamWTensor, NVFP4Error, adamw
-from .linear import NVFP4Linear
-
-
-def _version(p):
-    return 0 if p.is_inference() else p._version
+from .linear import NVFP4Linear, _state_of
 
 
 class AdamW:
@@ -35,7 +31,8 @@ class AdamW:
         self.lr, self.betas, self.eps, self.max_norm, self.seed = lr, betas, eps, max_norm, seed
         self.states, self.steps = states, 0
         self.params, self.grads, self.masters, tensors = [], [], [], []
-        self._held = []                                      # (owner, attribute, the tensor it has to stay)
+        self._sources = []                                   # (parameter as given, its address)
+        self._held = []                                      # (owner of a gradient, attribute, its address)
         for entry in entries:
             param, grad, *decay = entry
             p = param.detach()
@@ -48,23 +45,29 @@ class AdamW:
                                        w_out=p if p.dtype == torch.bfloat16 else None, **self._state(p)))
             self.params.append(p)
             self.grads.append(grad)
-            self._held.append((param, "data", p))
+            self._sources.append((param, p.data_ptr()))
             if param.is_leaf and param.grad is grad:
-                self._held.append((param, "grad", grad))
+                self._held.append((param, "grad", grad.data_ptr()))
             self.masters.append(master)
         self.plan = AdamWPlan(tensors)
         self.amax = torch.zeros((len(tensors),), dtype=torch.float32, device=self.plan.device)
         self._layers = list(layers)                          # (index of the weight, layer)
+        self._amaxes = [(self.amax[i:i + 1], self.params[i], layer) for i, layer in self._layers]
         self._mains = []                                     # (parameter, its main gradient)
-        self._seen = [_version(p) for p in self.params]
+        self._counted = [p for p in self.params if not p.is_inference()]     # torch counts their changes
+        self._followed = [(p, m) for p, m in zip(self.params, self.masters) if p is not m and not p.is_inference()]
+        self._see()
+
+    def _see(self):
+        self._seen = [p._version for p, _ in self._followed]
 
     def _follow_parameters(self):
         """Masters of parameters that changed since the last step: where the BF16 value is no longer the
         master's, the parameter's."""
-        for i, (p, m) in enumerate(zip(self.params, self.masters)):
-            if p is not m and _version(p) != self._seen[i]:
+        for (p, m), seen in zip(self._followed, self._seen):
+            if p._version != seen:
                 m.copy_(torch.where(p == m.bfloat16(), m, p.float()))
-                self._seen[i] = _version(p)
+        self._see()
 
     def _state(self, p):
         n, dev = p.numel(), p.device
@@ -95,7 +98,7 @@ class AdamW:
                 elif grad is not entries[at[id(p)]][1]:
                     entries[at[id(p)]][1].add_(grad)
                     setattr(m, main, entries[at[id(p)]][1])
-                held.append((m, main, entries[at[id(p)]][1]))
+                held.append((m, main, entries[at[id(p)]][1].data_ptr()))
                 if name == "weight":
                     layers.append((at[id(p)], m))
         mains = [(p, grad) for p, grad, _ in entries]
@@ -113,11 +116,13 @@ class AdamW:
     def step(self, lr: float | None = None):
         """One step; returns the gradients' norm with max_norm, else None. The kernel reads and writes
         the buffers that the optimizer was made with: one that has been replaced since is an error."""
-        for owner, name, buffer in self._held:
+        for param, address in self._sources:
+            if param.data_ptr() != address:
+                self._moved(param, "data")
+        for owner, name, address in self._held:
             now = getattr(owner, name)
-            if now is None or now.data_ptr() != buffer.data_ptr():
-                raise NVFP4Error(f"the {name} of {type(owner).__name__} {tuple(buffer.shape)} has moved since the optimizer "
-                                 f"was made: clear gradients with its zero_grad, make it anew after moving parameters")
+            if now is None or now.data_ptr() != address:
+                self._moved(owner, name)
         for p, main in self._mains:
             if p.grad is not None:                           # of a use without the main gradient
                 main.add_(p.grad)
@@ -127,11 +132,16 @@ class AdamW:
                      max_norm=self.max_norm, seed=self.seed, amax_out=self.amax)
         self.steps += 1
         # the kernel wrote them: autograd and the layers are to see it
-        torch.autograd.graph.increment_version([p for p in self.params if not p.is_inference()])
-        self._seen = [_version(p) for p in self.params]
-        for i, layer in self._layers:
-            layer.weight_amax = self.amax[i:i + 1]
+        torch.autograd.graph.increment_version(self._counted)
+        self._see()
+        for amax, param, layer in self._amaxes:
+            layer.__dict__["_weight_amax"] = amax, _state_of(param)       # layer.weight_amax, without Module's ways
         return norm
+
+    @staticmethod
+    def _moved(owner, name):
+        raise NVFP4Error(f"the {name} of a {type(owner).__name__} has moved since the optimizer was made: clear gradients with "
+                         f"its zero_grad, and make it anew after moving parameters")
 
     def zero_grad(self):
         torch._foreach_zero_(self.grads)
@@ -158,7 +168,7 @@ class AdamW:
         for p, m in zip(self.params, self.masters):
             if p is not m:
                 p.copy_(m)
-        self._seen = [_version(p) for p in self.params]
+        self._see()
         for _, layer in self._layers:
             layer.weight_amax = None                         # of the weights before
         self.steps, self.seed = state["steps"], state["seed"]
