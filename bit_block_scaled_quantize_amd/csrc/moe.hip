@@ -10,12 +10,12 @@
 //  1. k_route: logits (a wave per expert, 8 tokens at a time), x in FP16; the last workgroup of a
 //     token group to finish picks its tokens' experts, the last group to finish sorts the
 //     (token, expert) pairs by expert.
-//  2. k_expert<UP>: 32 rows (gated: 16 of each half) of one used expert times its tokens (skinny.h), the
-//     activation, h.
-//  3. k_expert<DOWN>: 32 or 64 rows of W2 likewise, the routing weight, one partial result per pair.
+//  2. k_expert<UP>: 32 rows (gated: 16 of each half; for one token 16) of one used expert times its tokens
+//     (skinny.h), the activation, h.
+//  3. k_expert<DOWN>: 16, 32 or 64 rows of W2 likewise, the routing weight, one partial result per pair.
 //  4. y, the k partials of each token added in order: up to 4 tokens by the last workgroup of a row tile
 //     to finish, beyond by k_join (there is so much to add that those workgroups would be the launch's tail).
-// Measured (that layer, us): 1 token 7.9 + 8.9 + 9.4 (the weights at 1.9 TB/s in the products: 17 MB each is
+// Measured (that layer, us): 1 token 8.0 + 8.0 + 8.6 (the weights at 2 TB/s in the products: 17 MB each is
 // 4 us of reading behind a launch's 3 us and the round trips to the routing, x and the weights); 64 tokens 17 +
 // 95 + 96 + 5 (3.6 TB/s). Routing one token is latency: the logits, the counter, the picks one after the other.
 // "The last to finish" is found with a counter that the last one resets: nothing waits for
@@ -608,10 +608,10 @@ template <bool UP, bool GATED, Shape S>
 hipError_t launch_expert_k(const MoeArgs& a, const MoeWork& w, hipStream_t stream) {
   // (us on 122 experts of 2688 x 1856, 64 tokens: up R = 2 with A = 1, 2, 3: 95, 95, 93, R = 4: 98; down
   // R = 2: 108 with A = 1, 110 with 2; R = 4: 96 with A = 1, 115 with 2. Few tokens, the whole layer of 128
-  // experts: R = 2 with A = 2, 3, 4, 5: 1 token 24.3, 24.9, 25.3, 25.5, 4 tokens 51, 58, 62, 64; 8 waves
-  // with A = 2 24.1 and 70, but at 64 tokens down 129 to 140)
+  // experts, weights from HBM: R = 2 with A = 2, 3, 4: 1 token 27.7, 28.1, 28.5, 4 tokens 59, 65, 70; R = 1:
+  // 25.6, 25.6, 25.8 and 68, 69, 69. 8 waves, R = 2, A = 2: 27.1 and 77, but at 64 tokens down 129 to 140)
   constexpr int R = UP ? 2 : 4, A = UP ? 3 : 1;
-  if (a.tokens == 1) return launch_expert_as<UP, GATED, 2, 2, 1, !UP, S>(a, w, stream);
+  if (a.tokens == 1) return launch_expert_as<UP, GATED, GATED ? 2 : 1, 2, 1, !UP, S>(a, w, stream);
   if (a.tokens <= kJoinTokens) return launch_expert_as<UP, GATED, 2, 2, kMostCols, !UP, S>(a, w, stream);
   return launch_expert_as<UP, GATED, R, A, kMostCols, false, S>(a, w, stream);
 }
