@@ -7,7 +7,7 @@
 // Bound by reading each chosen expert's weights once (9/16 byte per element): 1 token with 6 of
 // 128 experts of 2688 x 1856 reads 34 MB, 64 tokens read most of the 718 MB. Three launches, or four, each
 // depending on all of the one before:
-//  1. k_route: logits (a wave per expert, 8 tokens at a time), x in FP16; the last workgroup of a
+//  1. k_route: logits (4 experts and 8 tokens a workgroup), x in FP16; the last workgroup of a
 //     token group to finish picks its tokens' experts, the last group to finish sorts the
 //     (token, expert) pairs by expert.
 //  2. k_expert<UP>: 32 rows (gated: 16 of each half; for one token 16) of one used expert times its tokens
