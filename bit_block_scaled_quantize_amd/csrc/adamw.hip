@@ -31,8 +31,8 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPer = 8;                                       // elements per thread
-static_assert(kAdamWChunk == kThreads * kPer, "a workgroup takes a chunk");
+constexpr int kPer = 8;                                       // elements per thread and pass
+constexpr int64_t kPass = (int64_t)kThreads * kPer;
 
 struct Elems { float v[kPer]; };
 
@@ -209,12 +209,15 @@ __global__ __launch_bounds__(kThreads) void k_grad_norm(const AdamWEntry* __rest
     const AdamWEntry& t = table[chunk_of[c]];
     const int64_t n = t.n, c0 = (c - t.first_chunk) * kAdamWChunk;
     const bool bf16 = t.flags & kAdamWGradBf16;
-    const int64_t i = c0 + (int64_t)threadIdx.x * kPer;
     float s = 0.0f;
-    if (i < n) {
-      const Elems g = load_grad(t.grad, bf16, i, n);
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) s += g.v[q] * g.v[q];
+    for (int64_t o = 0; o < kAdamWChunk; o += kPass) {
+      const int64_t i = c0 + o + (int64_t)threadIdx.x * kPer;
+      if (i < n) {
+        const Elems g = load_grad(t.grad, bf16, i, n);
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) s += g.v[q] * g.v[q];
+      }
     }
     sum += (double)s;
   }
@@ -243,64 +246,69 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const AdamWEntry* __restrict
   }
   const float shrink = 1.0f - hp.lr * t.weight_decay;
   float mx = 0.0f;
-  const int64_t i = c0 + (int64_t)threadIdx.x * kPer;         // lanes past n carry zeros to the shuffles
-  Elems p = load_f32(t.p, i, n);
-  const Elems grad = load_grad(t.grad, bf16, i, n);
-  Elems m, v;
-  Codes mc{0, 0}, rc{0, 0};
-  uint32_t ms = 0, rs = 0;
-  if constexpr (EIGHT) {
-    mc = load_codes(static_cast<const uint8_t*>(t.m), i, n);
-    rc = load_codes(static_cast<const uint8_t*>(t.v), i, n);
-    if (i < n) {
-      ms = t.m_scale[i >> 5];
-      rs = t.v_scale[i >> 5];
-    }
-    m = decode_codes(mc, e8m0_value(ms));
-    v = decode_codes(rc, e8m0_value(rs));
-  } else {
-    m = load_f32(static_cast<const float*>(t.m), i, n);
-    v = load_f32(static_cast<const float*>(t.v), i, n);
-  }
-  if (!skip) {
-    Elems r;
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      const float g = parts > 0 ? grad.v[q] * clip : grad.v[q];
-      const float v0 = EIGHT ? v.v[q] * v.v[q] : v.v[q];
-      m.v[q] = hp.beta1 * m.v[q] + hp.one_beta1 * g;
-      v.v[q] = hp.beta2 * v0 + hp.one_beta2 * (g * g);
-      r.v[q] = sqrtf(v.v[q]);
-      const float denom = r.v[q] * hp.inv_sqrt_bc2 + hp.eps;
-      p.v[q] = p.v[q] * shrink - hp.step_size * (m.v[q] / denom);
-    }
+#pragma unroll 1
+  for (int64_t o = 0; o < kAdamWChunk && c0 + o < n; o += kPass) {
+    const int64_t i = c0 + o + (int64_t)threadIdx.x * kPer;   // lanes past n carry zeros to the shuffles
+    Elems p = load_f32(t.p, i, n);
+    const Elems grad = load_grad(t.grad, bf16, i, n);
+    Elems m, v;
+    Codes mc{0, 0}, rc{0, 0};
+    uint32_t ms = 0, rs = 0;
     if constexpr (EIGHT) {
-      const uint64_t grp = (uint64_t)i >> 3;
-      const u32x4 rnd = philox4x32_10(u32x4{(uint32_t)grp, (uint32_t)(grp >> 32), hp.step, (uint32_t)ti},
-                                      (uint32_t)hp.seed, (uint32_t)(hp.seed >> 32));
-      // (elements past n are 0 in m and r: they do not count towards their block's maximum)
-      mc = encode_codes<false>(m, rnd, ms);
-      rc = encode_codes<true>(r, rnd, rs);
-    }
-  }
-  if (i < n) {
-    store_f32(t.p_out, i, n, p);
-    if (t.w_out != nullptr) {
-      mx = store_bf16(t.w_out, i, n, p);
-    } else {
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) mx = fmaxf(mx, fabsf(p.v[q]));
-    }
-    if constexpr (EIGHT) {
-      store_codes(static_cast<uint8_t*>(t.m_out), i, n, mc);
-      store_codes(static_cast<uint8_t*>(t.v_out), i, n, rc);
-      if ((i & 31) == 0) {
-        t.m_scale_out[i >> 5] = (uint8_t)ms;
-        t.v_scale_out[i >> 5] = (uint8_t)rs;
+      mc = load_codes(static_cast<const uint8_t*>(t.m), i, n);
+      rc = load_codes(static_cast<const uint8_t*>(t.v), i, n);
+      if (i < n) {
+        ms = t.m_scale[i >> 5];
+        rs = t.v_scale[i >> 5];
       }
+      m = decode_codes(mc, e8m0_value(ms));
+      v = decode_codes(rc, e8m0_value(rs));
     } else {
-      store_f32(static_cast<float*>(t.m_out), i, n, m);
-      store_f32(static_cast<float*>(t.v_out), i, n, v);
+      m = load_f32(static_cast<const float*>(t.m), i, n);
+      v = load_f32(static_cast<const float*>(t.v), i, n);
+    }
+    if (!skip) {
+      Elems r;
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        const float g = parts > 0 ? grad.v[q] * clip : grad.v[q];
+        const float v0 = EIGHT ? v.v[q] * v.v[q] : v.v[q];
+        m.v[q] = hp.beta1 * m.v[q] + hp.one_beta1 * g;
+        v.v[q] = hp.beta2 * v0 + hp.one_beta2 * (g * g);
+        r.v[q] = sqrtf(v.v[q]);
+        const float denom = r.v[q] * hp.inv_sqrt_bc2 + hp.eps;
+        p.v[q] = p.v[q] * shrink - hp.step_size * (m.v[q] / denom);
+      }
+      if constexpr (EIGHT) {
+        const uint64_t grp = (uint64_t)i >> 3;
+        const u32x4 rnd = philox4x32_10(u32x4{(uint32_t)grp, (uint32_t)(grp >> 32), hp.step, (uint32_t)ti},
+                                        (uint32_t)hp.seed, (uint32_t)(hp.seed >> 32));
+        // (elements past n are 0 in m and r: they do not count towards their block's maximum)
+        mc = encode_codes<false>(m, rnd, ms);
+        rc = encode_codes<true>(r, rnd, rs);
+      }
+    }
+    if (i < n) {
+      store_f32(t.p_out, i, n, p);
+      float big = 0.0f;
+      if (t.w_out != nullptr) {
+        big = store_bf16(t.w_out, i, n, p);
+      } else {
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) big = fmaxf(big, fabsf(p.v[q]));
+      }
+      mx = fmaxf(mx, big);
+      if constexpr (EIGHT) {
+        store_codes(static_cast<uint8_t*>(t.m_out), i, n, mc);
+        store_codes(static_cast<uint8_t*>(t.v_out), i, n, rc);
+        if ((i & 31) == 0) {
+          t.m_scale_out[i >> 5] = (uint8_t)ms;
+          t.v_scale_out[i >> 5] = (uint8_t)rs;
+        }
+      } else {
+        store_f32(static_cast<float*>(t.m_out), i, n, m);
+        store_f32(static_cast<float*>(t.v_out), i, n, v);
+      }
     }
   }
   if (amax_out != nullptr) {                                  // uniform
