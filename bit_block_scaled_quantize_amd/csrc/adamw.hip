@@ -33,6 +33,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPer = 8;                                       // elements per thread and pass
 constexpr int64_t kPass = (int64_t)kThreads * kPer;
+static_assert(kAdamWChunk % kPass == 0, "a workgroup takes a chunk in whole passes");
 
 struct Elems { float v[kPer]; };
 
@@ -246,6 +247,8 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const AdamWEntry* __restrict
   }
   const float shrink = 1.0f - hp.lr * t.weight_decay;
   float mx = 0.0f;
+  // one pass, and a loop all the same: ahead of it the compiler asks for the entry's pointers together, without
+  // it one after the other (a dozen tensors of 1 to 20480 elements 4.2 us, 4.9 without the loop)
 #pragma unroll 1
   for (int64_t o = 0; o < kAdamWChunk && c0 + o < n; o += kPass) {
     const int64_t i = c0 + o + (int64_t)threadIdx.x * kPer;   // lanes past n carry zeros to the shuffles
