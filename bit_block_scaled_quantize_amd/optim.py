@@ -33,6 +33,7 @@ class AdamW:
         self.params, self.grads, self.masters, tensors = [], [], [], []
         self._sources = []                                   # (parameter as given, its address)
         self._held = []                                      # (owner of a gradient, attribute, its address)
+        named = set()
         for entry in entries:
             param, grad, *decay = entry
             p = param.detach()
@@ -40,6 +41,9 @@ class AdamW:
                 raise NVFP4Error("parameters must be contiguous bfloat16 or float32 tensors")
             if grad is None or grad.shape != p.shape:
                 raise NVFP4Error("every parameter needs a gradient of its shape that stays where it is")
+            if p.numel() and p.data_ptr() in named:
+                raise NVFP4Error("a parameter is named twice: give it one entry, with the sum of its gradients")
+            named.add(p.data_ptr())
             master = p.float() if p.dtype == torch.bfloat16 else p
             tensors.append(AdamWTensor(p=master, grad=grad, weight_decay=decay[0] if decay else weight_decay,
                                        w_out=p if p.dtype == torch.bfloat16 else None, **self._state(p)))

@@ -411,3 +411,13 @@ def test_a_refused_step_is_not_counted(monkeypatch):
     with pytest.raises(nv.NVFP4Error):
         opt.step(lr=float("nan"))
     assert opt.steps == 1
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_parameter_named_twice_is_refused(dtype):
+    """Two entries of one tensor would step it twice at once, or from two masters."""
+    p = torch.nn.Parameter(torch.ones(8, dtype=dtype))
+    with pytest.raises(nv.NVFP4Error, match="twice"):
+        AdamW([(p, torch.ones(8)), (p, torch.ones(8))])
+    empty = torch.nn.Parameter(torch.ones(0, dtype=dtype))
+    AdamW([(empty, torch.ones(0)), (torch.nn.Parameter(torch.ones(0)), torch.ones(0)), (p, torch.ones(8))])
