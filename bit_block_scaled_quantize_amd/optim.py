@@ -32,6 +32,7 @@ class AdamW:
         self.states, self.steps = states, 0
         self.params, self.grads, self.masters, tensors = [], [], [], []
         self._sources = []                                   # (parameter as given, its address)
+        self._places = []                                    # (a layer's parameters, name, its address)
         self._held = []                                      # (owner of a gradient, attribute, its address)
         named = set()
         for entry in entries:
@@ -88,7 +89,7 @@ class AdamW:
         class, not set_to_none). A parameter that several layers share is stepped once, with all of
         their gradients: the layers share one main gradient from here on, and what other uses of the
         parameter leave in its .grad is added there by step()."""
-        entries, layers, held, at = [], [], [], {}
+        entries, layers, held, places, at = [], [], [], [], {}
         for m in module.modules():
             if not isinstance(m, NVFP4Linear):
                 continue
@@ -102,6 +103,7 @@ class AdamW:
                 elif grad is not entries[at[id(p)]][1]:
                     entries[at[id(p)]][1].add_(grad)
                     setattr(m, main, entries[at[id(p)]][1])
+                places.append((m._parameters, name, p.data_ptr()))
                 held.append((m, main, entries[at[id(p)]][1].data_ptr()))
                 if name == "weight":
                     layers.append((at[id(p)], m))
@@ -115,6 +117,7 @@ class AdamW:
         opt = cls(entries, weight_decay=weight_decay, layers=layers, **kw)
         opt._mains = mains
         opt._held += held
+        opt._places += places
         return opt
 
     def step(self, lr: float | None = None):
@@ -122,11 +125,15 @@ class AdamW:
         the buffers that the optimizer was made with: one that has been replaced since is an error."""
         for param, address in self._sources:
             if param.data_ptr() != address:
-                self._moved(param, "data")
+                self._moved("data of a parameter")
+        for parameters, name, address in self._places:
+            now = parameters.get(name)
+            if now is None or now.data_ptr() != address:
+                self._moved(f"{name} of a layer")
         for owner, name, address in self._held:
             now = getattr(owner, name)
             if now is None or now.data_ptr() != address:
-                self._moved(owner, name)
+                self._moved(f"{name} of a {type(owner).__name__}")
         for p, main in self._mains:
             if p.grad is not None:                           # of a use without the main gradient
                 main.add_(p.grad)
@@ -143,9 +150,9 @@ class AdamW:
         return norm
 
     @staticmethod
-    def _moved(owner, name):
-        raise NVFP4Error(f"the {name} of a {type(owner).__name__} has moved since the optimizer was made: clear gradients with "
-                         f"its zero_grad, and make it anew after moving parameters")
+    def _moved(what):
+        raise NVFP4Error(f"the {what} has moved since the optimizer was made: clear gradients with its zero_grad, and make "
+                         f"it anew after moving parameters")
 
     def zero_grad(self):
         torch._foreach_zero_(self.grads)

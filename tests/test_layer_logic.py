@@ -421,3 +421,15 @@ def test_a_parameter_named_twice_is_refused(dtype):
         AdamW([(p, torch.ones(8)), (p, torch.ones(8))])
     empty = torch.nn.Parameter(torch.ones(0, dtype=dtype))
     AdamW([(empty, torch.ones(0)), (torch.nn.Parameter(torch.ones(0)), torch.ones(0)), (p, torch.ones(8))])
+
+
+@pytest.mark.parametrize("name", ["weight", "bias"])
+def test_a_step_of_a_parameter_that_its_layer_no_longer_has_is_refused(name):
+    """load_state_dict(assign=True) and the like put other parameters in the layer's place."""
+    layer = _layer(32, 32, 16, bias=True)
+    opt = AdamW.of(layer)
+    opt.step()
+    layer.load_state_dict({k: v.clone() if k == name else v for k, v in layer.state_dict(keep_vars=True).items()}, assign=True)
+    with pytest.raises(nv.NVFP4Error, match=f"{name}.*moved"):
+        opt.step()
+    assert opt.steps == 1
