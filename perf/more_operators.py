@@ -106,7 +106,6 @@ def prepare(case, seed):
         st["x"] = _outliers(g, _randn(g, (case["m"], case["n"]))).to(_DT[case["dt"]])
     elif op == "rht8":
         st["x8"] = _to_fp8(_outliers(g, _randn(g, (case["m"], case["n"]))))
-        st["pairs"] = _e2m1_pairs()
     elif op == "act_grad8":
         m, n = case["m"], case["n"]
         st["dy"] = _randn(g, (m, n), 1e-3).to(_DT[case["dy"]])
@@ -200,8 +199,7 @@ def _views(q):
 def _own_rht8(st):
     import bit_block_scaled_quantize_amd as nv
     q = nv.rht_quantize(_fp8(nv, st["x8"]), SIGN_MASK, "rn")
-    values = torch.index_select(st["pairs"], 0, q.codes.reshape(-1).int())
-    return {"values": values.view(torch.float8_e4m3fn).reshape(q.rows, q.cols), "scales": q.scales.view(torch.float8_e4m3fn), "global": q.global_scale}
+    return {"values": _e2m1_values(q.codes), "scales": q.scales.view(torch.float8_e4m3fn), "global": q.global_scale}
 
 
 def _own_act_grad8(st):
@@ -298,11 +296,10 @@ def _hadamard16():
 _GRID = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
 
 
-def _e2m1_pairs():
-    """Byte of two packed E2M1 codes -> the two values that they stand for (exact in E4M3), as one 16-bit word."""
-    lut = torch.tensor(_GRID + [-x for x in _GRID], device=DEV).to(torch.float8_e4m3fn).view(torch.uint8).int()
-    byte = torch.arange(256, device=DEV)
-    return (lut[byte & 15] | (lut[byte >> 4] << 8)).to(torch.uint16).view(torch.int16)
+def _e2m1_values(codes):
+    """Packed E2M1 codes [r, c/2] as the values [r, c] that they stand for (exact in E4M3)."""
+    lut = torch.tensor(_GRID + [-x for x in _GRID], device=codes.device).to(torch.float8_e4m3fn).view(torch.uint8)
+    return torch.stack([lut[(codes & 15).long()], lut[(codes >> 4).long()]], -1).reshape(codes.shape[0], -1).view(torch.float8_e4m3fn)
 
 
 def _plain_rht8(st):
