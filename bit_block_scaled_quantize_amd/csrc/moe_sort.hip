@@ -16,6 +16,7 @@
 // 4.1 TB/s), combined in 225 us (FP32, 1.15 GB, 5.1 TB/s), the gradient in 333 (1.69 GB, 5.1 TB/s).
 #include "eight.h"
 #include "launch.h"
+#include "moe_layout.h"
 
 namespace nvfp4 {
 namespace {
@@ -88,7 +89,7 @@ __device__ __forceinline__ void lay_out(const int* total, int* start, int expert
   static_assert(kMoeSortMaxExperts <= kSortThreads, "an expert each");
   __shared__ int sums[kSortWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = threadIdx.x;
-  const int mine = e < experts ? (total[e] + align - 1) / align * align : 0;
+  const int mine = e < experts ? padded_run(total[e], align) : 0;
   int upto = mine;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -114,7 +115,7 @@ __device__ __forceinline__ void mark(const int* total, const int* start, int exp
   if (part == 0)
     for (int e = threadIdx.x; e <= experts; e += kSortThreads) offsets[e] = start[e];
   for (int e = part * kSortWaves + wave; e < experts; e += parts * kSortWaves)
-    for (int r = start[e] + total[e] + lane; r < start[e + 1]; r += 64) pair_of[r] = -1;
+    each_64th(start[e] + total[e], start[e + 1], lane, [&](int64_t r) { pair_of[r] = -1; });
   for (int64_t r = start[experts] + (int64_t)part * kSortThreads + threadIdx.x; r < rows; r += (int64_t)parts * kSortThreads) pair_of[r] = -1;
 }
 

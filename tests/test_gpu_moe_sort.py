@@ -236,3 +236,17 @@ def test_rows_of_many(t, k, h, dt):
     square = xf.square().sum(1)[:, None].expand(t, k)
     bound = (h / 64 + 16) * 2.0 ** -24 * square
     assert bool(((dw.double() - torch.where(s.row_of >= 0, square, 0.0)).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("e,align", [(1, 2 ** 31 - 1), (2, 2 ** 30 - 1)])
+def test_runs_that_end_at_the_last_row_there_is(e, align):
+    """Rows up to 2^31 - 1: a count and its alignment together, and a row and the next one of its lane, are more."""
+    log(f"moe_sort of {e}, align {align}")
+    ids = torch.tensor([[e - 1], [0], [-1], [e - 1]], dtype=torch.int32, device="cuda")
+    s = nv.moe_sort(ids, e, align)
+    want = {1: ([0, align], [0, 1, -1, 2], {0: 0, 1: 1, 2: 3}), 2: ([0, align, 2 * align], [align, 0, -1, align + 1], {0: 1, align: 0, align + 1: 3})}[e]
+    assert s.offsets.tolist() == want[0] and s.rows == want[0][-1] and s.row_of.reshape(-1).tolist() == want[1]
+    for row, pair in want[2].items():
+        assert int(s.pair_of[row]) == pair
+        s.pair_of[row] = -1
+    assert int(s.pair_of.min()) == int(s.pair_of.max()) == -1
