@@ -5,8 +5,10 @@
 // x [T, H] and W [V, H] in BF16, products and sums in FP32; a target outside 0 .. V - 1 does not count: loss 0, G 0.
 //
 // Forward: one product in tiles of W's rows times tokens. A lane of a finished tile holds one token's logits for its
-// rows, so the tile leaves the maximum and the sum of exp(l - maximum) of each of its tokens, and the logit of a
-// token whose target lies in it; k_merge joins the tiles' pairs. Backward: the logits are computed again, a piece of
+// rows, so the tile leaves the maximum and the sum of exp(l - maximum) of each of its tokens without their targets, and the logit of a
+// token whose target lies in it. k_merge joins the tiles' pairs: with d = log(sum over the other words of exp(l - l[target])) the loss is
+// log(1 + exp(d)), which keeps the digits of a small loss (as lse - l[target], two numbers rounded at their size, a loss of 1e-6 at
+// logits of 25 was all rounding). Backward: the logits are computed again, a piece of
 // the vocabulary at a time, and leave the product as G in BF16 (8 bits of G's own size: as much as the BF16
 // gradients that follow keep). The target's G, mostly a token's largest by far, keeps what BF16 leaves of it in FP32: dx gets
 // it when its shares are joined, dW from the tile that holds the word. dW's rows of the piece are G^T x, and dx grows by G W in FP32, rounded once
@@ -81,7 +83,7 @@ enum Epilogue : int { kLse = 0, kGrad = 1, kStoreBf16 = 2, kStoreF32 = 3, kAddF3
 struct Out {
   // kLse: A is W (m a word), B is x (n a token)
   const int64_t* targets;
-  float* part;                  // [tiles of m * waves of m][2][tokens]: maximum, sum
+  float* part;                  // [tiles of m * waves of m][2][tokens]: maximum, sum, of the words that are not the token's target
   float* picked;                // [tokens]: the target's logit
   // kGrad: likewise; d [tokens, ld] BF16
   const float *lse, *grad;
@@ -398,6 +400,18 @@ __global__ __launch_bounds__(kThreads, C::kAtOnce) void k_product(Rows A, Rows B
     for (int i = 0; i < TM; ++i) asm volatile("" : "+a"(acc[i][j]));
     const int64_t n = nw + 16 * j + lane_n;
     if constexpr (EPI == kLse) {
+      const int64_t word = n < B.rows ? o.targets[n] - mw : -1;
+      const int at = word >= 0 && word < rows ? (int)word : -1;
+      if (__ballot(at >= 0)) {                                // few tiles hold a target of their tokens
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (at >= 0 && at - lane_m == 16 * i + r) {
+              o.picked[n] = acc[i][j][r];
+              acc[i][j][r] = -INFINITY;
+            }
+      }
       float top = -INFINITY, sum = 0.0f;
       auto pass = [&](auto whole) {
         auto value = [&](int i, int r) { return decltype(whole)::value || 16 * i + lane_m + r < rows ? acc[i][j][r] : -INFINITY; };
@@ -407,11 +421,11 @@ __global__ __launch_bounds__(kThreads, C::kAtOnce) void k_product(Rows A, Rows B
           for (int r = 0; r < 4; ++r) top = fmaxf(top, value(i, r));
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float base = top == -INFINITY ? 0.0f : top * kLog2e;
+        const float base = top == -INFINITY ? 0.0f : top;
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(value(i, r), kLog2e, -base));
+          for (int r = 0; r < 4; ++r) sum += __builtin_amdgcn_exp2f((value(i, r) - base) * kLog2e);
       };
       if (rows == C::kWaveM) pass(std::true_type{});
       else pass(std::false_type{});
@@ -421,15 +435,6 @@ __global__ __launch_bounds__(kThreads, C::kAtOnce) void k_product(Rows A, Rows B
         float* part = o.part + (tm * C::kWavesM + wave / C::kWavesN) * 2 * B.rows + n;
         part[0] = top;
         part[B.rows] = sum;
-      }
-      const int64_t word = n < B.rows ? o.targets[n] - mw : -1;
-      const int at = word >= 0 && word < rows ? (int)word : -1;
-      if (__ballot(at >= 0)) {                                // few tiles hold a target of their tokens
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (at >= 0 && at - lane_m == 16 * i + r) o.picked[n] = acc[i][j][r];
       }
     } else if constexpr (kPacked) {
       float lse = 0.0f, gr = 0.0f;
@@ -498,7 +503,7 @@ __global__ __launch_bounds__(kMergeWaves * 64) void k_merge(const float* __restr
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, column = lane & (kMergeTokens - 1);
   const int64_t t = (int64_t)blockIdx.x * kMergeTokens + column;
   float top = -INFINITY, sum = 0.0f;
-  // sum exp(top) with another pair: a pair of rows past the vocabulary is (-inf, 0)
+  // sum exp(top) with another pair: a pair of no words (past the vocabulary, the target alone) is (-inf, 0)
   auto join = [](float& top, float& sum, float m, float s) {
     const float to = fmaxf(top, m), base = to == -INFINITY ? 0.0f : to;
     sum = sum * __builtin_amdgcn_exp2f((top - base) * kLog2e) + s * __builtin_amdgcn_exp2f((m - base) * kLog2e);
@@ -519,10 +524,15 @@ __global__ __launch_bounds__(kMergeWaves * 64) void k_merge(const float* __restr
   if (threadIdx.x < kMergeTokens && t < tokens) {
 #pragma unroll
     for (int w = 1; w < kMergeWaves; ++w) join(top, sum, tops[w][column], sums[w][column]);
-    const float l = top + logf(sum);
-    const int64_t target = targets[t];
+    const float others = top + logf(sum);                     // a token that does not count: of all words
+    float l = others, mine = 0.0f;
+    if ((uint64_t)targets[t] < (uint64_t)vocab) {
+      const float p = picked[t], d = (top - p) + logf(sum), more = log1pf(expf(-fabsf(d)));
+      mine = d > 0.0f ? d + more : p == INFINITY ? NAN : more;
+      l = d > 0.0f ? others + more : p + mine;
+    }
     if (lse) lse[t] = l;
-    if (loss) loss[t] = (uint64_t)target < (uint64_t)vocab ? l - picked[t] : 0.0f;
+    if (loss) loss[t] = mine;
   }
 }
 
