@@ -45,7 +45,7 @@ EXPORTED = ("nvfp4_quantize", "nvfp4_quantize_noalloc", "nvfp4_rht_quantize", "n
             "nvfp4_fp8_quantize", "nvfp4_fp8_dequantize", "nvfp4_rht_quantize_fp8", "nvfp4_act_grad_fp8",
             "nvfp4_rms_norm", "nvfp4_rms_norm_grad", "nvfp4_moe_sorted_rows", "nvfp4_moe_sort", "nvfp4_moe_gather",
             "nvfp4_moe_combine", "nvfp4_moe_combine_grad", "nvfp4_linear_cross_entropy",
-            "nvfp4_linear_cross_entropy_grad")
+            "nvfp4_linear_cross_entropy_grad", "nvfp4_linear_cross_entropy_grad_ex")
 
 
 class NVFP4Error(RuntimeError):
@@ -149,6 +149,7 @@ def _load():
     lib.nvfp4_moe_combine_grad.argtypes = [vp, ci, i64, i64, i64, vp, ci, i64, i64, vp, vp, i64, vp, vp, i64, vp, vp]
     lib.nvfp4_linear_cross_entropy.argtypes = [vp, i64, i64, vp, i64, i64, i64, vp, vp, vp, vp, sz, vp]
     lib.nvfp4_linear_cross_entropy_grad.argtypes = [vp, i64, i64, vp, i64, i64, i64, vp, vp, vp, vp, i64, vp, ci, i64, vp, sz, vp]
+    lib.nvfp4_linear_cross_entropy_grad_ex.argtypes = [vp, i64, i64, vp, i64, i64, i64, vp, vp, vp, vp, vp, i64, vp, ci, i64, vp, sz, vp]
     for name in EXPORTED:
         if name not in ("nvfp4_workspace_size", "nvfp4_last_error", "nvfp4_adamw_table_size", "nvfp4_moe_workspace_size",
                         "nvfp4_moe_sorted_rows"):
@@ -1198,14 +1199,17 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.T
 @_on_stream
 def linear_cross_entropy_grad(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor, grad: torch.Tensor,
                               dx: torch.Tensor | None = None, dweight: torch.Tensor | None = None, accumulate: bool = False,
-                              need_dx: bool = True, need_dweight: bool = True, workspace: torch.Tensor | None = None, stream=None):
-    """nvfp4_linear_cross_entropy_grad: (dx bfloat16 [tokens, hidden], dweight [vocab, hidden]) from the forward's lse
+                              need_dx: bool = True, need_dweight: bool = True, workspace: torch.Tensor | None = None, stream=None,
+                              loss: torch.Tensor | None = None):
+    """nvfp4_linear_cross_entropy_grad_ex: (dx bfloat16 [tokens, hidden], dweight [vocab, hidden]) from the forward's lse
+    and loss (without it the gradient of tokens that are nearly sure of their target is rounded as lse is)
     and grad (float32 [tokens]), the gradient of each token's loss. dweight is bfloat16 where it is allocated, or
     what is given: bfloat16, or float32, which with accumulate is added to. One that is not needed is None."""
     lib = _load()
     tokens, vocab, hidden = _head_input(x, weight, targets)
     _check_array(lse, tokens, torch.float32, "lse")
     _check_array(grad, tokens, torch.float32, "grad")
+    _check_array(loss, tokens, torch.float32, "loss")
     if need_dx:
         dx = torch.empty((tokens, hidden), dtype=torch.bfloat16, device=x.device) if dx is None else dx
         _check_rows(dx, tokens, hidden, (torch.bfloat16,), "dx")
@@ -1222,9 +1226,9 @@ def linear_cross_entropy_grad(x: torch.Tensor, weight: torch.Tensor, targets: to
         return None, None
     kind = OUT_BF16 if dweight is None or dweight.dtype == torch.bfloat16 else OUT_FP32_ACCUMULATE if accumulate else OUT_FP32
     workspace, ws_n = _ws_for(OP_HEAD_GRAD, tokens, vocab, hidden, workspace, x.device)
-    _same_device("linear_cross_entropy_grad", x, weight, targets, lse, grad, dx, dweight, workspace)
-    _check(lib.nvfp4_linear_cross_entropy_grad(_ptr(x), tokens, _row_stride(x), _ptr(weight), vocab, _row_stride(weight), hidden,
-                                               _ptr(targets), _ptr(lse), _ptr(grad), _ptr(dx), hidden if dx is None else _row_stride(dx),
-                                               _ptr(dweight), kind, hidden if dweight is None else _row_stride(dweight), _ptr(workspace),
-                                               ws_n, _stream(stream)))
+    _same_device("linear_cross_entropy_grad", x, weight, targets, lse, loss, grad, dx, dweight, workspace)
+    _check(lib.nvfp4_linear_cross_entropy_grad_ex(_ptr(x), tokens, _row_stride(x), _ptr(weight), vocab, _row_stride(weight), hidden,
+                                                  _ptr(targets), _ptr(lse), _ptr(loss), _ptr(grad), _ptr(dx),
+                                                  hidden if dx is None else _row_stride(dx), _ptr(dweight), kind,
+                                                  hidden if dweight is None else _row_stride(dweight), _ptr(workspace), ws_n, _stream(stream)))
     return dx, dweight

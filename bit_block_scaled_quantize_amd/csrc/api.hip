@@ -1025,9 +1025,10 @@ int nvfp4_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t ldx, c
                     "linear_cross_entropy");
 }
 
-int nvfp4_linear_cross_entropy_grad(const uint16_t* x, int64_t tokens, int64_t ldx, const uint16_t* w, int64_t vocab, int64_t ldw,
-                                    int64_t hidden, const int64_t* targets, const float* lse, const float* grad, uint16_t* dx, int64_t lddx,
-                                    void* dw, nvfp4_out dw_kind, int64_t lddw, void* workspace, size_t ws_bytes, void* hip_stream) {
+int nvfp4_linear_cross_entropy_grad_ex(const uint16_t* x, int64_t tokens, int64_t ldx, const uint16_t* w, int64_t vocab, int64_t ldw,
+                                       int64_t hidden, const int64_t* targets, const float* lse, const float* loss, const float* grad,
+                                       uint16_t* dx, int64_t lddx, void* dw, nvfp4_out dw_kind, int64_t lddw, void* workspace, size_t ws_bytes,
+                                       void* hip_stream) {
   int st;
   if ((st = check_head(x, tokens, ldx, w, vocab, ldw, hidden, targets))) return st;
   if (!dx && !dw && tokens > 0) return fail(NVFP4_ERR_INVALID, "neither dx nor dw given");
@@ -1035,13 +1036,21 @@ int nvfp4_linear_cross_entropy_grad(const uint16_t* x, int64_t tokens, int64_t l
   if (dx && (st = check_matrix(dx, NVFP4_IN_BF16, tokens, hidden, lddx, "dx"))) return st;
   if (dw && (st = check_matrix(dw, dw_kind == NVFP4_OUT_BF16 ? NVFP4_IN_BF16 : NVFP4_IN_FP32, vocab, hidden, lddw, "dw"))) return st;
   if (tokens > 0 && (!lse || !grad || !aligned(lse, 4) || !aligned(grad, 4))) return fail(NVFP4_ERR_INVALID, "lse or grad is NULL or misaligned");
+  if (!aligned(loss, 4)) return fail(NVFP4_ERR_INVALID, "loss is misaligned");
   const size_t need = nvfp4_workspace_size(NVFP4_OP_HEAD_GRAD, tokens, vocab, hidden);
   if (need && (!workspace || ws_bytes < need || !aligned(workspace, kWsAlign)))
     return fail(NVFP4_ERR_WORKSPACE, "workspace of %zu bytes (256-byte aligned) required, got %zu", need, workspace ? ws_bytes : (size_t)0);
   static_assert((int)NVFP4_OUT_FP32 == (int)nvfp4::kHeadF32 && (int)NVFP4_OUT_FP32_ACCUMULATE == (int)nvfp4::kHeadF32Add &&
                 (int)NVFP4_OUT_BF16 == (int)nvfp4::kHeadBf16, "output kinds");
-  return hip_status(nvfp4::launch_head_grad(x, tokens, ldx, w, vocab, ldw, hidden, targets, lse, grad, dx, lddx, dw, (int)dw_kind, lddw,
+  return hip_status(nvfp4::launch_head_grad(x, tokens, ldx, w, vocab, ldw, hidden, targets, lse, loss, grad, dx, lddx, dw, (int)dw_kind, lddw,
                                             workspace, (hipStream_t)hip_stream), "linear_cross_entropy_grad");
+}
+
+int nvfp4_linear_cross_entropy_grad(const uint16_t* x, int64_t tokens, int64_t ldx, const uint16_t* w, int64_t vocab, int64_t ldw,
+                                    int64_t hidden, const int64_t* targets, const float* lse, const float* grad, uint16_t* dx, int64_t lddx,
+                                    void* dw, nvfp4_out dw_kind, int64_t lddw, void* workspace, size_t ws_bytes, void* hip_stream) {
+  return nvfp4_linear_cross_entropy_grad_ex(x, tokens, ldx, w, vocab, ldw, hidden, targets, lse, nullptr, grad, dx, lddx, dw, dw_kind, lddw,
+                                            workspace, ws_bytes, hip_stream);
 }
 
 }  // extern "C"

@@ -1,6 +1,6 @@
 // Softmax cross entropy of a language model's output head, logits l = x W^T never kept:
 //   lse[t] = log sum over v of exp(l[t, v]);   loss[t] = lse[t] - l[t, target[t]]
-//   backward, with the gradient g[t] of each loss:  G[t, v] = g[t] (exp(l[t, v] - lse[t]) - [v = target[t]])
+//   backward, with the gradient g[t] of each loss:  G[t, v] = g[t] exp(l[t, v] - lse[t]),  the target's g[t] (exp(-loss[t]) - 1)
 //   dx = G W,  dW = G^T x
 // x [T, H] and W [V, H] in BF16, products and sums in FP32; a target outside 0 .. V - 1 does not count: loss 0, G 0.
 //
@@ -10,7 +10,8 @@
 // log(1 + exp(d)), which keeps the digits of a small loss (as lse - l[target], two numbers rounded at their size, a loss of 1e-6 at
 // logits of 25 was all rounding). Backward: the logits are computed again, a piece of
 // the vocabulary at a time, and leave the product as G in BF16 (8 bits of G's own size: as much as the BF16
-// gradients that follow keep). The target's G, mostly a token's largest by far, keeps what BF16 leaves of it in FP32: dx gets
+// gradients that follow keep). The target's G comes from the loss, since 1 - exp(l - lse) of a confident token is made of lse's rounding (logits
+// of 25: three times its value off). Mostly a token's largest by far, it keeps what BF16 leaves of it in FP32: dx gets
 // it when its shares are joined, dW from the tile that holds the word. dW's rows of the piece are G^T x, and dx grows by G W in FP32, rounded once
 // after the last piece. Four products in all, 2 T H V operations each: bound by the matrix cores.
 //
@@ -87,6 +88,7 @@ struct Out {
   float* picked;                // [tokens]: the target's logit
   // kGrad: likewise; d [tokens, ld] BF16
   const float *lse, *grad;
+  const float* loss;            // or null: the target's G from its logit and lse
   // of the target's G what BF16 leaves of it [tokens]: kGrad writes it, dW's products add it with x
   float* rest;
   const int *by_word, *start;   // the tokens in the order of their targets; where those of words 128 b begin
@@ -442,10 +444,21 @@ __global__ __launch_bounds__(kThreads, C::kAtOnce) void k_product(Rows A, Rows B
       float own_g = 0.0f;                                     // the target's G
       if constexpr (EPI == kGrad) {
         if (n < B.rows) {
-          lse = o.lse[n] * kLog2e;
+          lse = o.lse[n];
           const int64_t id = o.targets[n], word = id - o.first - mw;
           target = word >= lane_m && word < C::kWaveM ? (int)word - lane_m : -1;
           gr = (uint64_t)id < (uint64_t)o.vocab ? o.grad[n] : 0.0f;   // a token whose target does not count
+        }
+      }
+      float less = 0.0f;                                      // the target's probability - 1
+      if constexpr (EPI == kGrad) {
+        if (__ballot(target >= 0)) {                          // few tiles hold a target of their tokens
+#pragma unroll
+          for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) less = target == 16 * i + r ? acc[i][j][r] - lse : less;
+          if (target >= 0 && o.loss != nullptr) less = -o.loss[n];
+          less = expm1f(less);
         }
       }
 #pragma unroll
@@ -455,8 +468,8 @@ __global__ __launch_bounds__(kThreads, C::kAtOnce) void k_product(Rows A, Rows B
         for (int r = 0; r < 4; ++r) {
           v[r] = acc[i][j][r];
           if constexpr (EPI == kGrad) {
-            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(v[r], kLog2e, -lse));
-            v[r] = gr * (target == 16 * i + r ? p - 1.0f : p);
+            const float p = __builtin_amdgcn_exp2f((v[r] - lse) * kLog2e);
+            v[r] = gr * (target == 16 * i + r ? less : p);
             if (16 * i + r >= rows - lane_m || gr == 0.0f) v[r] = 0.0f;
             if (target == 16 * i + r) own_g = v[r];
           }
@@ -747,7 +760,7 @@ size_t head_grad_workspace_bytes(int64_t T, int64_t V, int64_t H) {
 }
 
 hipError_t launch_head_grad(const uint16_t* x, int64_t T, int64_t ldx, const uint16_t* w, int64_t V, int64_t ldw, int64_t H,
-                            const int64_t* targets, const float* lse, const float* grad, uint16_t* dx, int64_t lddx, void* dw,
+                            const int64_t* targets, const float* lse, const float* loss, const float* grad, uint16_t* dx, int64_t lddx, void* dw,
                             int dw_kind, int64_t lddw, void* ws, hipStream_t stream) {
   if (T == 0) {
     const int64_t size = dw_kind == kHeadBf16 ? 2 : 4;        // H is a multiple of 16
@@ -771,6 +784,7 @@ hipError_t launch_head_grad(const uint16_t* x, int64_t T, int64_t ldx, const uin
     o.targets = targets;
     o.lse = lse;
     o.grad = grad;
+    o.loss = loss;
     o.rest = rest;
     o.first = v0;
     o.vocab = V;

@@ -231,7 +231,7 @@ hipError_t launch_head_loss(const uint16_t* x, int64_t T, int64_t ldx, const uin
                             const int64_t* targets, float* loss, float* lse, void* ws, hipStream_t stream);
 size_t head_grad_workspace_bytes(int64_t T, int64_t V, int64_t H);
 hipError_t launch_head_grad(const uint16_t* x, int64_t T, int64_t ldx, const uint16_t* w, int64_t V, int64_t ldw, int64_t H,
-                            const int64_t* targets, const float* lse, const float* grad, uint16_t* dx, int64_t lddx, void* dw,
+                            const int64_t* targets, const float* lse, const float* loss, const float* grad, uint16_t* dx, int64_t lddx, void* dw,
                             int dw_kind, int64_t lddw, void* ws, hipStream_t stream);
 
 hipError_t launch_grouped_gemm(int64_t G, const int64_t* m_offsets, GemmOperand a, GemmOperand b,

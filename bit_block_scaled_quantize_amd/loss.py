@@ -15,16 +15,17 @@ class _HeadFn(torch.autograd.Function):
     def forward(ctx, x, weight, targets, layer):
         t = x.reshape(-1, x.shape[-1]).contiguous()
         loss, lse = linear_cross_entropy(t, weight, targets)
-        ctx.save_for_backward(t, weight, targets, lse)
+        # a copy: the caller may change the loss that it gets
+        ctx.save_for_backward(t, weight, targets, lse, loss.clone() if any(ctx.needs_input_grad) else loss)
         ctx.layer, ctx.x_shape = layer, x.shape
         return loss
 
     @staticmethod
     def backward(ctx, grad):
-        t, weight, targets, lse = ctx.saved_tensors
+        t, weight, targets, lse, loss = ctx.saved_tensors
         main = ctx.layer.main_grad
         dx, dw = linear_cross_entropy_grad(t, weight, targets, lse, grad.float().contiguous(), dweight=main, accumulate=main is not None,
-                                           need_dx=ctx.needs_input_grad[0], need_dweight=ctx.needs_input_grad[1])
+                                           need_dx=ctx.needs_input_grad[0], need_dweight=ctx.needs_input_grad[1], loss=loss)
         return None if dx is None else dx.view(ctx.x_shape), None if main is not None else dw, None, None
 
 

@@ -709,7 +709,7 @@ int nvfp4_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t ldx, c
 /*
  * nvfp4_linear_cross_entropy_grad - its backward (the same passage). The logits are computed again, in pieces of the
  * vocabulary:
- *   G[t, v] = grad[t] (exp(l[t, v] - lse[t]) - [v = targets[t]]), held in BF16 (the target's, mostly the
+ *   G[t, v] = grad[t] exp(l[t, v] - lse[t]), the target's grad[t] (exp(l - lse) - 1), held in BF16 (the target's, mostly the
  *   largest, with what that leaves of it), 0 for a token that does not count
  *   dx = BF16(G w);   dw = G^T x
  *   lse        the forward's.   grad: device float [tokens], the gradient of each token's loss.
@@ -717,11 +717,19 @@ int nvfp4_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t ldx, c
  *   dw         NULL, or device [vocab, hidden], row stride lddw >= hidden: FP32, FP32 added to what it holds, or BF16
  *              (dw_kind). dx and dw overlap no input.
  *   workspace  nvfp4_workspace_size(NVFP4_OP_HEAD_GRAD, tokens, vocab, hidden) bytes, 256-byte aligned.
- * The result is deterministic. Errors: as nvfp4_linear_cross_entropy.
+ * The result is deterministic. lse is rounded at its size, so the target's G is off by up to 2^-24 |lse| grad: much of it
+ * for a token that is nearly sure of its target; nvfp4_linear_cross_entropy_grad_ex takes the loss too. Errors: as nvfp4_linear_cross_entropy.
  */
 int nvfp4_linear_cross_entropy_grad(const uint16_t* x, int64_t tokens, int64_t ldx, const uint16_t* w, int64_t vocab, int64_t ldw,
                                     int64_t hidden, const int64_t* targets, const float* lse, const float* grad, uint16_t* dx, int64_t lddx,
                                     void* dw, nvfp4_out dw_kind, int64_t lddw, void* workspace, size_t ws_bytes, void* hip_stream);
+
+/* nvfp4_linear_cross_entropy_grad_ex - the same with loss (NULL, or the forward's, device float [tokens]): the target's G is then
+ * grad[t] (exp(-loss[t]) - 1), which keeps its digits however small the loss is (the same passage). Errors as there. */
+int nvfp4_linear_cross_entropy_grad_ex(const uint16_t* x, int64_t tokens, int64_t ldx, const uint16_t* w, int64_t vocab, int64_t ldw,
+                                       int64_t hidden, const int64_t* targets, const float* lse, const float* loss, const float* grad,
+                                       uint16_t* dx, int64_t lddx, void* dw, nvfp4_out dw_kind, int64_t lddw, void* workspace, size_t ws_bytes,
+                                       void* hip_stream);
 
 /* Bytes of device workspace `op` needs for the given shape (0 if none). The library allocates
  * no memory itself (caller-owned buffers, see the conventions above), so the partial maxima of

@@ -105,3 +105,10 @@ def test_head(lib):
     for t in (1, 8192):
         assert lib.nvfp4_workspace_size(nv.OP_HEAD_GRAD, t, 131072, 5120) < 2 << 30
     assert lib.nvfp4_workspace_size(nv.OP_HEAD_GRAD, 0, 100, 64) == 0
+
+
+def test_head_grad_with_the_loss(lib):
+    def g(loss=P, lse=P, dx=P, ws=None, n=0):
+        return lib.nvfp4_linear_cross_entropy_grad_ex(P, 8, 64, P, 100, 64, 64, P, lse, loss, P, dx, 64, P, 2, 64, ws, n, None)
+    assert g(loss=P + 2) == g(lse=None) == g(dx=P + 1) == INVALID
+    assert g() == g(loss=None) == g(ws=P, n=100) == WORKSPACE

@@ -1,15 +1,19 @@
-"""linear_cross_entropy where the target takes nearly all of a token's probability: the loss is a small difference there.
+"""linear_cross_entropy and its gradient where the target takes nearly all of a token's probability: the loss and the target's
+G = grad (p - 1) are small differences there.
 
-The logits are exact (a few bits each, one product a logit), so what is tested is the softmax alone.
+The logits are exact (a few bits each, one product a logit), so what is tested is the softmax alone. Every token has a column of x in
+which dW holds that token's G by itself, and one of w in which dx holds its target's G.
 
 Bounds. With d = log(sum over the others of exp(l - l[target])), loss = log(1 + exp(d)). An exponent l - top is exact or rounded once,
 and its product with log2(e) once (2^-24 of at most 128, each), the exponential itself to 2^-23, the additions of a tile, of the tiles and of the
 joins are some 150, of positive terms (2^-24 each), d is rounded twice at a size below 128 (2^-18 each): exp(d) is within 2^-15 of its value, relative, and so is the loss
-with a few roundings: held to 2^-14."""
+and 1 - p = 1 - exp(-loss), with a few roundings: held to 2^-14. G's other entries: exp(l - lse) with lse rounded (2^-24 of at most 128) and BF16: 2^-8 + 2^-16.
+dx and a BF16 dW: one rounding more, 2^-8; an FP32 dW of the target: its G's BF16 remainder in BF16, 2^-16."""
 import pytest
 import torch
 
 import bit_block_scaled_quantize_amd as nv
+from bit_block_scaled_quantize_amd.loss import LinearCrossEntropy
 from helpers import log
 
 pytestmark = pytest.mark.gpu
@@ -65,6 +69,60 @@ def test_loss_of_confident_tokens(v, h):
     assert not none[0].any() and bool(((none[1] - lse).abs() <= 2.0 ** -16 + 2.0 ** -14 * loss).all())
 
 
+@pytest.mark.parametrize("v,h", [(16, 48), (300, 64), (3001, 48), (70001, 64)])
+def test_gradient_of_confident_tokens(v, h):
+    (x, w, tg, grad), logits = _case(v, h, v)
+    log(f"confident gradient {v} words, hidden {h}")
+    t = x.shape[0]
+    at = torch.arange(t, device="cuda")
+    loss, lse = nv.linear_cross_entropy(x, w, tg)
+    _, G = _want(logits, tg, grad)
+    d32 = torch.empty((v, h), device="cuda")
+    dx, _ = nv.linear_cross_entropy_grad(x, w, tg, lse, grad, dweight=d32, loss=loss)
+    _, dw = nv.linear_cross_entropy_grad(x, w, tg, lse, grad, need_dx=False, loss=loss)
+    own = G[at, tg]
+    got = d32[:, 2:2 + t].double().t()                        # G
+    off = (got[at, tg] - own).abs() / own.abs()
+    assert float(off.max()) <= 2.0 ** -14 + 2.0 ** -15, (off.tolist(), own.tolist())
+    rest = torch.ones_like(G, dtype=torch.bool)
+    rest[at, tg] = False
+    normal = rest & (G.abs() > 2.0 ** -120)
+    assert float(((got - G).abs() / G.abs().clamp_min(1e-300))[normal].max()) <= 2.0 ** -8 + 2.0 ** -15
+    assert bool(((dx[at, 2 + t + at].double() - own).abs() <= (2.0 ** -8 + 2.0 ** -13) * own.abs()).all())
+    b = dw[:, 2:2 + t].double().t()
+    assert bool(((b[at, tg] - own).abs() <= (2.0 ** -8 + 2.0 ** -13) * own.abs()).all())
+
+
+def test_gradient_from_lse_alone():
+    """Without the loss p - 1 comes from the difference to lse: off by what lse was rounded by (half a step at its size) and 2^-14 of
+    itself, but by nothing more."""
+    (x, w, tg, grad), logits = _case(3001, 48, 5)
+    t = x.shape[0]
+    at = torch.arange(t, device="cuda")
+    _, lse = nv.linear_cross_entropy(x, w, tg)
+    d32 = torch.empty((3001, 48), device="cuda")
+    nv.linear_cross_entropy_grad(x, w, tg, lse, grad, dweight=d32, need_dx=False)
+    got = d32[:, 2:2 + t].t()[at, tg].double()
+    # the definition with this lse
+    l = logits[at, tg]
+    want = torch.expm1(l - lse.double()) * grad.double()
+    assert bool(((got - want).abs() <= 2.0 ** -14 * want.abs()).all()), (got.tolist(), want.tolist())
+
+
+def test_module_of_confident_tokens():
+    (x, w, tg, grad), logits = _case(3001, 48, 6)
+    t = x.shape[0]
+    at = torch.arange(t, device="cuda")
+    head = LinearCrossEntropy(48, 3001, device="cuda", reduction="none")
+    head.weight.data.copy_(w)
+    loss = head(x.requires_grad_(), tg)
+    loss.backward(grad)
+    want, G = _want(logits, tg, grad)
+    assert float(((loss.double() - want).abs() / want).max()) <= 2.0 ** -14
+    got = head.main_grad[:, 2:2 + t].t()[at, tg].double()
+    assert bool(((got - G[at, tg]).abs() <= (2.0 ** -14 + 2.0 ** -15) * G[at, tg].abs()).all())
+
+
 def test_one_word_and_words_alike():
     x = torch.randn(33, 32, device="cuda").bfloat16()
     tg = torch.zeros(33, dtype=torch.int64, device="cuda")
@@ -73,6 +131,8 @@ def test_one_word_and_words_alike():
     w = x[:1].expand(5, 32).contiguous()                      # five words alike: log 5 each
     loss, lse = nv.linear_cross_entropy(x, w, tg + 3)
     assert float((loss.double() - torch.log(torch.tensor(5.0, dtype=torch.float64))).abs().max()) <= 2.0 ** -20
+    dx, dw = nv.linear_cross_entropy_grad(x, w, tg + 3, lse, torch.ones(33, device="cuda"), loss=loss)
+    assert torch.isfinite(dx.float()).all() and torch.isfinite(dw.float()).all()
 
 
 def test_infinite_and_huge_logits():
@@ -87,3 +147,26 @@ def test_infinite_and_huge_logits():
     torch.cuda.synchronize()
     assert float(loss[0]) == 0.0 and float(lse[0]) == float((x[0].float() * w[3].float())[0]) and torch.isfinite(lse[0])
     assert not torch.isfinite(loss[1]) and not torch.isfinite(loss[2])
+
+
+def test_refuses_a_loss_of_another_kind():
+    (x, w, tg, grad), _ = _case(40, 48, 1)
+    loss, lse = nv.linear_cross_entropy(x, w, tg)
+    for bad in (loss[:3], loss.double(), loss.cpu()):
+        with pytest.raises(nv.NVFP4Error, match="loss"):
+            nv.linear_cross_entropy_grad(x, w, tg, lse, grad, loss=bad)
+
+
+def test_the_loss_that_a_caller_gets_may_be_changed():
+    (x, w, tg, grad), logits = _case(40, 48, 1)
+    head = LinearCrossEntropy(48, 40, device="cuda", reduction="none", fp32_main_grad=False)
+    head.weight.data.copy_(w)
+    a = head(x.requires_grad_(), tg)
+    a.backward(grad)
+    want = x.grad.clone()
+    x.grad = None
+    b = head(x, tg)
+    b.detach().zero_()
+    b.mul_(2.0)
+    b.backward(grad / 2)
+    assert torch.equal(x.grad, want)
