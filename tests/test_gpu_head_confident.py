@@ -170,3 +170,27 @@ def test_the_loss_that_a_caller_gets_may_be_changed():
     b.mul_(2.0)
     b.backward(grad / 2)
     assert torch.equal(x.grad, want)
+
+
+def test_tokens_that_lean_to_their_targets():
+    """Logits of real products, target logits from 5 to 60. A logit is off by at most e = 1e-5 of its addends' sizes (the library's bound
+    for an FP32 product), a difference of two by 2 e, so the loss and 1 - p by a factor exp(2 e), besides the bounds above."""
+    t, h, v = 60, 256, 3001
+    g = torch.Generator().manual_seed(3)
+    w, tg = torch.randn(v, h, generator=g) * h ** -0.5, torch.randperm(v, generator=g)[:t]
+    x = w[tg] * torch.linspace(5, 60, t)[:, None]
+    x, w = torch.cat([x, torch.eye(t)], 1).bfloat16(), torch.cat([w, torch.zeros(v, t)], 1).bfloat16()
+    x, w = (torch.nn.functional.pad(m, (0, -(h + t) % 16)).cuda() for m in (x, w))
+    tg, grad, at = tg.cuda(), torch.ones(t, device="cuda"), torch.arange(t, device="cuda")
+    logits = x.double() @ w.double().t()
+    want, G = _want(logits, tg, grad)
+    assert float(want.min()) < 1e-9 and float(want.max()) > 1
+    e = 1e-5 * float((x.double().abs() @ w.double().abs().t()).max())
+    rel = float(torch.expm1(torch.tensor(2 * e))) + 2.0 ** -14
+    assert rel < 0.01
+    loss, lse = nv.linear_cross_entropy(x, w, tg)
+    assert bool(((loss.double() - want).abs() <= rel * want).all())
+    d32 = torch.empty(w.shape, device="cuda")
+    nv.linear_cross_entropy_grad(x, w, tg, lse, grad, dweight=d32, need_dx=False, loss=loss)
+    own = G[at, tg]
+    assert bool(((d32[tg, h + at].double() - own).abs() <= (rel + 2.0 ** -15) * own.abs()).all())
