@@ -80,7 +80,8 @@ class _CombineFn(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout):
         y, w = ctx.saved_tensors
-        if dout.dtype not in (torch.bfloat16, torch.float32):
+        # dy leaves the kernel in dout's type: of FP32 rows in FP32, for a pass over dout, which has the fewest rows
+        if dout.dtype not in (torch.bfloat16, torch.float32) or y.dtype == torch.float32:
             dout = dout.float()
         dy, dw = moe_combine_grad(dout.contiguous(), y, ctx.sort, w, need_dy=ctx.needs_input_grad[0],
                                   need_dweights=ctx.needs_input_grad[1])
