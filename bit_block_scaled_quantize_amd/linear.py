@@ -39,6 +39,7 @@ import torch
 
 from . import (ACTIVATIONS, FP8Tensor, NVFP4Error, act_grad, amax, amax_pair, fp8_quantize, gemm_act, gemm_ex, quantize,
                rht_quantize)
+from .first_order import first_order
 
 
 def _state_of(weight):
@@ -112,6 +113,7 @@ class _LinearFn(torch.autograd.Function):
         return y.view(*x.shape[:-1], weight.shape[0])
 
     @staticmethod
+    @first_order
     def backward(ctx, dy):
         t, _ = _saved(ctx)
         if _rows_of(t) == 0:
@@ -196,6 +198,7 @@ class _LinearActFn(torch.autograd.Function):
         return y.view(*x.shape[:-1], weight.shape[0])
 
     @staticmethod
+    @first_order
     def backward(ctx, dy):
         layer = ctx.layer
         t, z = _saved(ctx)

@@ -8,6 +8,7 @@ from __future__ import annotations
 import torch
 
 from . import NVFP4Error, linear_cross_entropy, linear_cross_entropy_grad
+from .first_order import first_order
 
 
 class _HeadFn(torch.autograd.Function):
@@ -21,6 +22,7 @@ class _HeadFn(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @first_order
     def backward(ctx, grad):
         t, weight, targets, lse, loss = ctx.saved_tensors
         main = ctx.layer.main_grad

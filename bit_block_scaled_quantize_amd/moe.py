@@ -12,6 +12,7 @@ import torch
 
 from . import (MoESort, MoEWeights, NVFP4Error, NVFP4Tensor, _moe_call, _on_stream, moe_combine, moe_combine_grad, moe_gather,
                moe_workspace, quantize)
+from .first_order import first_order
 
 
 class MoETokens:
@@ -63,6 +64,7 @@ class _GatherFn(torch.autograd.Function):
         return moe_gather(x.contiguous(), sort)
 
     @staticmethod
+    @first_order
     def backward(ctx, dxs):
         if dxs.dtype not in (torch.bfloat16, torch.float32):
             dxs = dxs.float()
@@ -78,6 +80,7 @@ class _CombineFn(torch.autograd.Function):
         return moe_combine(y, sort, w, out_dtype=out_dtype)
 
     @staticmethod
+    @first_order
     def backward(ctx, dout):
         y, w = ctx.saved_tensors
         # dy leaves the kernel in dout's type: of FP32 rows in FP32, for a pass over dout, which has the fewest rows

@@ -9,6 +9,7 @@ from __future__ import annotations
 import torch
 
 from . import FP8Tensor, NVFP4Error, rms_norm, rms_norm_grad
+from .first_order import first_order
 
 
 class _NormFn(torch.autograd.Function):
@@ -31,6 +32,7 @@ class _NormFn(torch.autograd.Function):
         return y.view(x.shape) if h is None else (y.view(x.shape), h.view(x.shape))
 
     @staticmethod
+    @first_order
     def backward(ctx, dy, dh=None):
         h, weight = ctx.saved_tensors
         dr = None if dh is None else dh.reshape(h.shape).to(h.dtype).contiguous()

@@ -1,9 +1,13 @@
-"""What the step's modules do with gradients at the edges of their use."""
+"""What the step's modules do with gradients at the edges of their use: types that differ between the two sides, second
+derivatives."""
 import pytest
 import torch
 
 import bit_block_scaled_quantize_amd as nv
-from bit_block_scaled_quantize_amd.moe import combine_tokens
+from bit_block_scaled_quantize_amd.linear import NVFP4Linear
+from bit_block_scaled_quantize_amd.loss import LinearCrossEntropy
+from bit_block_scaled_quantize_amd.moe import combine_tokens, gather_tokens
+from bit_block_scaled_quantize_amd.norm import RMSNorm
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +43,59 @@ def test_combine_gradient_in_the_rows_type(y_dtype, out_dtype):
     rows, on = s.row_of.clamp_min(0).long(), (s.row_of >= 0)
     terms = torch.where(on[:, :, None], y.detach().double()[rows], 0.0) * dout.double()[:, None, :]
     assert bool(((w.grad.double() - terms.sum(2)).abs() <= (h / 64 + 16) * 2.0 ** -24 * terms.abs().sum(2)).all())
+
+
+def _second(make):
+    """The gradient of `make()`'s output with respect to its leaf, as a graph, and a penalty on it."""
+    out, leaf = make()
+    first, = torch.autograd.grad(out.float().sum(), leaf, create_graph=True)
+    return first, first.float().square().sum()
+
+
+def _norm():
+    x = _rand(1, 16, 64).bfloat16().requires_grad_()
+    return RMSNorm(64, device="cuda")(x), x
+
+
+def _head():
+    x = _rand(1, 16, 64).bfloat16().requires_grad_()
+    head = LinearCrossEntropy(64, 100, device="cuda")
+    head.weight.data.copy_(_rand(2, 100, 64))
+    return head(x, torch.arange(16, device="cuda")), x
+
+
+def _gather():
+    x = _rand(1, 16, 64).requires_grad_()
+    return gather_tokens(x, nv.moe_sort(torch.zeros((16, 1), dtype=torch.int32, device="cuda"), 2)), x
+
+
+def _combine():
+    s = nv.moe_sort(torch.zeros((16, 1), dtype=torch.int32, device="cuda"), 2)
+    w = torch.rand((16, 1), device="cuda", requires_grad=True)
+    return combine_tokens(_rand(1, s.rows, 64), s, w), w
+
+
+def _linear(**kw):
+    def make():
+        x = _rand(1, 16, 64).bfloat16().requires_grad_()
+        layer = NVFP4Linear(64, 96, device="cuda", **kw)
+        layer.weight.data.copy_(_rand(3, 96, 64, std=0.1))
+        return layer(x), x
+    return make
+
+
+MAKERS = {"norm": _norm, "head": _head, "gather": _gather, "combine": _combine, "linear": _linear(),
+          "linear with activation": _linear(activation="silu", bias=True)}
+
+
+@pytest.mark.parametrize("name", MAKERS)
+def test_second_derivatives_are_refused(name):
+    """A penalty on a gradient raises when it is differentiated, instead of adding nothing; a gradient kept as a graph and not
+    differentiated further is the ordinary one."""
+    first, penalty = _second(MAKERS[name])
+    out, leaf = MAKERS[name]()
+    if name != "combine":                                     # its weights differ from call to call
+        plain, = torch.autograd.grad(out.float().sum(), leaf)
+        assert torch.equal(first, plain)
+    with pytest.raises(RuntimeError, match="second"):
+        penalty.backward()

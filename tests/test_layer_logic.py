@@ -433,3 +433,22 @@ def test_a_step_of_a_parameter_that_its_layer_no_longer_has_is_refused(name):
     with pytest.raises(nv.NVFP4Error, match=f"{name}.*moved"):
         opt.step()
     assert opt.steps == 1
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(bias=True, activation="relu2")], ids=["plain", "act"])
+def test_a_gradient_is_not_differentiated_again(kw):
+    """A penalty on the input's gradient raises, also beside a loss whose own gradient exists; a gradient that is only kept as a graph
+    does not, and the residual's, which is the output's, keeps its graph."""
+    layer = _layer(32, 48, 1, **kw)
+    x, scale = _x(16, 32).requires_grad_(), torch.ones((), requires_grad=True)
+    y = layer(x).float() * scale
+    first, = torch.autograd.grad(y.sum(), x, create_graph=True)
+    layer.zero_grad()
+    plain, = torch.autograd.grad((layer(x).float() * scale).sum(), x)
+    assert torch.equal(first, plain)
+    with pytest.raises(nv.NVFP4Error, match="second"):
+        (y.sum() + first.float().square().sum()).backward()
+    r = _x(16, 48, 1).requires_grad_()
+    dr, = torch.autograd.grad((layer(x, residual=r).float() * scale).square().sum(), r, create_graph=True)
+    again, = torch.autograd.grad(dr.float().sum(), scale, retain_graph=True, allow_unused=True)
+    assert again is not None
