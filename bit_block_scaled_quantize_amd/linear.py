@@ -37,7 +37,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (ACTIVATIONS, FP8Tensor, NVFP4Error, act_grad, amax, amax_pair, fp8_quantize, gemm_act, gemm_ex, quantize,
+from . import (ACTIVATIONS, FP8Tensor, NVFP4Error, _check_q, act_grad, amax, amax_pair, fp8_quantize, gemm_act, gemm_ex, quantize,
                rht_quantize)
 from .first_order import first_order
 
@@ -54,8 +54,9 @@ def _save(ctx, layer, t, z, x_fp8):
         ctx.save_for_backward(t, z)
         return
     q = fp8_quantize(t) if x_fp8 is None else x_fp8
-    qz = None if z is None else fp8_quantize(z)
-    ctx.save_for_backward(q.codes, q.scales, *(() if qz is None else (qz.codes, qz.scales)))
+    kept = [q] if z is None else [q, fp8_quantize(z)]
+    ctx.eight_shapes = [(e.rows, e.cols) for e in kept]
+    ctx.save_for_backward(*(t for e in kept for t in (e.codes, e.scales)))
 
 
 def _saved(ctx):
@@ -63,7 +64,7 @@ def _saved(ctx):
     if not ctx.eight:
         return ctx.saved_tensors
     pairs = ctx.saved_tensors
-    eight = [FP8Tensor(pairs[i], pairs[i + 1], *pairs[i].shape) for i in range(0, len(pairs), 2)]
+    eight = [FP8Tensor(pairs[2 * i], pairs[2 * i + 1], *shape) for i, shape in enumerate(ctx.eight_shapes)]
     return eight[0], eight[1] if len(eight) > 1 else None
 
 
@@ -73,6 +74,9 @@ def _check_fp8(x_fp8, t, layer):
             raise NVFP4Error('x_fp8 is of use to a layer with checkpoint="fp8"')
         if (x_fp8.rows, x_fp8.cols) != tuple(t.shape):
             raise NVFP4Error(f"x_fp8 shape ({x_fp8.rows}, {x_fp8.cols}) is not x's, {tuple(t.shape)}")
+        _check_q(x_fp8, what="x_fp8")
+        if not x_fp8.codes.device == x_fp8.scales.device == t.device:
+            raise NVFP4Error(f"x_fp8 is not on x's device, {t.device}")
 
 
 def _rows_of(t):

@@ -1,5 +1,5 @@
 """What the step's modules do with gradients at the edges of their use: types that differ between the two sides, second
-derivatives."""
+derivatives, 8-bit tensors of other shapes."""
 import pytest
 import torch
 
@@ -99,3 +99,30 @@ def test_second_derivatives_are_refused(name):
         assert torch.equal(first, plain)
     with pytest.raises(RuntimeError, match="second"):
         penalty.backward()
+
+
+def test_fp8_input_with_codes_of_another_shape():
+    """x_fp8 is what its rows and columns say, however the codes' tensor is shaped, as in the other calls that take one."""
+    x = _rand(1, 32, 64).bfloat16().requires_grad_()
+    dy = _rand(2, 32, 96).bfloat16()
+    q = nv.fp8_quantize(x.detach())
+    got = []
+    for codes, scales in ((q.codes, q.scales), (q.codes.reshape(-1), q.scales.reshape(-1)), (q.codes.view(2, 16, 64), q.scales.view(4, 16))):
+        layer = NVFP4Linear(64, 96, device="cuda", checkpoint="fp8")
+        layer.weight.data.copy_(_rand(3, 96, 64, std=0.1))
+        x.grad = None
+        layer(x, x_fp8=nv.FP8Tensor(codes, scales, 32, 64)).backward(dy)
+        got.append((x.grad.clone(), layer.main_grad.clone()))
+    for dx, dw in got[1:]:
+        assert torch.equal(dx, got[0][0]) and torch.equal(dw, got[0][1])
+
+
+def test_fp8_input_is_checked_before_the_forward():
+    layer = NVFP4Linear(64, 96, device="cuda", checkpoint="fp8")
+    torch.nn.init.normal_(layer.weight, std=0.1)
+    x = _rand(1, 32, 64).bfloat16().requires_grad_()
+    q = nv.fp8_quantize(x.detach())
+    for codes, scales in ((q.codes[:16], q.scales), (q.codes, q.scales[:16]), (q.codes.int(), q.scales), (q.codes.cpu(), q.scales)):
+        with pytest.raises(nv.NVFP4Error, match="x_fp8"):
+            layer(x, x_fp8=nv.FP8Tensor(codes, scales, 32, 64))
+    assert layer._calls == 0
