@@ -48,24 +48,25 @@ def _state_of(weight):
 
 
 def _save(ctx, layer, t, z, x_fp8):
-    """Keeps the input t and the pre-activation z (or None) for the backward pass."""
+    """Keeps the input t, if the weight's gradient is wanted, and the pre-activation z (or None) for the backward pass."""
     ctx.eight = layer.checkpoint == "fp8"
+    ctx.tokens = t.shape[0]
+    if not ctx.needs_input_grad[1]:
+        t = None
     if not ctx.eight:
         ctx.save_for_backward(t, z)
         return
-    q = fp8_quantize(t) if x_fp8 is None else x_fp8
-    kept = [q] if z is None else [q, fp8_quantize(z)]
-    ctx.eight_shapes = [(e.rows, e.cols) for e in kept]
-    ctx.save_for_backward(*(t for e in kept for t in (e.codes, e.scales)))
+    kept = [None if t is None else fp8_quantize(t) if x_fp8 is None else x_fp8, None if z is None else fp8_quantize(z)]
+    ctx.eight_shapes = [None if e is None else (e.rows, e.cols) for e in kept]
+    ctx.save_for_backward(*(a for e in kept if e is not None for a in (e.codes, e.scales)))
 
 
 def _saved(ctx):
-    """The input and the pre-activation as _save kept them: tensors, or FP8Tensors."""
+    """The input and the pre-activation as _save kept them: tensors, or FP8Tensors, or None."""
     if not ctx.eight:
         return ctx.saved_tensors
-    pairs = ctx.saved_tensors
-    eight = [FP8Tensor(pairs[2 * i], pairs[2 * i + 1], *shape) for i, shape in enumerate(ctx.eight_shapes)]
-    return eight[0], eight[1] if len(eight) > 1 else None
+    buffers = iter(ctx.saved_tensors)
+    return [None if shape is None else FP8Tensor(next(buffers), next(buffers), *shape) for shape in ctx.eight_shapes]
 
 
 def _check_fp8(x_fp8, t, layer):
@@ -77,10 +78,6 @@ def _check_fp8(x_fp8, t, layer):
         _check_q(x_fp8, what="x_fp8")
         if not x_fp8.codes.device == x_fp8.scales.device == t.device:
             raise NVFP4Error(f"x_fp8 is not on x's device, {t.device}")
-
-
-def _rows_of(t):
-    return t.rows if isinstance(t, FP8Tensor) else t.shape[0]
 
 
 class _LinearFn(torch.autograd.Function):
@@ -120,7 +117,7 @@ class _LinearFn(torch.autograd.Function):
     @first_order
     def backward(ctx, dy):
         t, _ = _saved(ctx)
-        if _rows_of(t) == 0:
+        if ctx.tokens == 0:
             return dy.new_zeros(ctx.x_shape), _nothing(ctx, 1, ctx.layer.weight, ctx.layer.main_grad), None, None, None, None
         g = dy.reshape(-1, dy.shape[-1])
         if g.dtype not in (torch.bfloat16, torch.float32):
@@ -136,7 +133,7 @@ def _nothing(ctx, i, param, main_grad):
 
 def _gradient_gemms(ctx, t, g):
     """dX and dW (None when it went into main_grad, or the weight is frozen) of one call from its input
-    t and the gradient g of its product."""
+    t (for dW alone) and the gradient g of its product."""
     layer = ctx.layer
     pair = amax_pair(g, layer.sign_mask)                     # max|dY|, max|H dY| from one read
     qdy, _ = quantize(g, "1x16", "sr", seed=layer.seed, offset=2 * ctx.call, amax=pair[0:1])
@@ -207,7 +204,7 @@ class _LinearActFn(torch.autograd.Function):
         layer = ctx.layer
         t, z = _saved(ctx)
         dr = dy if ctx.needs_input_grad[3] else None
-        if _rows_of(t) == 0:
+        if ctx.tokens == 0:
             return (dy.new_zeros(ctx.x_shape), _nothing(ctx, 1, layer.weight, layer.main_grad),
                     _nothing(ctx, 2, layer.bias, layer.bias_main_grad), dr, None, None, None, None)
         g = dy.reshape(-1, dy.shape[-1])

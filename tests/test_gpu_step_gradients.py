@@ -126,3 +126,21 @@ def test_fp8_input_is_checked_before_the_forward():
         with pytest.raises(nv.NVFP4Error, match="x_fp8"):
             layer(x, x_fp8=nv.FP8Tensor(codes, scales, 32, 64))
     assert layer._calls == 0
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(bias=True, activation="gelu")], ids=["plain", "act"])
+def test_frozen_layer_with_8_bit_checkpoints(kw):
+    """The input's gradient is the trained layer's, also from no tokens; x_fp8 is not needed and does no harm."""
+    x, dy = _rand(1, 32, 64).bfloat16().requires_grad_(), _rand(2, 32, 96).bfloat16()
+    layer = NVFP4Linear(64, 96, device="cuda", checkpoint="fp8", **kw)
+    layer.weight.data.copy_(_rand(3, 96, 64, std=0.1))
+    got = []
+    for frozen, q in ((False, None), (True, None), (True, nv.fp8_quantize(x.detach()))):
+        layer.weight.requires_grad_(not frozen)
+        layer._calls, x.grad = 0, None
+        layer(x, x_fp8=q).backward(dy)
+        got.append(x.grad.clone())
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+    x.grad = None
+    layer(x[:0]).sum().backward()
+    assert not x.grad.any()

@@ -452,3 +452,32 @@ def test_a_gradient_is_not_differentiated_again(kw):
     dr, = torch.autograd.grad((layer(x, residual=r).float() * scale).square().sum(), r, create_graph=True)
     again, = torch.autograd.grad(dr.float().sum(), scale, retain_graph=True, allow_unused=True)
     assert again is not None
+
+
+@pytest.mark.parametrize("checkpoint", ["bf16", "fp8"])
+@pytest.mark.parametrize("kw", [dict(), dict(bias=True, activation="relu2")], ids=["plain", "act"])
+def test_what_a_layer_keeps_for_its_backward(monkeypatch, library, kw, checkpoint):
+    """The input only where the weight's gradient is wanted, the pre-activation where there is an activation: a frozen layer neither
+    quantizes nor holds its input. The gradients are the same."""
+    def fp8_quantize(x):
+        library.append(("fp8_quantize", tuple(x.shape)))
+        return nv.FP8Tensor(x.detach().clone(), torch.empty(0), *x.shape)
+    plain_rht, plain_act = linear.rht_quantize, linear.act_grad
+    monkeypatch.setattr(linear, "fp8_quantize", fp8_quantize)
+    monkeypatch.setattr(linear, "rht_quantize", lambda x, *a, **k: plain_rht(x.codes if isinstance(x, nv.FP8Tensor) else x, *a, **k))
+    monkeypatch.setattr(linear, "act_grad", lambda dy, z=None, **k: plain_act(dy, z.codes if isinstance(z, nv.FP8Tensor) else z, **k))
+    x = _x(32, 48).requires_grad_()
+    layer = _layer(48, 64, 1, checkpoint=checkpoint, **kw)
+    got = {}
+    for frozen in (False, True):
+        layer.weight.requires_grad_(not frozen)
+        library.clear()
+        x.grad = None
+        y = layer(x)
+        kept = [t for t in y.grad_fn.saved_tensors if t is not None and t.numel()]
+        shapes = ([] if frozen else [(32, 48)]) + ([(32, 64)] if "activation" in kw else [])
+        assert [tuple(t.shape) for t in kept] == shapes
+        assert [s for name, s in library if name == "fp8_quantize"] == (shapes if checkpoint == "fp8" else [])
+        y.float().square().sum().backward()
+        got[frozen] = x.grad.clone()
+    assert torch.equal(got[True], got[False])
