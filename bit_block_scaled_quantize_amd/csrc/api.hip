@@ -840,6 +840,14 @@ static int check_norm(int64_t rows, int64_t cols, const void* weight, nvfp4_dtyp
   return check_matrix(weight, weight_dt, rows, cols, cols, "weight");
 }
 
+// An output in the place of an input, row by row: a row is read before it is written, but by nobody else's rows' writes.
+static int check_in_place(const void* out, nvfp4_dtype out_dt, int64_t ldo, const void* in, nvfp4_dtype in_dt, int64_t ldi, int64_t rows,
+                          const char* names) {
+  auto pitch = [](nvfp4_dtype dt, int64_t ld) { return ld * (dt == NVFP4_IN_FP32 ? 4 : 2); };
+  if (out == nullptr || out != in || rows < 2 || pitch(out_dt, ldo) == pitch(in_dt, ldi)) return NVFP4_OK;
+  return fail(NVFP4_ERR_INVALID, "%s begin at the same address with unequal row strides", names);
+}
+
 int nvfp4_rms_norm(const void* x, nvfp4_dtype dt, int64_t rows, int64_t cols, int64_t ldx, const void* weight, nvfp4_dtype weight_dt,
                    float eps, const void* residual, int64_t ldr, void* residual_out, int64_t ldro, uint16_t* y, int64_t ldy,
                    nvfp4_fp8_tensor* y8, float* amax_out, void* hip_stream) {
@@ -850,6 +858,11 @@ int nvfp4_rms_norm(const void* x, nvfp4_dtype dt, int64_t rows, int64_t cols, in
   if (residual_out && !residual) return fail(NVFP4_ERR_INVALID, "residual_out without a residual");
   if (residual_out && (st = check_matrix(residual_out, dt, rows, cols, ldro, "residual_out"))) return st;
   if (y && (st = check_matrix(y, NVFP4_IN_BF16, rows, cols, ldy, "y"))) return st;
+  if (y && y == residual_out && rows > 0) return fail(NVFP4_ERR_INVALID, "y and residual_out are one buffer");
+  if ((st = check_in_place(residual_out, dt, ldro, x, dt, ldx, rows, "residual_out and x")) ||
+      (st = check_in_place(residual_out, dt, ldro, residual, dt, ldr, rows, "residual_out and residual")) ||
+      (st = check_in_place(y, NVFP4_IN_BF16, ldy, x, dt, ldx, rows, "y and x")) ||
+      (st = check_in_place(y, NVFP4_IN_BF16, ldy, residual, dt, ldr, rows, "y and residual"))) return st;
   if (y8) {
     if ((st = check_fp8(y8, "y8"))) return st;
     if (y8->rows != rows || y8->cols != cols)
@@ -881,6 +894,9 @@ int nvfp4_rms_norm_grad(const void* dy, nvfp4_dtype dy_dt, int64_t rows, int64_t
   if ((st = check_norm(rows, cols, weight, weight_dt, eps)) || (st = check_matrix(dy, dy_dt, rows, cols, lddy, "dy")) ||
       (st = check_matrix(h, dt, rows, cols, ldh, "h")) || (st = check_matrix(dx, dt, rows, cols, lddx, "dx"))) return st;
   if (dresidual && (st = check_matrix(dresidual, dt, rows, cols, lddr, "dresidual"))) return st;
+  if ((st = check_in_place(dx, dt, lddx, dresidual, dt, lddr, rows, "dx and dresidual")) ||
+      (st = check_in_place(dx, dt, lddx, dy, dy_dt, lddy, rows, "dx and dy")) ||
+      (st = check_in_place(dx, dt, lddx, h, dt, ldh, rows, "dx and h"))) return st;
   if (!aligned(dweight, 4)) return fail(NVFP4_ERR_INVALID, "dweight is not aligned to its element size");
   const size_t need = dweight ? nvfp4_workspace_size(NVFP4_OP_NORM_GRAD, rows, cols, 1) : 0;
   if (need && (!workspace || ws_bytes < need || !aligned(workspace, kWsAlign)))

@@ -112,3 +112,19 @@ def test_head_grad_with_the_loss(lib):
         return lib.nvfp4_linear_cross_entropy_grad_ex(P, 8, 64, P, 100, 64, 64, P, lse, loss, P, dx, 64, P, 2, 64, ws, n, None)
     assert g(loss=P + 2) == g(lse=None) == g(dx=P + 1) == INVALID
     assert g() == g(loss=None) == g(ws=P, n=100) == WORKSPACE
+
+
+def test_norm_in_place(lib):
+    """An output may be an input only row for row: the same address with unequal strides would overwrite rows that are still to be read."""
+    Q, S = 0x20000, 0x30000
+
+    def f(x=P, ldx=64, r=Q, ldr=64, ro=None, ldro=64, y=S, ldy=64, dt=0, rows=4):
+        return lib.nvfp4_rms_norm(x, dt, rows, 64, ldx, S, 1, 1e-6, r, ldr, ro, ldro, y, ldy, None, None, None)
+    assert f(ro=P, ldro=72) == f(ro=Q, ldro=72) == f(ro=P, ldx=72) == f(ro=Q, ldr=72, dt=1) == INVALID
+    assert b"unequal row strides" in lib.nvfp4_last_error()
+    assert f(ro=S, y=S) == f(y=P, ldy=72) == f(y=Q, dt=1) == INVALID
+
+    def g(dy=P, lddy=64, h=Q, ldh=64, dr=None, lddr=64, dx=S, lddx=64, dydt=0):
+        return lib.nvfp4_rms_norm_grad(dy, dydt, 4, 64, lddy, h, 0, ldh, S, 1, 1e-6, dr, lddr, dx, lddx, None, 0, None, 0, None)
+    assert g(dr=S, lddr=72) == g(dx=P, lddx=72) == g(dx=P, dydt=1) == g(dx=Q, ldh=72) == INVALID
+    assert b"unequal row strides" in lib.nvfp4_last_error()
