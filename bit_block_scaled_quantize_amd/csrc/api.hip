@@ -836,7 +836,9 @@ int nvfp4_act_grad_fp8(const void* dy, nvfp4_dtype dt, int64_t ldy, const nvfp4_
 static int check_norm(int64_t rows, int64_t cols, const void* weight, nvfp4_dtype weight_dt, float eps) {
   if (rows < 0 || cols < 1) return fail(NVFP4_ERR_INVALID, "bad shape [%lld, %lld]", (long long)rows, (long long)cols);
   if (cols > nvfp4::kNormMaxCols) return fail(NVFP4_ERR_UNSUPPORTED, "cols (%lld) above %lld", (long long)cols, (long long)nvfp4::kNormMaxCols);
-  if (!(eps > 0) || !std::isfinite(eps)) return fail(NVFP4_ERR_INVALID, "eps (%g) must be positive and finite", (double)eps);
+  // (the root's instruction takes a subnormal for zero: a row of zeros would become NaNs)
+  if (!(eps >= 0x1p-126f) || !std::isfinite(eps))
+    return fail(NVFP4_ERR_INVALID, "eps (%g) must be positive, finite and no subnormal number", (double)eps);
   return check_matrix(weight, weight_dt, rows, cols, cols, "weight");
 }
 

@@ -613,7 +613,7 @@ int nvfp4_act_grad_fp8(const void* dy, nvfp4_dtype dt, int64_t ldy, const nvfp4_
  *   y          NULL, or device BF16, row stride ldy >= cols.   y8: NULL, or an 8-bit tensor [rows, cols].
  *   amax_out   NULL, or device float[1] receiving max|y| over the BF16 values: the amax_in of y's quantization.
  * Other outputs overlap no input; buffers that begin at the same address with unequal row strides are refused.
- * cols 1 .. 16384 (NVFP4_ERR_UNSUPPORTED above), eps > 0. Values whose squares leave FP32 are outside the contract.
+ * cols 1 .. 16384 (NVFP4_ERR_UNSUPPORTED above), eps at least 2^-126. Values whose squares leave FP32 are outside the contract.
  * Errors: NVFP4_ERR_INVALID (null or misaligned pointers, shapes, strides, enums, neither y nor y8), NVFP4_ERR_HIP.
  */
 int nvfp4_rms_norm(const void* x, nvfp4_dtype dt, int64_t rows, int64_t cols, int64_t ldx, const void* weight, nvfp4_dtype weight_dt,

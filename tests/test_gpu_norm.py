@@ -164,3 +164,21 @@ def test_refusals():
         nv.rms_norm_grad(x, x, w, dresidual=x.float())
     with pytest.raises(bad, match="dweight"):
         nv.rms_norm_grad(x, x, w, dweight=torch.ones(64, dtype=torch.bfloat16, device="cuda"))
+
+
+@pytest.mark.parametrize("eps", [1e-30, 1.2e-38])
+def test_norm_of_zeros_with_a_tiny_eps(eps):
+    x, w = torch.zeros(3, 96, device="cuda"), torch.ones(96, device="cuda")
+    assert not nv.rms_norm(x, w, eps=eps).any()
+    dx = nv.rms_norm_grad(x.bfloat16(), x, w, eps=eps)
+    assert not dx.any()
+
+
+def test_a_subnormal_eps_is_refused():
+    """Its inverse root would come out infinite, and a row of zeros NaN."""
+    x, w = torch.zeros(3, 96, device="cuda"), torch.ones(96, device="cuda")
+    for eps in (1.17e-38, 1e-40):
+        with pytest.raises(nv.NVFP4Error, match="eps"):
+            nv.rms_norm(x, w, eps=eps)
+        with pytest.raises(nv.NVFP4Error, match="eps"):
+            nv.rms_norm_grad(x, x, w, eps=eps)
