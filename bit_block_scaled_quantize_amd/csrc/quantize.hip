@@ -498,7 +498,7 @@ __global__ __launch_bounds__(kThreads) void k_encode_1x16(
       if (r < seg_lo || r >= seg_hi) {                       // uniform: another segment
         const int64_t sg = find_segment(off, nseg, r);
         seg_lo = off[sg];
-        seg_hi = off[sg + 1];
+        seg_hi = sg + 1 < nseg ? off[sg + 1] : INT64_MAX;    // the last one's table also for the rows behind it
         s_enc = tensor_encode_scale(amax[sg]);
         __builtin_amdgcn_wave_barrier();                     // the wave's reads of the old table
         tab[lane] = block_recip(lane, s_enc);

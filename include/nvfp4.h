@@ -112,9 +112,11 @@ typedef struct nvfp4_fp8_tensor {
  *             (lo32 seed, hi32 seed) and counter (lo32 b, hi32 b, lo32 offset, hi32 offset);
  *             it rounds up iff frac + byte/256 >= 1.
  *   segments  NULL (nseg must be 1) or device int64[nseg+1] row offsets with
- *             segments[0] = 0 <= ... <= segments[nseg] = rows (non-decreasing; multiples
+ *             segments[0] = 0 <= ... <= segments[nseg] <= rows (non-decreasing; multiples
  *             of 16 for 16X16). Each segment gets its own amax and global scale (expert
- *             stacks of a mixture-of-experts layer).
+ *             stacks of a mixture-of-experts layer). Rows from segments[nseg] on (nvfp4_moe_sort
+ *             can leave some, which nvfp4_moe_gather fills with zeros) count as the last segment's,
+ *             in its amax too.
  *   amax_in   NULL, or device float[nseg] holding max|x| per segment; then the amax pass is
  *             skipped and no workspace is needed.
  *   out       codes/scales/global_scale as documented above; out->rows == rows,
@@ -175,7 +177,8 @@ int nvfp4_quantize_noalloc(const void* x, nvfp4_dtype dt, int64_t rows, int64_t 
  *              1x16 blocks along tokens (out->rows == cols, out->cols == tokens).
  *   rnd/seed/offset as for nvfp4_quantize (SR block index is over the output [cols, tokens]).
  *   segments   NULL (nseg must be 1) or device int64[nseg+1] TOKEN offsets, multiples of 16,
- *              non-decreasing from 0 to tokens: the tokens routed to each expert of a
+ *              non-decreasing from 0 to at most tokens (those behind count as the last
+ *              segment's, as in nvfp4_quantize): the tokens routed to each expert of a
  *              mixture-of-experts layer, whose weight gradients are separate GEMMs over their
  *              own tokens (nvfp4_grouped_gemm_k). Each token range gets its own amax (over its
  *              transformed values) and global scale: out->global_scale[nseg]; out's column

@@ -1,5 +1,5 @@
 """What the step's modules do with gradients at the edges of their use: types that differ between the two sides, second
-derivatives, 8-bit tensors of other shapes."""
+derivatives, 8-bit tensors of other shapes, tables that end below the rows."""
 import pytest
 import torch
 
@@ -144,3 +144,46 @@ def test_frozen_layer_with_8_bit_checkpoints(kw):
     x.grad = None
     layer(x[:0]).sum().backward()
     assert not x.grad.any()
+
+
+def test_weight_gradients_by_expert_with_rows_behind_the_last():
+    """rht_quantize with the sort's offsets as segments and grouped_gemm_k over them, the offsets ending below the rows: each expert's
+    gradient is that of its own rows."""
+    t, k, e, h, n = 200, 2, 5, 128, 96
+    rng = torch.Generator().manual_seed(7)
+    ids = torch.randint(-1, e - 1, (t, k), generator=rng, dtype=torch.int32).cuda()     # the last expert gets none
+    s = nv.moe_sort(ids, e)
+    off = s.offsets.tolist()
+    assert off[-1] < s.rows and off[-1] == off[-2]
+    x, dy = nv.moe_gather(_rand(1, t, h).bfloat16(), s), nv.moe_gather(_rand(2, t, n).bfloat16(), s)
+    a, b = (nv.rht_quantize(m, 0x1234, segments=s.offsets) for m in (dy, x))
+    d = nv.grouped_gemm_k(s.offsets, a, b)
+    for g in range(e):
+        lo, hi = off[g], off[g + 1]
+        got = d[g * n:(g + 1) * n]
+        if lo == hi:
+            assert not got.any()
+            continue
+        one, two = (nv.rht_quantize(m[lo:hi].contiguous(), 0x1234) for m in (dy, x))
+        assert torch.equal(one.global_scale, a.global_scale[g:g + 1]) and torch.equal(two.global_scale, b.global_scale[g:g + 1])
+        assert torch.equal(one.codes, a.codes[:, lo // 2:hi // 2]) and torch.equal(two.scales, b.scales[:, lo // 16:hi // 16])
+        ref = nv.dequantize(one).double() @ nv.dequantize(two).double().t()
+        size = nv.dequantize(one).double().abs() @ nv.dequantize(two).double().abs().t()
+        assert bool(((got.double() - ref).abs() <= 1e-5 * size).all())
+
+
+@pytest.mark.parametrize("block", ["1x16", "16x16"])
+@pytest.mark.parametrize("last", [0, 64])
+def test_rows_behind_the_last_segment_count_as_its(block, last):
+    """A table that ends below the rows gives what the same table gives with the rows as its end, in quantize, rht_quantize and amax."""
+    rows, cols = 320, 96
+    x = _rand(1, rows, cols).bfloat16()
+    x[200:] *= 3
+    short = torch.tensor([0, 64, 128, 128 + last], device="cuda")
+    whole = torch.tensor([0, 64, 128, rows], device="cuda")
+    for call in (lambda s: nv.quantize(x, block, segments=s)[0], lambda s: nv.rht_quantize(x, 0x77, segments=s)):
+        a, b = call(short), call(whole)
+        for one, two in ((a.codes, b.codes), (a.scales, b.scales), (a.global_scale, b.global_scale)):
+            assert torch.equal(one, two)
+    for rht in (False, True):
+        assert torch.equal(nv.amax(x, segments=short, rht=rht), nv.amax(x, segments=whole, rht=rht))
