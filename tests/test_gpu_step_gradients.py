@@ -1,5 +1,6 @@
 """What the step's modules do with gradients at the edges of their use: types that differ between the two sides, second
-derivatives, 8-bit tensors of other shapes, tables that end below the rows."""
+derivatives, 8-bit tensors of other shapes, tables that end below the rows, a captured
+step of the head."""
 import pytest
 import torch
 
@@ -187,3 +188,42 @@ def test_rows_behind_the_last_segment_count_as_its(block, last):
             assert torch.equal(one, two)
     for rht in (False, True):
         assert torch.equal(nv.amax(x, segments=short, rht=rht), nv.amax(x, segments=whole, rht=rht))
+
+
+@pytest.mark.parametrize("reduction", ["mean", "sum"])
+@pytest.mark.parametrize("t", [300, 40000])
+def test_captured_step_of_the_head(reduction, t):
+    """Forward and backward of the module in one graph, replayed several times with other work between; each is the eager result."""
+    h, v = 32, 130
+    head = LinearCrossEntropy(h, v, device="cuda", reduction=reduction)
+    head.weight.data.copy_(_rand(1, v, h, std=0.2))
+    x = _rand(2, t, h).bfloat16().requires_grad_()
+    tg = torch.randint(0, v, (t,), device="cuda")
+
+    def step():
+        head.main_grad.zero_()
+        loss = head(x, tg)
+        dx, = torch.autograd.grad(loss, x)
+        return loss.detach(), dx, head.main_grad             # nothing holds the autograd graph
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for turn in range(5):
+        with torch.no_grad():
+            x.copy_(_rand(10 + turn, t, h))
+            tg.copy_(torch.randint(-20, v, (t,), device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.detach().clone() for o in out]
+        want = [o.detach().clone() for o in step()]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), turn
+        torch.empty(1 << 20, device="cuda").fill_(float(turn)).sum()
