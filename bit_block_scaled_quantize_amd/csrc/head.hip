@@ -9,11 +9,14 @@
 // token whose target lies in it. k_merge joins the tiles' pairs: with d = log(sum over the other words of exp(l - l[target])) the loss is
 // log(1 + exp(d)), which keeps the digits of a small loss (as lse - l[target], two numbers rounded at their size, a loss of 1e-6 at
 // logits of 25 was all rounding). Backward: the logits are computed again, a piece of
-// the vocabulary at a time, and leave the product as G in BF16 (8 bits of G's own size: as much as the BF16
-// gradients that follow keep). The target's G comes from the loss, since 1 - exp(l - lse) of a confident token is made of lse's rounding (logits
-// of 25: three times its value off). Mostly a token's largest by far, it keeps what BF16 leaves of it in FP32: dx gets
-// it when its shares are joined, dW from the tile that holds the word. dW's rows of the piece are G^T x, and dx grows by G W in FP32, rounded once
-// after the last piece. Four products in all, 2 T H V operations each: bound by the matrix cores.
+// the vocabulary at a time, and leave the product as G in BF16: 8 bits of each entry's own size, what a BF16 dx or dW keeps of its sums, and
+// what x and W, its partners in both products, keep of the numbers that they stand for. An FP32 dW is the FP32 sum of these
+// (1024 tokens, 8000 words, hidden 512: off by 5.7e-5 of its norm, in the words that are no token's target by 1.4e-3; a BF16 dW by
+// 1.7e-3); the other half of each G would be a fifth product, a third of the backward's time. The target's G comes from the loss, since 1 - exp(l - lse)
+// of a confident token is made of lse's rounding (logits of 25: three times its value off). Mostly a token's largest by far, it keeps
+// what BF16 leaves of it in FP32: dx gets it when its shares are joined, dW, in BF16 once more (2^-17 of G), from the tile that holds the
+// word. dW's rows of the piece are G^T x, and dx grows by G W in FP32, rounded once after the last piece. Four products in all, 2 T H V
+// operations each: bound by the matrix cores.
 //
 // One kernel does all of them: D[n, m] = sum over k of A[m, k] B[n, k]. A workgroup of 4 waves owns a tile, a wave TM x TN
 // tiles of v_mfma_f32_16x16x32_bf16 (of the two shapes the one that moves fewer accumulators per operation: the chip is at
@@ -28,8 +31,8 @@
 // larger shape, one every four products 2220): several fill the address unit's queue, and the wave waits.
 // FP32 gradients that are added to are on their way two columns before their addition (50021 words, hidden 1040, 333 tokens:
 // dW 212 us without, 143 with).
-// Measured: 8192 tokens, 131072 words, hidden 5120: forward 7.7 ms (1.43 PFLOP/s), backward 25 (1.32). 1003 tokens, 32003 words,
-// hidden 2704: forward 180 us (0.97). 333 tokens, 50021 words, hidden 1040: forward 75, G 68, dx 73, dW 72 us; rows of 2080
+// Measured: 8192 tokens, 131072 words, hidden 5120: forward 7.8 ms (1.42 PFLOP/s), backward 25 (1.30). 1003 tokens, 32003 words,
+// hidden 2704: forward 175 to 180 us (0.97). 333 tokens, 50021 words, hidden 1040: forward 76, G 69, dx 73, dW 72 us; rows of 2080
 // bytes begin inside a line of 128, so each piece of a stage is parts of two (hidden 1024: 66 and 59 us), and a round of tiles has
 // 17 steps of a us, or 6 for dW, between its first loads and its last stores.
 #include <type_traits>
@@ -290,6 +293,8 @@ __device__ __forceinline__ void multiply(Rows A, Rows B, int64_t m0, int64_t n0,
 
 // acc += rest[t] x[t] over the tokens whose target is one of the tile's words (dW's products: B's rows are words), [from, to) in the order
 // of words: 32 at a time one more half step, whose B holds rest (in BF16: 2^-17 of G) at each token's word and zeros.
+// Words that many tokens end in make their tiles longer. G and dW of 8192 tokens, 131072 words, hidden 5120: 17.0 ms with targets drawn
+// uniformly, 17.1 with the v-th word's share proportional to 1 / v, 17.0 with one word for all; 8192, 32768 and 1024: 1.12 ms, 1.24, 1.52.
 template <class C>
 __device__ __forceinline__ void add_rest(const Rows& A, int64_t m0, int64_t n0, int from, int to, const Out& o,
                                          f32x4 (&acc)[C::kTilesM][C::kTilesN]) {
@@ -578,7 +583,8 @@ __global__ __launch_bounds__(kThreads) void k_join_shares(const float* __restric
 
 // by_word = the counted tokens in the order of (target, token), behind them the others; start[b] = the number of counted tokens with a
 // target below 128 b, b = 0 .. buckets. A lane a token (a bound), its place the number of those before it; the workgroup's waves look
-// through a share of the tokens each (8192 tokens, 32768 words: 31 us; 333 and 50021: 6).
+// through a share of the tokens each. Every token looks at every other: with 32768 words 6 us for 333 tokens, 30 for 8192, 0.33 ms
+// for 32768, 3.9 ms for 131072 (with hidden 1024 one in seven of what the products take there), some 1 s at the limit of 2^21.
 constexpr int kOrderWaves = 16;
 __global__ __launch_bounds__(kOrderWaves * 64) void k_order(const int64_t* __restrict__ targets, int64_t tokens, int64_t vocab, int64_t buckets,
                                                             int* __restrict__ by_word, int* __restrict__ start) {
@@ -660,7 +666,7 @@ constexpr int64_t kPad = 64;
 int64_t odd_lines(int64_t v) { return ((v + kPad - 1) / kPad | 1) * kPad; }
 
 // Rows that begin inside a line of 128 bytes cost the DMA two lines for a piece. Where hidden makes x's rows so, large products read a
-// copy of x in whole lines (W would be too much to copy): from 2^36 products on (8192 x 32768 x 5136: forward 2116 us
+// copy of x in whole lines (W would be too much to copy; where only x's stride makes them so, it stays): from 2^36 products on (8192 x 32768 x 5136: forward 2116 us
 // against 2341, backward 6841 against 7114; 1003 x 32003 x 2704, at the limit: 185 and 191; 333 x 50021 x 1040, a quarter of
 // it: 4 us less in whole lines, and the copy takes 5).
 __global__ __launch_bounds__(kThreads) void k_realign(const uint16_t* __restrict__ x, int64_t ldx, int64_t tokens, int64_t hidden,

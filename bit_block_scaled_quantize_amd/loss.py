@@ -38,6 +38,7 @@ class LinearCrossEntropy(torch.nn.Module):
     count. reduction: "mean" over the targets that count (0 if none does), "sum", or "none" (float32, the targets' shape).
     main_grad: with ``fp32_main_grad`` (default) the weight gradient is accumulated into the FP32 tensor
     ``self.main_grad``, as NVFP4Linear's, and ``weight.grad`` stays None; otherwise ``weight.grad`` receives it in BF16.
+    (Either way its addends are of softmax gradients held in BF16, the targets' in twice as many bits.)
     """
 
     bias = bias_main_grad = None                             # as NVFP4Linear without a bias

@@ -714,12 +714,12 @@ int nvfp4_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t ldx, c
  * nvfp4_linear_cross_entropy_grad - its backward (the same passage). The logits are computed again, in pieces of the
  * vocabulary:
  *   G[t, v] = grad[t] exp(l[t, v] - lse[t]), the target's grad[t] (exp(l - lse) - 1), held in BF16 (the target's, mostly the
- *   largest, with what that leaves of it), 0 for a token that does not count
+ *   largest, with what that leaves of it), 0 for a token that does not count (whose x has to be finite all the same: 0 x is in dw's sums)
  *   dx = BF16(G w);   dw = G^T x
  *   lse        the forward's.   grad: device float [tokens], the gradient of each token's loss.
  *   dx         NULL, or device BF16 [tokens, hidden], row stride lddx >= hidden.
  *   dw         NULL, or device [vocab, hidden], row stride lddw >= hidden: FP32, FP32 added to what it holds, or BF16
- *              (dw_kind). dx and dw overlap no input.
+ *              (dw_kind), each the FP32 sum of addends that carry G's rounding (2^-8 of each). dx and dw overlap no input.
  *   workspace  nvfp4_workspace_size(NVFP4_OP_HEAD_GRAD, tokens, vocab, hidden) bytes, 256-byte aligned.
  * The result is deterministic. lse is rounded at its size, so the target's G is off by up to 2^-24 |lse| grad: much of it
  * for a token that is nearly sure of its target; nvfp4_linear_cross_entropy_grad_ex takes the loss too. Errors: as nvfp4_linear_cross_entropy.
