@@ -13,11 +13,11 @@ from .first_order import first_order
 
 class _HeadFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, targets, layer):
+    def forward(ctx, x, weight, targets, layer, train):
         t = x.reshape(-1, x.shape[-1]).contiguous()
         loss, lse = linear_cross_entropy(t, weight, targets)
-        # a copy: the caller may change the loss that it gets
-        ctx.save_for_backward(t, weight, targets, lse, loss.clone() if any(ctx.needs_input_grad) else loss)
+        if train:                                            # a copy: the caller may change the loss that it gets
+            ctx.save_for_backward(t, weight, targets, lse, loss.clone())
         ctx.layer, ctx.x_shape = layer, x.shape
         return loss
 
@@ -28,7 +28,7 @@ class _HeadFn(torch.autograd.Function):
         main = ctx.layer.main_grad
         dx, dw = linear_cross_entropy_grad(t, weight, targets, lse, grad.float().contiguous(), dweight=main, accumulate=main is not None,
                                            need_dx=ctx.needs_input_grad[0], need_dweight=ctx.needs_input_grad[1], loss=loss)
-        return None if dx is None else dx.view(ctx.x_shape), None if main is not None else dw, None, None
+        return None if dx is None else dx.view(ctx.x_shape), None if main is not None else dw, None, None, None
 
 
 class LinearCrossEntropy(torch.nn.Module):
@@ -57,7 +57,8 @@ class LinearCrossEntropy(torch.nn.Module):
         if targets.shape != x.shape[:-1]:
             raise NVFP4Error(f"targets shape {tuple(targets.shape)} is not x's, {tuple(x.shape[:-1])}")
         flat = targets.reshape(-1).contiguous()
-        loss = _HeadFn.apply(x, self.weight, flat, self)
+        train = torch.is_grad_enabled() and (x.requires_grad or self.weight.requires_grad)   # hidden from a Function's forward
+        loss = _HeadFn.apply(x, self.weight, flat, self, train)
         if self.reduction == "none":
             return loss.view(targets.shape)
         if self.reduction == "sum":

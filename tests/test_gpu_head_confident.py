@@ -194,3 +194,20 @@ def test_tokens_that_lean_to_their_targets():
     nv.linear_cross_entropy_grad(x, w, tg, lse, grad, dweight=d32, need_dx=False, loss=loss)
     own = G[at, tg]
     assert bool(((d32[tg, h + at].double() - own).abs() <= (rel + 2.0 ** -15) * own.abs()).all())
+
+
+def test_module_without_gradients(monkeypatch):
+    """Evaluation: the same losses, and no copy of them is kept for a backward pass."""
+    (x, w, tg, grad), _ = _case(40, 48, 1)
+    head = LinearCrossEntropy(48, 40, device="cuda", reduction="none")
+    head.weight.data.copy_(w)
+    want = head(x, tg).detach().clone()
+    copies, clone = [], torch.Tensor.clone
+    monkeypatch.setattr(torch.Tensor, "clone", lambda t, **kw: copies.append(t.shape) or clone(t, **kw))
+    with torch.no_grad():
+        got = head(x, tg)
+    assert torch.equal(got, want) and not copies
+    head(x, tg)
+    assert len(copies) == 1
+    head.weight.requires_grad_(False)
+    assert torch.equal(head(x, tg), want) and len(copies) == 1
